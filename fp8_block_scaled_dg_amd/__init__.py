@@ -10,6 +10,9 @@ Entry points (same names as the C ABI):
     dg_fp8_gemm_nt(c, a, b, sa, sb, a_block_rows, workspace=None)
     dg_fp8_grouped_gemm_contig(c, a, b, sa, sb, a_block_rows, m_indices, workspace=None)
     dg_fp8_grouped_gemm_masked(c, a, b, sa, sb, a_block_rows, masked_m, workspace=None)
+    dg_quantize_mxfp4(x, q, sf, qt, sft), dg_dequantize_mxfp4(out, q, sf)
+    dg_mxfp4_gemm_nt(c, a, b, sfa, sfb), dg_mxfp4_gemm_nt_bf16a(c, a, b, sfb)
+    dg_moe_layer(y, x, w13, w2, s13, s2, ids, weights, logits)
     (and the UE8M0, fused-A, epilogue, layout and K-grouped entry points)
 Conveniences mirroring the DeepGEMM page's Python API (pzsr.cn, s4.1):
     to_fp8(x, block_rows=128) -> (q, scales)
@@ -104,6 +107,24 @@ def _load():
                                                ctypes.c_size_t, vp]
     lib.dg_fp8_gemm_nt_noalloc.restype = i32
     lib.dg_fp8_gemm_nt_noalloc.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp]
+    sz = ctypes.c_size_t
+    lib.dg_quantize_mxfp4.restype = i32
+    lib.dg_quantize_mxfp4.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp]
+    lib.dg_dequantize_mxfp4.restype = i32
+    lib.dg_dequantize_mxfp4.argtypes = [vp, i32, vp, vp, i64, i64, vp]
+    lib.dg_mxfp4_gemm_nt_workspace_bytes.restype = sz
+    lib.dg_mxfp4_gemm_nt_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.dg_mxfp4_gemm_nt.restype = i32
+    lib.dg_mxfp4_gemm_nt.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
+    lib.dg_mxfp4_gemm_nt_bf16a_workspace_bytes.restype = sz
+    lib.dg_mxfp4_gemm_nt_bf16a_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.dg_mxfp4_gemm_nt_bf16a.restype = i32
+    lib.dg_mxfp4_gemm_nt_bf16a.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]
+    lib.dg_moe_layer_workspace_bytes.restype = sz
+    lib.dg_moe_layer_workspace_bytes.argtypes = [i32, i32, i32, i64, i64]
+    lib.dg_moe_layer.restype = i32
+    lib.dg_moe_layer.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i64,
+                                 i64, vp, sz, vp]
     if lib.dg_abi_version() != ABI_VERSION:
         raise ImportError("libdg ABI %d != binding ABI %d" % (lib.dg_abi_version(), ABI_VERSION))
     return lib
@@ -560,6 +581,149 @@ def dg_fp8_grouped_gemm_masked(c, a, b, sa, sb, a_block_rows: int, masked_m, wor
 
 
 # ---------------------------------------------------------------------------
+# MXFP4 and the mixture-of-experts layer
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def mxfp4_shapes(rows: int, cols: int):
+    """(shape of the codes, shape of the scale words) of rows x cols values."""
+    return (rows, cdiv(cols, 32) * 16), (cdiv(cols, 128), rows)
+
+
+def _mxfp4_pair(q, sf, rows, cols, what):
+    if (q is None) != (sf is None):
+        raise ValueError("%s needs codes and scales" % what)
+    if q is None:
+        return
+    _require(q, torch.uint8, what)
+    _require(sf, torch.int32, "scales of " + what)
+    if (tuple(q.shape), tuple(sf.shape)) != mxfp4_shapes(rows, cols):
+        raise ValueError("%s must be codes %s and scales %s" % ((what,) + mxfp4_shapes(rows, cols)))
+
+
+def dg_quantize_mxfp4(x, q=None, sf=None, qt=None, sft=None, stream=None) -> None:
+    """x float32 or bfloat16 [rows, cols], its rows contiguous (any row stride)
+    -> MXFP4 codes and scales along the rows (q, sf), along the columns (qt,
+    sft: those of x.t()), or both; shapes as mxfp4_shapes gives them."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
+        raise TypeError("x must be a float32 or bfloat16 tensor")
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1 or rows > 1 and x.stride(0) < cols:
+        raise ValueError("the rows of x must be contiguous and must not overlap")
+    _mxfp4_pair(q, sf, rows, cols, "q")
+    _mxfp4_pair(qt, sft, cols, rows, "qt")
+    _check(lib.dg_quantize_mxfp4(_ptr(q), _ptr(sf), _ptr(qt), _ptr(sft), _ptr(x),
+                                 _DTYPES[x.dtype], rows, cols, x.stride(0) if rows > 1 else cols,
+                                 _stream(stream)), "dg_quantize_mxfp4")
+
+
+def dg_dequantize_mxfp4(out, q, sf, stream=None) -> None:
+    """out [rows, cols] (float32 or bfloat16) = the values of codes q, sf."""
+    if not isinstance(out, torch.Tensor) or out.dtype not in _DTYPES:
+        raise TypeError("out must be a float32 or bfloat16 tensor")
+    _require(out, out.dtype, "out")
+    rows, cols = out.shape
+    _mxfp4_pair(q, sf, rows, cols, "q")
+    _check(lib.dg_dequantize_mxfp4(_ptr(out), _DTYPES[out.dtype], _ptr(q), _ptr(sf), rows, cols,
+                                   _stream(stream)), "dg_dequantize_mxfp4")
+
+
+def dg_mxfp4_gemm_nt_workspace_bytes(M: int, N: int, K: int) -> int:
+    return lib.dg_mxfp4_gemm_nt_workspace_bytes(M, N, K)
+
+
+def dg_mxfp4_gemm_nt(c, a, b, sfa, sfb, workspace=None, stream=None) -> None:
+    """C[M,N] (bf16) = A . B^T, both MXFP4 (codes [M, K/2] and [N, K/2])."""
+    c = _bf16(c, "c")
+    M, N = c.shape
+    K = 2 * a.shape[1]
+    if a.shape[0] != M or tuple(b.shape) != (N, K // 2):
+        raise ValueError("shape mismatch: a %s, b %s, c %s" % (tuple(a.shape), tuple(b.shape),
+                                                              tuple(c.shape)))
+    _mxfp4_pair(a, sfa, M, K, "a")
+    _mxfp4_pair(b, sfb, N, K, "b")
+    _check(lib.dg_mxfp4_gemm_nt(_ptr(c), _ptr(a), _ptr(b), _ptr(sfa), _ptr(sfb), M, N, K,
+                                _ptr(workspace), _workspace_bytes(workspace), _stream(stream)),
+           "dg_mxfp4_gemm_nt")
+
+
+MXFP4_BF16A_MAX_M = 64
+
+
+def dg_mxfp4_gemm_nt_bf16a_workspace_bytes(M: int, N: int, K: int) -> int:
+    return lib.dg_mxfp4_gemm_nt_bf16a_workspace_bytes(M, N, K)
+
+
+def dg_mxfp4_gemm_nt_bf16a(c, a, b, sfb, workspace=None, stream=None) -> None:
+    """C[M,N] (bf16) = A[M,K] (bf16, not quantised) . B[N,K]^T (MXFP4);
+    M <= MXFP4_BF16A_MAX_M."""
+    c = _bf16(c, "c")
+    a = _bf16(a, "a")
+    M, K = a.shape
+    N = b.shape[0]
+    if tuple(b.shape) != (N, K // 2) or c.shape != (M, N):
+        raise ValueError("shape mismatch: a %s, b %s, c %s" % (tuple(a.shape), tuple(b.shape),
+                                                              tuple(c.shape)))
+    _mxfp4_pair(b, sfb, N, K, "b")
+    _check(lib.dg_mxfp4_gemm_nt_bf16a(_ptr(c), _ptr(a), _ptr(b), _ptr(sfb), M, N, K,
+                                      _ptr(workspace), _workspace_bytes(workspace),
+                                      _stream(stream)), "dg_mxfp4_gemm_nt_bf16a")
+
+
+MOE_SCORINGS = {"softmax": 0, "sigmoid": 1}
+
+
+def dg_moe_layer_workspace_bytes(T: int, E: int, k: int, H: int, I: int) -> int:
+    return lib.dg_moe_layer_workspace_bytes(T, E, k, H, I)
+
+
+def dg_moe_layer(y, x, w13, w2, s13, s2, ids, weights, logits=None, scoring: str = "softmax",
+                 workspace=None, stream=None) -> None:
+    """y [T,H] (bf16) = the mixture-of-experts layer on x [T,H] (bf16), T <=
+    64.  w13 [E, 2I, H] (row 2i gate, 2i+1 up), w2 [E, H, I]: MXFP4 codes
+    (uint8, two a byte, int32 scales [E, ceil(H/128), 2I] and [E, ceil(I/128),
+    H]) or E4M3 (uint8 / float8_e4m3fn, float32 scales [E, H/128,
+    ceil(2I/128)] and [E, I/128, ceil(H/128)]); the scales' type tells which.
+    With logits float32 [T, E], ids int32 [T, k] and weights float32 [T, k]
+    are outputs (the top k and their normalised scores); without, inputs.
+    workspace: dg_moe_layer_workspace_bytes(T, E, k, H, I) bytes."""
+    y = _bf16(y, "y")
+    x = _bf16(x, "x")
+    w13 = _codes(w13, "w13")
+    w2 = _codes(w2, "w2")
+    if not isinstance(s13, torch.Tensor) or s13.dtype not in (torch.int32, torch.float32):
+        raise TypeError("s13 must be int32 (MXFP4) or float32 (E4M3)")
+    fp8 = s13.dtype == torch.float32
+    _require(s13, s13.dtype, "s13")
+    _require(s2, s13.dtype, "s2")
+    _require(ids, torch.int32, "ids")
+    _require(weights, torch.float32, "weights")
+    T, H = x.shape
+    E = w13.shape[0]
+    I = w13.shape[1] // 2
+    k = ids.shape[-1]
+    per = 1 if fp8 else 2
+    scales = (((E, cdiv(H, 128), cdiv(2 * I, 128)), (E, cdiv(I, 128), cdiv(H, 128))) if fp8 else
+              ((E, cdiv(H, 128), 2 * I), (E, cdiv(I, 128), H)))
+    if (y.shape != x.shape or tuple(w13.shape) != (E, 2 * I, H // per)
+            or tuple(w2.shape) != (E, H, I // per) or tuple(ids.shape) != (T, k)
+            or tuple(weights.shape) != (T, k) or (tuple(s13.shape), tuple(s2.shape)) != scales):
+        raise ValueError("inconsistent mixture-of-experts shapes")
+    if logits is not None:
+        _require(logits, torch.float32, "logits")
+        if tuple(logits.shape) != (T, E):
+            raise ValueError("logits must be [T, E]")
+    _check(lib.dg_moe_layer(_ptr(y), _ptr(x), _ptr(w13), _ptr(w2), _ptr(s13), _ptr(s2), int(fp8),
+                            _ptr(ids), _ptr(weights), _ptr(logits), MOE_SCORINGS[scoring], T, E, k,
+                            H, I, _ptr(workspace), _workspace_bytes(workspace), _stream(stream)),
+           "dg_moe_layer")
+
+
+# ---------------------------------------------------------------------------
 # Conveniences (allocate outputs with torch)
 # ---------------------------------------------------------------------------
 
@@ -595,6 +759,48 @@ def fp8_grouped_gemm_contig(c, a, b, sa, sb, m_indices, a_block_rows: int = 1):
     return c
 
 
+def to_mxfp4(x, transposed: bool = False):
+    """Quantise a float32 or bfloat16 device matrix to MXFP4 along its rows,
+    or (transposed) along its columns -> (codes, scales) of x, or of x.t()."""
+    rows, cols = x.shape
+    if transposed:
+        rows, cols = cols, rows
+    qs, ss = mxfp4_shapes(rows, cols)
+    q = torch.empty(qs, dtype=torch.uint8, device=x.device)
+    sf = torch.empty(ss, dtype=torch.int32, device=x.device)
+    if transposed:
+        dg_quantize_mxfp4(x, qt=q, sft=sf)
+    else:
+        dg_quantize_mxfp4(x, q, sf)
+    return q, sf
+
+
+def to_mxfp4_both(x):
+    """Both directions from one reading of x: (q, sf) of x, (qt, sft) of
+    x.t()."""
+    rows, cols = x.shape
+    out = []
+    for shape in (mxfp4_shapes(rows, cols), mxfp4_shapes(cols, rows)):
+        out.append(torch.empty(shape[0], dtype=torch.uint8, device=x.device))
+        out.append(torch.empty(shape[1], dtype=torch.int32, device=x.device))
+    dg_quantize_mxfp4(x, *out)
+    return tuple(out)
+
+
+def from_mxfp4(q, sf, cols: int, dtype=torch.bfloat16):
+    """The values [rows, cols] of MXFP4 codes q and scales sf."""
+    out = torch.empty((q.shape[0], cols), dtype=dtype, device=q.device)
+    dg_dequantize_mxfp4(out, q, sf)
+    return out
+
+
+def mxfp4_gemm_nt(a, b, sfa, sfb, workspace=None):
+    """A . B^T of two MXFP4 matrices -> bfloat16 [M, N]."""
+    c = torch.empty((a.shape[0], b.shape[0]), dtype=torch.bfloat16, device=a.device)
+    dg_mxfp4_gemm_nt(c, a, b, sfa, sfb, workspace)
+    return c
+
+
 __all__ = [
     "lib", "LIB_PATH", "DGError", "status_string", "get_mk_alignment_for_contiguous_layout",
     "dg_quantize_fp8_block", "dg_fp8_gemm_nt_workspace_bytes", "dg_fp8_gemm_nt",
@@ -605,6 +811,10 @@ __all__ = [
     "dg_fp8_grouped_gemm_masked", "dg_fp8_grouped_gemm_masked_workspace_bytes",
     "dg_fp8_grouped_gemm_contig_ue8m0", "dg_fp8_grouped_gemm_masked_ue8m0", "alloc_workspace",
     "WORKSPACE_COUNTER_BYTES", "dg_fp8_gemm_nt_noalloc", "NOALLOC_SCRATCH_BYTES",
+    "mxfp4_shapes", "dg_quantize_mxfp4", "dg_dequantize_mxfp4", "to_mxfp4", "to_mxfp4_both",
+    "from_mxfp4", "dg_mxfp4_gemm_nt_workspace_bytes", "dg_mxfp4_gemm_nt", "mxfp4_gemm_nt",
+    "dg_mxfp4_gemm_nt_bf16a_workspace_bytes", "dg_mxfp4_gemm_nt_bf16a", "MXFP4_BF16A_MAX_M",
+    "dg_moe_layer_workspace_bytes", "dg_moe_layer", "MOE_SCORINGS",
 ]
 # (the _epilogue C entry points are reached through the act / residual
 # arguments of dg_fp8_grouped_gemm_contig and dg_fp8_grouped_gemm_masked)

@@ -448,4 +448,134 @@ int dg_fp8_gemm_nt_noalloc(uint16_t* c, const uint8_t* a, const uint8_t* b, cons
   return dg_fp8_gemm_nt(c, a, b, sa, sb, a_block_rows, M, N, K, ws, need, stream);
 }
 
+// ---- MXFP4 and the mixture-of-experts layer ----
+
+namespace {
+
+constexpr int64_t kMaxScaleWords = int64_t(1) << 29;  // scale arrays below 2^31 bytes
+
+bool scale_words_ok(int64_t rows, int64_t cols) {
+  return (cols + 127) / 128 <= (kMaxScaleWords - 1) / rows;
+}
+
+int check_mxfp4(const void* c, const void* a, const void* b, const void* sfb, int64_t M, int64_t N,
+                int64_t K) {
+  if (!c || !a || !b || !sfb) return DG_ERR_NULL;
+  if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || K > (int64_t(1) << 23)) return DG_ERR_SHAPE;
+  if (M > INT32_MAX || N > INT32_MAX || !scale_words_ok(M, K) || !scale_words_ok(N, K))
+    return DG_ERR_SHAPE;
+  if (!aligned(c, N % 4 == 0 ? 8 : 2) || !aligned(a, 16) || !aligned(b, 16) || !aligned(sfb, 4))
+    return DG_ERR_ALIGN;
+  return DG_OK;
+}
+
+int run_mxfp4(const dg::Mxfp4Problem& p, void* workspace, size_t workspace_bytes, void* stream) {
+  if (workspace != nullptr && workspace_bytes > 0) {
+    if (workspace_bytes < dg::mxfp4_workspace_bytes(p.M, p.N, p.K, p.sfa == nullptr))
+      return DG_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return DG_ERR_ALIGN;
+  } else {
+    workspace = nullptr;
+    workspace_bytes = 0;
+  }
+  return from_hip(dg::launch_gemm_mxfp4(p, workspace, workspace_bytes,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+int dg_quantize_mxfp4(uint8_t* q, int32_t* sf, uint8_t* qt, int32_t* sft, const void* x, int dtype,
+                      int64_t rows, int64_t cols, int64_t ldx, void* stream) {
+  if (!x || (!q && !qt) || !q != !sf || !qt != !sft) return DG_ERR_NULL;
+  if (dtype != DG_DTYPE_F32 && dtype != DG_DTYPE_BF16) return DG_ERR_UNSUPPORTED;
+  if (rows < 1 || cols < 1 || ldx < cols || ldx > INT64_MAX / 4 / rows) return DG_ERR_SHAPE;
+  if (!scale_words_ok(rows, cols) || !scale_words_ok(cols, rows)) return DG_ERR_SHAPE;
+  if (!aligned(x, dtype == DG_DTYPE_BF16 ? 2 : 4) || !aligned(q, 16) || !aligned(qt, 16) ||
+      !aligned(sf, 4) || !aligned(sft, 4))
+    return DG_ERR_ALIGN;
+  return from_hip(dg::launch_quantize_mxfp4(q, reinterpret_cast<uint32_t*>(sf), qt,
+                                            reinterpret_cast<uint32_t*>(sft), x,
+                                            dtype == DG_DTYPE_BF16, rows, cols, ldx,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+int dg_dequantize_mxfp4(void* out, int dtype, const uint8_t* q, const int32_t* sf, int64_t rows,
+                        int64_t cols, void* stream) {
+  if (!out || !q || !sf) return DG_ERR_NULL;
+  if (dtype != DG_DTYPE_F32 && dtype != DG_DTYPE_BF16) return DG_ERR_UNSUPPORTED;
+  if (rows < 1 || cols < 1 || !scale_words_ok(rows, cols)) return DG_ERR_SHAPE;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(sf, 4)) return DG_ERR_ALIGN;
+  return from_hip(dg::launch_dequantize_mxfp4(out, dtype == DG_DTYPE_BF16, q,
+                                              reinterpret_cast<const uint32_t*>(sf), rows, cols,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+size_t dg_mxfp4_gemm_nt_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || N < 1 || K < 1) return 0;
+  return dg::mxfp4_workspace_bytes(M, N, K, false);
+}
+
+int dg_mxfp4_gemm_nt(uint16_t* c, const uint8_t* a, const uint8_t* b, const int32_t* sfa,
+                     const int32_t* sfb, int64_t M, int64_t N, int64_t K, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  const int st = check_mxfp4(c, a, b, sfb, M, N, K);
+  if (st != DG_OK) return st;
+  if (!sfa) return DG_ERR_NULL;
+  if (!aligned(sfa, 4)) return DG_ERR_ALIGN;
+  const dg::Mxfp4Problem p{c, a, b, reinterpret_cast<const uint32_t*>(sfa),
+                           reinterpret_cast<const uint32_t*>(sfb), M, N, K};
+  return run_mxfp4(p, workspace, workspace_bytes, stream);
+}
+
+size_t dg_mxfp4_gemm_nt_bf16a_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || N < 1 || K < 1) return 0;
+  return dg::mxfp4_workspace_bytes(M, N, K, true);
+}
+
+int dg_mxfp4_gemm_nt_bf16a(uint16_t* c, const uint16_t* a, const uint8_t* b, const int32_t* sfb,
+                           int64_t M, int64_t N, int64_t K, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const int st = check_mxfp4(c, a, b, sfb, M, N, K);
+  if (st != DG_OK) return st;
+  if (M > DG_MXFP4_BF16A_MAX_M) return DG_ERR_SHAPE;
+  const dg::Mxfp4Problem p{c, a, b, nullptr, reinterpret_cast<const uint32_t*>(sfb), M, N, K};
+  return run_mxfp4(p, workspace, workspace_bytes, stream);
+}
+
+namespace {
+
+// H / 16 column tiles each have an arrival counter in the workspace
+static_assert(131072 / 16 * 4 <= DG_WORKSPACE_COUNTER_BYTES, "counters of the layer");
+
+bool moe_shape_ok(int T, int E, int k, int64_t H, int64_t I) {
+  return T >= 1 && T <= DG_MOE_MAX_TOKENS && E >= 1 && E <= DG_MOE_MAX_EXPERTS && k >= 1 &&
+         k <= E && k <= DG_MOE_MAX_SLOTS && H >= 32 && H <= 131072 && I >= 32 &&
+         I <= (int64_t(1) << 20) && scale_words_ok(2 * I, H) && scale_words_ok(H, I);
+}
+
+}  // namespace
+
+size_t dg_moe_layer_workspace_bytes(int T, int E, int k, int64_t H, int64_t I) {
+  return moe_shape_ok(T, E, k, H, I) ? dg::moe_workspace_bytes(T, E, k, H, I) : 0;
+}
+
+int dg_moe_layer(uint16_t* y, const uint16_t* x, const uint8_t* w13, const uint8_t* w2,
+                 const void* s13, const void* s2, int format, int32_t* ids, float* weights,
+                 const float* logits, int scoring, int T, int E, int k, int64_t H, int64_t I,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!y || !x || !w13 || !w2 || !s13 || !s2 || !ids || !weights) return DG_ERR_NULL;
+  if (format != DG_MOE_MXFP4 && format != DG_MOE_FP8) return DG_ERR_UNSUPPORTED;
+  if (logits && scoring != DG_MOE_SOFTMAX && scoring != DG_MOE_SIGMOID) return DG_ERR_UNSUPPORTED;
+  const int64_t step = format == DG_MOE_FP8 ? 128 : 32;
+  if (!moe_shape_ok(T, E, k, H, I) || H % step != 0 || I % step != 0) return DG_ERR_SHAPE;
+  if (!workspace || workspace_bytes < dg::moe_workspace_bytes(T, E, k, H, I))
+    return DG_ERR_WORKSPACE;
+  if (!aligned(y, 16) || !aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) ||
+      !aligned(workspace, 16) || !aligned(s13, 4) || !aligned(s2, 4) || !aligned(ids, 4) ||
+      !aligned(weights, 4) || !aligned(logits, 4))
+    return DG_ERR_ALIGN;
+  dg::MoeProblem p{y, x, w13, w2, s13, s2, ids, weights, logits, scoring, format, T, E, k, H, I};
+  return from_hip(dg::launch_moe_layer(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

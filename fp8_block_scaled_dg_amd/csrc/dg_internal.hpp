@@ -111,4 +111,49 @@ hipError_t launch_zero_counters(void* scratch_ptr, hipStream_t stream);
 hipError_t launch_gemm_stream(const GemmProblem& p, hipStream_t stream);
 bool stream_preferred(int64_t M, int64_t N, int64_t K);
 
+// MXFP4 quantiser: rowwise q / sf and, or, transposed qt / sft (null: not
+// wanted) of x [rows][ldx] (BF16 or FP32), and its inverse.
+hipError_t launch_quantize_mxfp4(uint8_t* q, uint32_t* sf, uint8_t* qt, uint32_t* sft,
+                                 const void* x, bool bf16, int64_t rows, int64_t cols, int64_t ldx,
+                                 hipStream_t stream);
+hipError_t launch_dequantize_mxfp4(void* out, bool bf16, const uint8_t* q, const uint32_t* sf,
+                                   int64_t rows, int64_t cols, hipStream_t stream);
+
+// C = A . B^T with B in MXFP4 and A in MXFP4 (sfa given) or BF16 (sfa null).
+struct Mxfp4Problem {
+  uint16_t* c;
+  const void* a;
+  const uint8_t* b;
+  const uint32_t* sfa;
+  const uint32_t* sfb;
+  int64_t M, N, K;
+};
+size_t mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K, bool bf16_a);
+hipError_t launch_gemm_mxfp4(const Mxfp4Problem& p, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+// Mixture-of-experts layer for a few tokens.  logits null: ids and weights
+// are inputs.
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxSlots = 16;
+constexpr int kMoeMaxPairs = kMoeMaxTokens * kMoeMaxSlots;
+constexpr int kMoeMaxExperts = 1024;
+enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 };
+struct MoeProblem {
+  uint16_t* y;
+  const uint16_t* x;
+  const uint8_t* w13;
+  const uint8_t* w2;
+  const void* s13;
+  const void* s2;
+  int32_t* ids;
+  float* weights;
+  const float* logits;
+  int scoring, format;  // format: 0 MXFP4, 1 E4M3 with FP32 block scales
+  int T, E, k;
+  int64_t H, I;
+};
+size_t moe_workspace_bytes(int T, int E, int k, int64_t H, int64_t I);
+hipError_t launch_moe_layer(const MoeProblem& p, void* workspace, hipStream_t stream);
+
 }  // namespace dg

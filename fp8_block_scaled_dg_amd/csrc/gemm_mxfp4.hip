@@ -1,0 +1,201 @@
+// MXFP4 NT products for gfx950:
+//   C[m][n] = bf16( sum_k A[m][k] B[n][k] ),
+// B in MXFP4 (mxfp4_device.hpp), A in MXFP4 or in BF16.
+//
+// gemm_mxfp4_stream_kernel: a workgroup's four waves take the same 16 NF rows
+// of B and 16 NI rows of A and a quarter each of a run of K; their FP32 sums
+// meet in LDS and are added in wave order.  With S > 1 the run is the S-th
+// part of K: each part's sums go to the workspace and the last workgroup to
+// arrive adds the parts in order, so the result does not depend on which one
+// that is.
+#include "mxfp4_device.hpp"
+
+namespace dg {
+namespace {
+
+constexpr int kMaxCounters = (int)(kSplitkCounterBytes / 4);
+constexpr int kWaves = 4;
+
+struct Mxfp4Args {
+  uint16_t* c;
+  const uint8_t* a;
+  const uint8_t* b;
+  const uint32_t* sfa;
+  const uint32_t* sfb;
+  int64_t M, N, K;
+  float* partials;  // [tile][S][NF NI][64] quads, when S > 1
+  int* counters;
+  int S;
+};
+
+// Four consecutive outputs of row m from column n (n % 4 == 0), as far as the
+// row goes; rows of C start 8-byte aligned only if N % 4 == 0.
+__device__ __forceinline__ void store_quad(uint16_t* c, int64_t m, int64_t n, int64_t N, v4f t) {
+  const uint32_t lo = bf16x2_rne(t[0], t[1]), hi = bf16x2_rne(t[2], t[3]);
+  uint16_t* d = c + m * N + n;
+  if ((N & 3) == 0) {
+    if (n < N) *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+    return;
+  }
+  if (n < N) d[0] = (uint16_t)lo;
+  if (n + 1 < N) d[1] = (uint16_t)(lo >> 16);
+  if (n + 2 < N) d[2] = (uint16_t)hi;
+  if (n + 3 < N) d[3] = (uint16_t)(hi >> 16);
+}
+
+template <int AF, int NI, int NF, int U>
+__global__ void __launch_bounds__(64 * kWaves) gemm_mxfp4_stream_kernel(Mxfp4Args p) {
+  constexpr int Q = NF * NI;
+  __shared__ v4f red[kWaves][Q][64];
+  __shared__ int s_last;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fr = lane & 15;
+  const int tile_n = blockIdx.x / p.S;
+  const int split = blockIdx.x - tile_n * p.S;
+  const int64_t n0 = (int64_t)tile_n * (16 * NF);
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * NI);
+  const int rows_b = (int)(p.N - n0 < 16 * NF ? p.N - n0 : 16 * NF);
+  const int rows_a = (int)(p.M - m0 < 16 * NI ? p.M - m0 : 16 * NI);
+  const int64_t ldb = p.K / 2, lda = AF == ACT_BF16 ? p.K * 2 : p.K / 2;
+  const int nkb = (int)((p.K + 127) / 128);
+
+  StreamOperands o;
+  o.b = buffer_of(p.b + n0 * ldb, rows_b * ldb);
+  o.sb = buffer_of(p.sfb + n0, (nkb * p.N - n0) * 4);
+  o.sb_step = (uint32_t)p.N * 4;
+  o.a = buffer_of(p.a + m0 * lda, rows_a * lda);
+  if (AF == ACT_MXFP4) {
+    o.sa = buffer_of(p.sfa + m0, (nkb * p.M - m0) * 4);
+    o.sa_step = (uint32_t)p.M * 4;
+  }
+  Stream<AF, FMT_MXFP4, NI, NF, U> s;
+  s.g = lane >> 4;
+#pragma unroll
+  for (int f = 0; f < NF; ++f) {
+    const int r = 16 * f + fr;
+    s.vb[f] = r < rows_b ? (uint32_t)(r * ldb + 16 * s.g) : kOob;
+    s.vsb[f] = r < rows_b ? (uint32_t)(4 * r) : kOob;
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = 16 * i + fr;
+    s.va[i] = r < rows_a ? (uint32_t)(r * lda + (AF == ACT_BF16 ? 64 : 16) * s.g) : kOob;
+    s.vsa[i] = r < rows_a ? (uint32_t)(4 * r) : kOob;
+  }
+  const int parts = p.S * kWaves, part = split * kWaves + wave;
+  const int kb0 = (int)((int64_t)part * nkb / parts);
+  const int kb1 = (int)((int64_t)(part + 1) * nkb / parts);
+  const int kmax = kb1 * 128 < p.K ? kb1 * 128 : (int)p.K;
+
+  v4f acc[NF][NI];
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) acc[f][i] = v4f{0.f, 0.f, 0.f, 0.f};
+  s.run(o, kb0, kb1, kmax, acc);
+
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) red[wave][f * NI + i][lane] = acc[f][i];
+  __syncthreads();
+
+  const int64_t tile = (int64_t)blockIdx.y * (gridDim.x / p.S) + tile_n;
+  auto sum_waves = [&](int q) {
+    v4f t = red[0][q][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) t += red[w][q][lane];
+    return t;
+  };
+  auto store = [&](int q, v4f t) {
+    const int f = q / NI, i = q - f * NI;
+    const int64_t m = m0 + 16 * i + fr;
+    if (m < p.M) store_quad(p.c, m, n0 + 16 * f + 4 * s.g, p.N, t);
+  };
+  if (p.S == 1) {
+    for (int q = wave; q < Q; q += kWaves) store(q, sum_waves(q));
+    return;
+  }
+  float* part0 = p.partials + tile * p.S * (Q * 256);
+  for (int q = wave; q < Q; q += kWaves)
+    publish4(part0 + split * (Q * 256) + (q * 64 + lane) * 4, sum_waves(q));
+  if (!arrive_last(&p.counters[tile], p.S, &s_last)) return;
+  for (int q = wave; q < Q; q += kWaves) {
+    v4f t = collect4(part0 + (q * 64 + lane) * 4);
+    for (int sp = 1; sp < p.S; ++sp) t += collect4(part0 + sp * (Q * 256) + (q * 64 + lane) * 4);
+    store(q, t);
+  }
+  if (threadIdx.x == 0)  // zero again for the next call
+    __hip_atomic_store(&p.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Rows of A per workgroup, rows of B per workgroup and K parts of the stream
+// kernel for a shape.
+struct StreamPlan {
+  int ni, nf, S;
+  int64_t tiles_m, tiles_n;
+};
+
+StreamPlan stream_plan(int64_t M, int64_t N, int64_t K) {
+  StreamPlan s;
+  s.ni = M <= 16 ? 1 : (M <= 32 ? 2 : (M <= 48 ? 3 : 4));
+  s.nf = 1;
+  s.tiles_m = (M + 16 * s.ni - 1) / (16 * s.ni);
+  s.tiles_n = (N + 16 * s.nf - 1) / (16 * s.nf);
+  s.S = 1;
+  const int64_t tiles = s.tiles_m * s.tiles_n, nkb = (K + 127) / 128;
+  while (tiles * s.S < 512 && tiles <= kMaxCounters && nkb / (2 * s.S) >= 16 && s.S < 16) s.S *= 2;
+  return s;
+}
+
+template <int AF, int NI>
+hipError_t launch_stream(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
+  constexpr int U = AF == ACT_BF16 ? (NI > 2 ? 1 : 2) : 4;
+  dim3 grid((unsigned)(s.tiles_n * p.S), (unsigned)s.tiles_m);
+  hipLaunchKernelGGL((gemm_mxfp4_stream_kernel<AF, NI, 1, U>), grid, dim3(64 * kWaves), 0, stream,
+                     p);
+  return hipGetLastError();
+}
+
+size_t plan_bytes(const StreamPlan& s) {
+  if (s.S == 1) return 0;
+  return kSplitkCounterBytes + (size_t)(s.tiles_m * s.tiles_n) * s.S * s.ni * s.nf * 1024;
+}
+
+}  // namespace
+
+size_t mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K, bool bf16_a) {
+  (void)bf16_a;
+  return plan_bytes(stream_plan(M, N, K));
+}
+
+hipError_t launch_gemm_mxfp4(const Mxfp4Problem& q, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+  Mxfp4Args p;
+  p.c = q.c;
+  p.a = static_cast<const uint8_t*>(q.a);
+  p.b = q.b;
+  p.sfa = q.sfa;
+  p.sfb = q.sfb;
+  p.M = q.M;
+  p.N = q.N;
+  p.K = q.K;
+  StreamPlan s = stream_plan(q.M, q.N, q.K);
+  if (workspace_bytes < plan_bytes(s)) s.S = 1;
+  p.S = s.S;
+  p.counters = static_cast<int*>(workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kSplitkCounterBytes);
+  if (q.sfa == nullptr) {
+    if (s.ni == 1) return launch_stream<ACT_BF16, 1>(p, s, stream);
+    if (s.ni == 2) return launch_stream<ACT_BF16, 2>(p, s, stream);
+    if (s.ni == 3) return launch_stream<ACT_BF16, 3>(p, s, stream);
+    return launch_stream<ACT_BF16, 4>(p, s, stream);
+  }
+  if (s.ni == 1) return launch_stream<ACT_MXFP4, 1>(p, s, stream);
+  if (s.ni == 2) return launch_stream<ACT_MXFP4, 2>(p, s, stream);
+  if (s.ni == 3) return launch_stream<ACT_MXFP4, 3>(p, s, stream);
+  return launch_stream<ACT_MXFP4, 4>(p, s, stream);
+}
+
+}  // namespace dg

@@ -448,6 +448,106 @@ int dg_fp8_gemm_nt_noalloc(uint16_t *c, const uint8_t *a, const uint8_t *b,
                            const float *sa, const float *sb, int a_block_rows,
                            int64_t M, int64_t N, int64_t K, void *stream);
 
+/*
+ * MXFP4 (microscaled 4-bit floating point): E2M1 codes (magnitudes 0 .5 1 1.5
+ * 2 3 4 6, bit 3 the sign) with one E8M0 exponent byte (2^(byte - 127); 255:
+ * the block is NaN) per 32 values along a row.
+ *   codes : uint8 [rows][ceil(cols/32) * 16]; value k of a row in nibble k % 2
+ *           (0: low) of byte k / 2, zeros past cols.
+ *   sf    : int32 [ceil(cols/128)][rows], K-block-major, byte j of a word the
+ *           exponent of 32-block 4 * (cols index / 128) + j, 0 past the end.
+ *
+ * dg_quantize_mxfp4: codes and exponents of x along its rows (q, sf), along
+ * its columns (qt, sft: those of the transpose, [cols] rows of `rows` values),
+ * or both from one reading of x; a pair of NULLs leaves a direction out.
+ *   x     : dtype DG_DTYPE_BF16 or DG_DTYPE_F32, [rows][ldx], ldx >= cols
+ *           elements from row to row, aligned to its element only.
+ * e = max(floor(log2(amax)) - 2, -127) per block, codes rounded to nearest,
+ * ties to even, saturating at 6.  A block with an infinity or a NaN gets the
+ * exponent byte 255 and codes 0.  q, qt 16-byte, sf, sft 4-byte aligned.
+ *
+ * dg_dequantize_mxfp4: the values, [rows][cols] contiguous in dtype (exact in
+ * BF16 except below 2^-126, where they are BF16 subnormals, exact too).
+ *
+ * rows, cols >= 1, rows * ceil(cols/128) and cols * ceil(rows/128) < 2^29.
+ * (OCP Microscaling Formats 1.0, MXFP4; the framework's own scale layout.)
+ */
+#define DG_DTYPE_F32 0
+#define DG_DTYPE_BF16 1
+int dg_quantize_mxfp4(uint8_t *q, int32_t *sf, uint8_t *qt, int32_t *sft, const void *x,
+                      int dtype, int64_t rows, int64_t cols, int64_t ldx, void *stream);
+int dg_dequantize_mxfp4(void *out, int dtype, const uint8_t *q, const int32_t *sf, int64_t rows,
+                        int64_t cols, void *stream);
+
+/*
+ * C[M][N] (BF16) = A[M][K] . B[N][K]^T, both MXFP4 as above (codes [M][K/2]
+ * and [N][K/2]), sums in FP32.  K % 32 == 0; M and N are free (no alignment
+ * of N).  Scale bytes past K are ignored.  A block whose exponent byte is 255
+ * makes its row's (column's) outputs NaN.
+ *   workspace : optional split-K scratch of
+ *               dg_mxfp4_gemm_nt_workspace_bytes(M, N, K) bytes, as for
+ *               dg_fp8_gemm_nt; without one (or with a smaller one:
+ *               DG_ERR_WORKSPACE) the plan does not split K.
+ * Requirements: M, N >= 1; 32 <= K <= 2^23; M * ceil(K/128) and
+ * N * ceil(K/128) < 2^29; c 2-byte (8-byte if N % 4 == 0), codes 16-byte,
+ * scales 4-byte aligned.  Deterministic.
+ */
+size_t dg_mxfp4_gemm_nt_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int dg_mxfp4_gemm_nt(uint16_t *c, const uint8_t *a, const uint8_t *b, const int32_t *sfa,
+                     const int32_t *sfb, int64_t M, int64_t N, int64_t K, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * dg_mxfp4_gemm_nt with A in BF16 [M][K] (16-byte aligned), not quantised,
+ * M <= DG_MXFP4_BF16A_MAX_M: B is widened to BF16 (exact) on its way into the
+ * matrix cores.  Workspace: dg_mxfp4_gemm_nt_bf16a_workspace_bytes.
+ */
+#define DG_MXFP4_BF16A_MAX_M 64
+size_t dg_mxfp4_gemm_nt_bf16a_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int dg_mxfp4_gemm_nt_bf16a(uint16_t *c, const uint16_t *a, const uint8_t *b, const int32_t *sfb,
+                           int64_t M, int64_t N, int64_t K, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (T <= 64):
+ *   h[t][j] = w[t][j] * silu(x[t] . Wg^T) * (x[t] . Wu^T),  y[t] = sum_j h[t][j] . W2^T
+ * with the weights of expert ids[t][j], each expert's weights read once.
+ *   y, x    : BF16 [T][H]; y may not alias x.
+ *   w13     : codes [E][2 I][H]: row 2i gate, row 2i + 1 up of hidden unit i.
+ *   w2      : codes [E][H][I].
+ *   format  : DG_MOE_MXFP4 (codes and sf per expert as above: s13 int32
+ *             [E][ceil(H/128)][2 I], s2 int32 [E][ceil(I/128)][H]; H and I
+ *             multiples of 32) or DG_MOE_FP8 (E4M3, s13 FP32
+ *             [E][H/128][ceil(2 I/128)], s2 FP32 [E][I/128][ceil(H/128)];
+ *             H and I multiples of 128).
+ *   logits  : FP32 [T][E], or NULL.  Given: ids (int32 [T][k]) and weights
+ *             (FP32 [T][k]) are outputs: the k largest logits of each token
+ *             in descending order (ties: lowest index) and their scores
+ *             (scoring DG_MOE_SOFTMAX or DG_MOE_SIGMOID) divided by their sum.
+ *             Logits of -inf or NaN are never chosen; slots without an expert
+ *             get id -1 and weight 0.  NULL: ids and weights are inputs, an
+ *             id outside [0, E) is an empty slot, scoring is ignored.
+ *   A token without an expert gets y = 0.
+ *   workspace: dg_moe_layer_workspace_bytes bytes, required, 16-byte aligned,
+ *             counter region as for the split-K workspaces.
+ * The hidden values h are rounded to BF16 once (with their weight); all sums
+ * are FP32.  Requirements: 1 <= T <= DG_MOE_MAX_TOKENS, 1 <= E <=
+ * DG_MOE_MAX_EXPERTS, 1 <= k <= min(E, DG_MOE_MAX_SLOTS), H <= 131072,
+ * I <= 2^20; x, y, codes 16-byte, the rest 4-byte aligned.  Deterministic.
+ */
+#define DG_MOE_MXFP4 0
+#define DG_MOE_FP8 1
+#define DG_MOE_SOFTMAX 0
+#define DG_MOE_SIGMOID 1
+#define DG_MOE_MAX_TOKENS 64
+#define DG_MOE_MAX_SLOTS 16
+#define DG_MOE_MAX_EXPERTS 1024
+size_t dg_moe_layer_workspace_bytes(int T, int E, int k, int64_t H, int64_t I);
+int dg_moe_layer(uint16_t *y, const uint16_t *x, const uint8_t *w13, const uint8_t *w2,
+                 const void *s13, const void *s2, int format, int32_t *ids, float *weights,
+                 const float *logits, int scoring, int T, int E, int k, int64_t H, int64_t I,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
