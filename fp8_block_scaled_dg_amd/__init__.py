@@ -142,13 +142,15 @@ def get_mk_alignment_for_contiguous_layout() -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
+    """The stream's handle; by default the current stream's of the current
+    device (asked for by handle: a torch.cuda.Stream object costs 3 us)."""
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    return ctypes.c_void_p(stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream
 
 
 def _check(rc: int, where: str):
@@ -168,16 +170,21 @@ def _require(t, dtype, name):
 
 
 def _codes(t, name):
-    if t.dtype == torch.float8_e4m3fn:
-        t = t.view(torch.uint8)
-    _require(t, torch.uint8, name)
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
+        _require(t, torch.float8_e4m3fn, name)
+    else:
+        _require(t, torch.uint8, name)
     return t
 
 
+_BF16_TYPES = (torch.bfloat16, getattr(torch, "uint16", torch.int16))  # or int16: raw bits
+
+
 def _bf16(t, name):
-    if t.dtype in (torch.bfloat16, getattr(torch, "uint16", torch.int16)):
-        t = t.view(torch.int16)
-    _require(t, torch.int16, name)
+    if isinstance(t, torch.Tensor) and t.dtype in _BF16_TYPES:
+        _require(t, t.dtype, name)
+    else:
+        _require(t, torch.int16, name)
     return t
 
 
@@ -593,32 +600,36 @@ def mxfp4_shapes(rows: int, cols: int):
 
 
 def _mxfp4_pair(q, sf, rows, cols, what):
-    if (q is None) != (sf is None):
-        raise ValueError("%s needs codes and scales" % what)
-    if q is None:
-        return
     _require(q, torch.uint8, what)
     _require(sf, torch.int32, "scales of " + what)
-    if (tuple(q.shape), tuple(sf.shape)) != mxfp4_shapes(rows, cols):
+    if q.shape != (rows, (cols + 31) // 32 * 16) or sf.shape != ((cols + 127) // 128, rows):
         raise ValueError("%s must be codes %s and scales %s" % ((what,) + mxfp4_shapes(rows, cols)))
+
+
+def _mxfp4_source(x):
+    """(rows, cols, row stride, dtype code) of a matrix to quantise."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
+        raise TypeError("x must be a float32 or bfloat16 tensor")
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    rows, cols = x.shape
+    ld, one = x.stride()
+    if cols > 1 and one != 1 or rows > 1 and ld < cols:
+        raise ValueError("the rows of x must be contiguous and must not overlap")
+    return rows, cols, ld if rows > 1 else cols, _DTYPES[x.dtype]
 
 
 def dg_quantize_mxfp4(x, q=None, sf=None, qt=None, sft=None, stream=None) -> None:
     """x float32 or bfloat16 [rows, cols], its rows contiguous (any row stride)
     -> MXFP4 codes and scales along the rows (q, sf), along the columns (qt,
     sft: those of x.t()), or both; shapes as mxfp4_shapes gives them."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
-        raise TypeError("x must be a float32 or bfloat16 tensor")
-    if not x.is_cuda:
-        raise ValueError("x must be a device tensor")
-    rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1 or rows > 1 and x.stride(0) < cols:
-        raise ValueError("the rows of x must be contiguous and must not overlap")
-    _mxfp4_pair(q, sf, rows, cols, "q")
-    _mxfp4_pair(qt, sft, cols, rows, "qt")
-    _check(lib.dg_quantize_mxfp4(_ptr(q), _ptr(sf), _ptr(qt), _ptr(sft), _ptr(x),
-                                 _DTYPES[x.dtype], rows, cols, x.stride(0) if rows > 1 else cols,
-                                 _stream(stream)), "dg_quantize_mxfp4")
+    rows, cols, ld, dtype = _mxfp4_source(x)
+    if q is not None or sf is not None:
+        _mxfp4_pair(q, sf, rows, cols, "q")
+    if qt is not None or sft is not None:
+        _mxfp4_pair(qt, sft, cols, rows, "qt")
+    _check(lib.dg_quantize_mxfp4(_ptr(q), _ptr(sf), _ptr(qt), _ptr(sft), _ptr(x), dtype, rows,
+                                 cols, ld, _stream(stream)), "dg_quantize_mxfp4")
 
 
 def dg_dequantize_mxfp4(out, q, sf, stream=None) -> None:
@@ -641,7 +652,7 @@ def dg_mxfp4_gemm_nt(c, a, b, sfa, sfb, workspace=None, stream=None) -> None:
     c = _bf16(c, "c")
     M, N = c.shape
     K = 2 * a.shape[1]
-    if a.shape[0] != M or tuple(b.shape) != (N, K // 2):
+    if a.shape[0] != M or b.shape != (N, K // 2):
         raise ValueError("shape mismatch: a %s, b %s, c %s" % (tuple(a.shape), tuple(b.shape),
                                                               tuple(c.shape)))
     _mxfp4_pair(a, sfa, M, K, "a")
@@ -665,7 +676,7 @@ def dg_mxfp4_gemm_nt_bf16a(c, a, b, sfb, workspace=None, stream=None) -> None:
     a = _bf16(a, "a")
     M, K = a.shape
     N = b.shape[0]
-    if tuple(b.shape) != (N, K // 2) or c.shape != (M, N):
+    if b.shape != (N, K // 2) or c.shape != (M, N):
         raise ValueError("shape mismatch: a %s, b %s, c %s" % (tuple(a.shape), tuple(b.shape),
                                                               tuple(c.shape)))
     _mxfp4_pair(b, sfb, N, K, "b")
@@ -709,13 +720,13 @@ def dg_moe_layer(y, x, w13, w2, s13, s2, ids, weights, logits=None, scoring: str
     per = 1 if fp8 else 2
     scales = (((E, cdiv(H, 128), cdiv(2 * I, 128)), (E, cdiv(I, 128), cdiv(H, 128))) if fp8 else
               ((E, cdiv(H, 128), 2 * I), (E, cdiv(I, 128), H)))
-    if (y.shape != x.shape or tuple(w13.shape) != (E, 2 * I, H // per)
-            or tuple(w2.shape) != (E, H, I // per) or tuple(ids.shape) != (T, k)
-            or tuple(weights.shape) != (T, k) or (tuple(s13.shape), tuple(s2.shape)) != scales):
+    if (y.shape != x.shape or w13.shape != (E, 2 * I, H // per) or w2.shape != (E, H, I // per)
+            or ids.shape != (T, k) or weights.shape != (T, k)
+            or (tuple(s13.shape), tuple(s2.shape)) != scales):
         raise ValueError("inconsistent mixture-of-experts shapes")
     if logits is not None:
         _require(logits, torch.float32, "logits")
-        if tuple(logits.shape) != (T, E):
+        if logits.shape != (T, E):
             raise ValueError("logits must be [T, E]")
     _check(lib.dg_moe_layer(_ptr(y), _ptr(x), _ptr(w13), _ptr(w2), _ptr(s13), _ptr(s2), int(fp8),
                             _ptr(ids), _ptr(weights), _ptr(logits), MOE_SCORINGS[scoring], T, E, k,
@@ -759,32 +770,34 @@ def fp8_grouped_gemm_contig(c, a, b, sa, sb, m_indices, a_block_rows: int = 1):
     return c
 
 
+def _mxfp4_empty(rows, cols, device):
+    qs, ss = mxfp4_shapes(rows, cols)
+    return (torch.empty(qs, dtype=torch.uint8, device=device),
+            torch.empty(ss, dtype=torch.int32, device=device))
+
+
 def to_mxfp4(x, transposed: bool = False):
     """Quantise a float32 or bfloat16 device matrix to MXFP4 along its rows,
     or (transposed) along its columns -> (codes, scales) of x, or of x.t()."""
-    rows, cols = x.shape
-    if transposed:
-        rows, cols = cols, rows
-    qs, ss = mxfp4_shapes(rows, cols)
-    q = torch.empty(qs, dtype=torch.uint8, device=x.device)
-    sf = torch.empty(ss, dtype=torch.int32, device=x.device)
-    if transposed:
-        dg_quantize_mxfp4(x, qt=q, sft=sf)
-    else:
-        dg_quantize_mxfp4(x, q, sf)
+    rows, cols, ld, dtype = _mxfp4_source(x)
+    q, sf = _mxfp4_empty(cols, rows, x.device) if transposed else _mxfp4_empty(rows, cols, x.device)
+    p = q.data_ptr(), sf.data_ptr()
+    p = (None, None) + p if transposed else p + (None, None)
+    _check(lib.dg_quantize_mxfp4(*p, x.data_ptr(), dtype, rows, cols, ld, _stream(None)),
+           "dg_quantize_mxfp4")
     return q, sf
 
 
 def to_mxfp4_both(x):
     """Both directions from one reading of x: (q, sf) of x, (qt, sft) of
     x.t()."""
-    rows, cols = x.shape
-    out = []
-    for shape in (mxfp4_shapes(rows, cols), mxfp4_shapes(cols, rows)):
-        out.append(torch.empty(shape[0], dtype=torch.uint8, device=x.device))
-        out.append(torch.empty(shape[1], dtype=torch.int32, device=x.device))
-    dg_quantize_mxfp4(x, *out)
-    return tuple(out)
+    rows, cols, ld, dtype = _mxfp4_source(x)
+    q, sf = _mxfp4_empty(rows, cols, x.device)
+    qt, sft = _mxfp4_empty(cols, rows, x.device)
+    _check(lib.dg_quantize_mxfp4(q.data_ptr(), sf.data_ptr(), qt.data_ptr(), sft.data_ptr(),
+                                 x.data_ptr(), dtype, rows, cols, ld, _stream(None)),
+           "dg_quantize_mxfp4")
+    return q, sf, qt, sft
 
 
 def from_mxfp4(q, sf, cols: int, dtype=torch.bfloat16):

@@ -455,16 +455,17 @@ namespace {
 constexpr int64_t kMaxScaleWords = int64_t(1) << 29;  // scale arrays below 2^31 bytes
 
 bool scale_words_ok(int64_t rows, int64_t cols) {
-  return (cols + 127) / 128 <= (kMaxScaleWords - 1) / rows;
+  return rows < kMaxScaleWords && cols < kMaxScaleWords &&
+         (cols + 127) / 128 <= (kMaxScaleWords - 1) / rows;
 }
 
 int check_mxfp4(const void* c, const void* a, const void* b, const void* sfb, int64_t M, int64_t N,
                 int64_t K) {
   if (!c || !a || !b || !sfb) return DG_ERR_NULL;
   if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || K > (int64_t(1) << 23)) return DG_ERR_SHAPE;
-  if (M > INT32_MAX || N > INT32_MAX || !scale_words_ok(M, K) || !scale_words_ok(N, K))
+  if (!scale_words_ok(M, K) || !scale_words_ok(N, K) || M > (int64_t(1) << 44) / N)
     return DG_ERR_SHAPE;
-  if (!aligned(c, N % 4 == 0 ? 8 : 2) || !aligned(a, 16) || !aligned(b, 16) || !aligned(sfb, 4))
+  if (!aligned(c, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(sfb, 4))
     return DG_ERR_ALIGN;
   return DG_OK;
 }
@@ -488,7 +489,7 @@ int dg_quantize_mxfp4(uint8_t* q, int32_t* sf, uint8_t* qt, int32_t* sft, const 
                       int64_t rows, int64_t cols, int64_t ldx, void* stream) {
   if (!x || (!q && !qt) || !q != !sf || !qt != !sft) return DG_ERR_NULL;
   if (dtype != DG_DTYPE_F32 && dtype != DG_DTYPE_BF16) return DG_ERR_UNSUPPORTED;
-  if (rows < 1 || cols < 1 || ldx < cols || ldx > INT64_MAX / 4 / rows) return DG_ERR_SHAPE;
+  if (rows < 1 || rows > (1 << 22) || cols < 1 || ldx < cols || ldx > INT64_MAX / 4 / rows) return DG_ERR_SHAPE;
   if (!scale_words_ok(rows, cols) || !scale_words_ok(cols, rows)) return DG_ERR_SHAPE;
   if (!aligned(x, dtype == DG_DTYPE_BF16 ? 2 : 4) || !aligned(q, 16) || !aligned(qt, 16) ||
       !aligned(sf, 4) || !aligned(sft, 4))

@@ -9,6 +9,7 @@
 // arrive adds the parts in order, so the result does not depend on which one
 // that is.
 #include "mxfp4_device.hpp"
+#include <stdlib.h>
 
 namespace dg {
 namespace {
@@ -54,9 +55,8 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_mxfp4_stream_kernel(Mxfp4Arg
   const int tile_n = blockIdx.x / p.S;
   const int split = blockIdx.x - tile_n * p.S;
   const int64_t n0 = (int64_t)tile_n * (16 * NF);
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * NI);
   const int rows_b = (int)(p.N - n0 < 16 * NF ? p.N - n0 : 16 * NF);
-  const int rows_a = (int)(p.M - m0 < 16 * NI ? p.M - m0 : 16 * NI);
+  const int rows_a = (int)p.M;  // <= 16 NI
   const int64_t ldb = p.K / 2, lda = AF == ACT_BF16 ? p.K * 2 : p.K / 2;
   const int nkb = (int)((p.K + 127) / 128);
 
@@ -64,9 +64,9 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_mxfp4_stream_kernel(Mxfp4Arg
   o.b = buffer_of(p.b + n0 * ldb, rows_b * ldb);
   o.sb = buffer_of(p.sfb + n0, (nkb * p.N - n0) * 4);
   o.sb_step = (uint32_t)p.N * 4;
-  o.a = buffer_of(p.a + m0 * lda, rows_a * lda);
+  o.a = buffer_of(p.a, rows_a * lda);
   if (AF == ACT_MXFP4) {
-    o.sa = buffer_of(p.sfa + m0, (nkb * p.M - m0) * 4);
+    o.sa = buffer_of(p.sfa, nkb * p.M * 4);
     o.sa_step = (uint32_t)p.M * 4;
   }
   Stream<AF, FMT_MXFP4, NI, NF, U> s;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_mxfp4_stream_kernel(Mxfp4Arg
     for (int i = 0; i < NI; ++i) red[wave][f * NI + i][lane] = acc[f][i];
   __syncthreads();
 
-  const int64_t tile = (int64_t)blockIdx.y * (gridDim.x / p.S) + tile_n;
+  const int tile = tile_n;
   auto sum_waves = [&](int q) {
     v4f t = red[0][q][lane];
 #pragma unroll
@@ -110,14 +110,14 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_mxfp4_stream_kernel(Mxfp4Arg
   };
   auto store = [&](int q, v4f t) {
     const int f = q / NI, i = q - f * NI;
-    const int64_t m = m0 + 16 * i + fr;
+    const int64_t m = 16 * i + fr;
     if (m < p.M) store_quad(p.c, m, n0 + 16 * f + 4 * s.g, p.N, t);
   };
   if (p.S == 1) {
     for (int q = wave; q < Q; q += kWaves) store(q, sum_waves(q));
     return;
   }
-  float* part0 = p.partials + tile * p.S * (Q * 256);
+  float* part0 = p.partials + (int64_t)tile * p.S * (Q * 256);
   for (int q = wave; q < Q; q += kWaves)
     publish4(part0 + split * (Q * 256) + (q * 64 + lane) * 4, sum_waves(q));
   if (!arrive_last(&p.counters[tile], p.S, &s_last)) return;
@@ -130,48 +130,128 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_mxfp4_stream_kernel(Mxfp4Arg
     __hip_atomic_store(&p.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// The same with the activations in LDS (Shared, mxfp4_device.hpp): 128 rows of
+// B a workgroup, eight waves.
+template <int AF, int NI, int KS>
+__global__ void __launch_bounds__(kSharedThreads) gemm_mxfp4_shared_kernel(Mxfp4Args p) {
+  constexpr int NF = 4, QT = 2 * NF * NI;
+  typedef Shared<AF, FMT_MXFP4, NI, NF, KS> S;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+  __shared__ int s_last;
+  const int tile = blockIdx.x / p.S;
+  const int split = blockIdx.x - tile * p.S;
+  const int64_t n0 = (int64_t)tile * (32 * NF);
+  const int rows_b = (int)(p.N - n0 < 32 * NF ? p.N - n0 : 32 * NF);
+  const int rows_a = (int)p.M;
+  const int64_t ldb = p.K / 2, lda = AF == ACT_BF16 ? p.K * 2 : p.K / 2;
+  const int nkb = (int)((p.K + 127) / 128);
+  StreamOperands o;
+  o.b = buffer_of(p.b + n0 * ldb, rows_b * ldb);
+  o.sb = buffer_of(p.sfb + n0, (nkb * p.N - n0) * 4);
+  o.sb_step = (uint32_t)p.N * 4;
+  o.a = buffer_of(p.a, rows_a * lda);
+  if (AF == ACT_MXFP4) {
+    o.sa = buffer_of(p.sfa, nkb * p.M * 4);
+    o.sa_step = (uint32_t)p.M * 4;
+  }
+  S s;
+  s.init(ldb, rows_b, lda, [&](int r) { return r < rows_a ? r : -1; });
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto store = [&](int q, v4f t) {
+    const int f = q / NI, i = q - f * NI;
+    const int64_t m = 16 * i + (lane & 15);
+    if (m < p.M) store_quad(p.c, m, n0 + 16 * f + 4 * (lane >> 4), p.N, t);
+  };
+  float* part0 = p.partials + (int64_t)tile * p.S * (QT * 256);
+  s.run(o, p.K, split * S::WK, p.S * S::WK, lds, [&](int f, int i, v4f t) {
+    const int q = f * NI + i;
+    if (p.S == 1) store(q, t);
+    else publish4(part0 + split * (QT * 256) + (q * 64 + lane) * 4, t);
+  });
+  if (p.S == 1) return;
+  if (!arrive_last(&p.counters[tile], p.S, &s_last)) return;
+  for (int q = wave; q < QT; q += 8) {
+    v4f t = collect4(part0 + (q * 64 + lane) * 4);
+    for (int sp = 1; sp < p.S; ++sp) t += collect4(part0 + sp * (QT * 256) + (q * 64 + lane) * 4);
+    store(q, t);
+  }
+  if (threadIdx.x == 0)
+    __hip_atomic_store(&p.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // Rows of A per workgroup, rows of B per workgroup and K parts of the stream
 // kernel for a shape.
 struct StreamPlan {
-  int ni, nf, S;
-  int64_t tiles_m, tiles_n;
+  int ni, nf, S, u;
+  int64_t tiles_n;
 };
 
-StreamPlan stream_plan(int64_t M, int64_t N, int64_t K) {
+int envi(const char* n, int d) { const char* e = getenv(n); return e ? atoi(e) : d; }
+
+StreamPlan stream_plan(int64_t M, int64_t N, int64_t K, bool bf16_a) {
   StreamPlan s;
   s.ni = M <= 16 ? 1 : (M <= 32 ? 2 : (M <= 48 ? 3 : 4));
-  s.nf = 1;
-  s.tiles_m = (M + 16 * s.ni - 1) / (16 * s.ni);
+  s.nf = envi("DG_NF", 1);
+  s.u = envi("DG_U", 1);
   s.tiles_n = (N + 16 * s.nf - 1) / (16 * s.nf);
   s.S = 1;
-  const int64_t tiles = s.tiles_m * s.tiles_n, nkb = (K + 127) / 128;
+  const int64_t tiles = s.tiles_n, nkb = (K + 127) / 128;
   while (tiles * s.S < 512 && tiles <= kMaxCounters && nkb / (2 * s.S) >= 16 && s.S < 16) s.S *= 2;
+  s.S = envi("DG_S", s.S);
   return s;
 }
 
-template <int AF, int NI>
+template <int AF, int NI, int NF, int U>
 hipError_t launch_stream(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
-  constexpr int U = AF == ACT_BF16 ? (NI > 2 ? 1 : 2) : 4;
-  dim3 grid((unsigned)(s.tiles_n * p.S), (unsigned)s.tiles_m);
-  hipLaunchKernelGGL((gemm_mxfp4_stream_kernel<AF, NI, 1, U>), grid, dim3(64 * kWaves), 0, stream,
-                     p);
+  hipLaunchKernelGGL((gemm_mxfp4_stream_kernel<AF, NI, NF, U>), dim3((unsigned)(s.tiles_n * p.S)),
+                     dim3(64 * kWaves), 0, stream, p);
   return hipGetLastError();
+}
+template <int AF, int NI, int NF>
+hipError_t launch_u(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
+  if (s.u == 1) return launch_stream<AF, NI, NF, 1>(p, s, stream);
+  if (s.u == 2) return launch_stream<AF, NI, NF, 2>(p, s, stream);
+  return launch_stream<AF, NI, NF, 4>(p, s, stream);
+}
+template <int AF, int NI, int KS>
+hipError_t launch_sh(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
+  hipLaunchKernelGGL((gemm_mxfp4_shared_kernel<AF, NI, KS>), dim3((unsigned)(s.tiles_n * p.S)),
+                     dim3(kSharedThreads), 0, stream, p);
+  return hipGetLastError();
+}
+template <int AF, int NI>
+hipError_t launch_nf(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
+  if (s.nf == 8) {
+    if (s.u == 1 && AF == ACT_BF16) return launch_sh<AF, NI, AF == ACT_BF16 ? 1 : 2>(p, s, stream);
+    return launch_sh<AF, NI, (AF == ACT_BF16 && NI > 2) ? 1 : 2>(p, s, stream);
+  }
+  if (s.nf == 1) return launch_u<AF, NI, 1>(p, s, stream);
+  if (s.nf == 2) return launch_u<AF, NI, 2>(p, s, stream);
+  return launch_u<AF, NI, 4>(p, s, stream);
+}
+template <int AF>
+hipError_t launch_ni(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
+  if (s.ni == 1) return launch_nf<AF, 1>(p, s, stream);
+  if (s.ni == 2) return launch_nf<AF, 2>(p, s, stream);
+  if (s.ni == 3) return launch_nf<AF, 3>(p, s, stream);
+  return launch_nf<AF, 4>(p, s, stream);
 }
 
 size_t plan_bytes(const StreamPlan& s) {
   if (s.S == 1) return 0;
-  return kSplitkCounterBytes + (size_t)(s.tiles_m * s.tiles_n) * s.S * s.ni * s.nf * 1024;
+  return kSplitkCounterBytes + (size_t)s.tiles_n * s.S * s.ni * s.nf * 1024;
 }
 
 }  // namespace
 
 size_t mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K, bool bf16_a) {
-  (void)bf16_a;
-  return plan_bytes(stream_plan(M, N, K));
+  if (M > 64) return 0;
+  return plan_bytes(stream_plan(M, N, K, bf16_a));
 }
 
 hipError_t launch_gemm_mxfp4(const Mxfp4Problem& q, void* workspace, size_t workspace_bytes,
                              hipStream_t stream) {
+  if (q.M > 64) return launch_gemm_mxfp4_tiled(q, stream);
   Mxfp4Args p;
   p.c = q.c;
   p.a = static_cast<const uint8_t*>(q.a);
@@ -181,21 +261,12 @@ hipError_t launch_gemm_mxfp4(const Mxfp4Problem& q, void* workspace, size_t work
   p.M = q.M;
   p.N = q.N;
   p.K = q.K;
-  StreamPlan s = stream_plan(q.M, q.N, q.K);
+  StreamPlan s = stream_plan(q.M, q.N, q.K, q.sfa == nullptr);
   if (workspace_bytes < plan_bytes(s)) s.S = 1;
   p.S = s.S;
   p.counters = static_cast<int*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kSplitkCounterBytes);
-  if (q.sfa == nullptr) {
-    if (s.ni == 1) return launch_stream<ACT_BF16, 1>(p, s, stream);
-    if (s.ni == 2) return launch_stream<ACT_BF16, 2>(p, s, stream);
-    if (s.ni == 3) return launch_stream<ACT_BF16, 3>(p, s, stream);
-    return launch_stream<ACT_BF16, 4>(p, s, stream);
-  }
-  if (s.ni == 1) return launch_stream<ACT_MXFP4, 1>(p, s, stream);
-  if (s.ni == 2) return launch_stream<ACT_MXFP4, 2>(p, s, stream);
-  if (s.ni == 3) return launch_stream<ACT_MXFP4, 3>(p, s, stream);
-  return launch_stream<ACT_MXFP4, 4>(p, s, stream);
+  return q.sfa ? launch_ni<ACT_MXFP4>(p, s, stream) : launch_ni<ACT_BF16>(p, s, stream);
 }
 
 }  // namespace dg

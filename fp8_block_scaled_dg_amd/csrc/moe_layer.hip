@@ -12,6 +12,7 @@
 // routing weight in its epilogue, and down, whose last workgroup per column
 // tile adds the k slots of each token in slot order.
 #include "mxfp4_device.hpp"
+#include <stdlib.h>
 
 namespace dg {
 namespace {
@@ -148,28 +149,31 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(MoeArgs p) {
   if (tid == 0) *p.tb.active = s_active;
 }
 
-// f(IntTag<NI>) for the 16-row fragments that `rows` rows need, at most 4
-template <class F>
+// f(IntTag<NI>) for the 16-row fragments that `rows` rows need, at most MAXNI
+template <int MAXNI, int NI = 1, class F>
 __device__ __forceinline__ void with_fragments(int rows, F&& f) {
-  if (rows <= 16) f(IntTag<1>{});
-  else if (rows <= 32) f(IntTag<2>{});
-  else if (rows <= 48) f(IntTag<3>{});
-  else f(IntTag<4>{});
+  if constexpr (NI == MAXNI) {
+    f(IntTag<NI>{});
+  } else {
+    if (rows <= 16 * NI) f(IntTag<NI>{});
+    else with_fragments<MAXNI, NI + 1>(rows, f);
+  }
 }
 
-// Sums over the four waves of one tile of 16 weight rows by 16 NI activation
-// rows; finish(i, quad) is called by the wave that owns fragment i.
-template <int BF, int NI, class Rows, class Finish>
+// Sums over the four waves of one tile of 16 NF weight rows by 16 NI
+// activation rows; finish(f, i, quad) is called for every fragment by the
+// wave that owns it.
+template <int BF, int NI, int NF, int U, class Rows, class Finish>
 __device__ __forceinline__ void expert_tile(const uint8_t* w, const void* scales, int64_t N,
                                             int64_t K, int64_t n0, const void* act,
-                                            int64_t act_bytes, Rows&& row_of, v4f (*red)[4][64],
+                                            int64_t act_bytes, Rows&& row_of, v4f* red,
                                             Finish&& finish) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15;
   const int nkb = (int)((K + 127) / 128);
   const int64_t ldb = BF == FMT_FP8 ? K : K / 2;
-  const int rows_b = (int)(N - n0 < 16 ? N - n0 : 16);
+  const int rows_b = (int)(N - n0 < 16 * NF ? N - n0 : 16 * NF);
   StreamOperands o;
   o.b = buffer_of(w + n0 * ldb, rows_b * ldb);
   if (BF == FMT_FP8) {
@@ -181,11 +185,14 @@ __device__ __forceinline__ void expert_tile(const uint8_t* w, const void* scales
     o.sb_step = (uint32_t)N * 4;
   }
   o.a = buffer_of(act, act_bytes);
-  constexpr int U = NI > 2 ? 1 : 2;
-  Stream<ACT_BF16, BF, NI, 1, U> s;
+  Stream<ACT_BF16, BF, NI, NF, U> s;
   s.g = lane >> 4;
-  s.vb[0] = fr < rows_b ? (uint32_t)(fr * ldb + (BF == FMT_FP8 ? 32 : 16) * s.g) : kOob;
-  s.vsb[0] = fr < rows_b ? (uint32_t)(4 * fr) : kOob;
+#pragma unroll
+  for (int f = 0; f < NF; ++f) {
+    const int r = 16 * f + fr;
+    s.vb[f] = r < rows_b ? (uint32_t)(r * ldb + (BF == FMT_FP8 ? 32 : 16) * s.g) : kOob;
+    s.vsb[f] = r < rows_b ? (uint32_t)(4 * r) : kOob;
+  }
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int r = row_of(16 * i + fr);  // row of the activations, -1: none
@@ -193,47 +200,52 @@ __device__ __forceinline__ void expert_tile(const uint8_t* w, const void* scales
   }
   const int kb0 = wave * nkb / kWaves, kb1 = (wave + 1) * nkb / kWaves;
   const int kmax = kb1 * 128 < K ? kb1 * 128 : (int)K;
-  v4f acc[1][NI];
+  v4f acc[NF][NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) acc[0][i] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) acc[f][i] = v4f{0.f, 0.f, 0.f, 0.f};
   s.run(o, kb0, kb1, kmax, acc);
+  constexpr int Q = NF * NI;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) red[wave][i][lane] = acc[0][i];
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) red[(wave * Q + f * NI + i) * 64 + lane] = acc[f][i];
   __syncthreads();
-  if (wave < NI) {
-    v4f t = red[0][wave][lane];
+  for (int q = wave; q < Q; q += kWaves) {
+    v4f t = red[q * 64 + lane];
 #pragma unroll
-    for (int q = 1; q < kWaves; ++q) t += red[q][wave][lane];
-    finish(wave, t);
+    for (int v = 1; v < kWaves; ++v) t += red[(v * Q + q) * 64 + lane];
+    finish(q / NI, q % NI, t);
   }
   __syncthreads();  // red is free again
 }
 
 // gate/up: rows 2i and 2i + 1 of W13 give gate and up of hidden unit i
-template <int BF>
+template <int BF, int MAXNI, int NF, int U>
 __global__ void __launch_bounds__(64 * kWaves) moe_up_kernel(MoeArgs p) {
-  __shared__ v4f red[kWaves][4][64];
+  __shared__ v4f red[kWaves * NF * MAXNI * 64];
   const int e = blockIdx.y;
   const int count = p.tb.counts[e];
   if (count == 0) return;
   const int lane = threadIdx.x & 63, fr = lane & 15;
-  const int64_t N = 2 * p.I, K = p.H, n0 = (int64_t)blockIdx.x * 16;
+  const int64_t N = 2 * p.I, K = p.H, n0 = (int64_t)blockIdx.x * (16 * NF);
   const int* list = p.tb.pairs + p.tb.offsets[e];
   const int64_t sstep = BF == FMT_FP8 ? (K / 128) * ((N + 127) / 128) : ((K + 127) / 128) * N;
   const uint8_t* w = p.w13 + (int64_t)e * N * (BF == FMT_FP8 ? K : K / 2);
   const void* sc = static_cast<const uint32_t*>(p.s13) + e * sstep;
-  for (int c0 = 0; c0 < count; c0 += 64) {
-    const int rows = count - c0 < 64 ? count - c0 : 64;
-    with_fragments(rows, [&](auto ni) {
-      expert_tile<BF, decltype(ni)::value>(
+  for (int c0 = 0; c0 < count; c0 += 16 * MAXNI) {
+    const int rows = count - c0 < 16 * MAXNI ? count - c0 : 16 * MAXNI;
+    with_fragments<MAXNI>(rows, [&](auto ni) {
+      expert_tile<BF, decltype(ni)::value, NF, U>(
           w, sc, N, K, n0, p.x, p.T * K * 2,
           [&](int r) { return r < rows ? list[c0 + r] / p.k : -1; }, red,
-          [&](int i, v4f t) {
+          [&](int f, int i, v4f t) {
             const int r = 16 * i + fr;
             if (r >= rows) return;
             const int pair = list[c0 + r];
             const float wt = p.weights[pair];
-            const int64_t u = (n0 + 4 * (lane >> 4)) / 2;  // hidden units u, u + 1 (I is even)
+            const int64_t u = (n0 + 16 * f + 4 * (lane >> 4)) / 2;  // units u, u + 1 (I is even)
             if (u >= p.I) return;
             *reinterpret_cast<uint32_t*>(p.h + pair * p.I + u) =
                 bf16x2_rne(silu_f(t[0]) * t[1] * wt, silu_f(t[2]) * t[3] * wt);
@@ -242,19 +254,19 @@ __global__ void __launch_bounds__(64 * kWaves) moe_up_kernel(MoeArgs p) {
   }
 }
 
-template <int BF>
+template <int BF, int MAXNI, int NF, int U>
 __global__ void __launch_bounds__(64 * kWaves) moe_down_kernel(MoeArgs p) {
-  __shared__ v4f red[kWaves][4][64];
+  __shared__ v4f red[kWaves * NF * MAXNI * 64];
   __shared__ int s_last;
   const int e = blockIdx.y;
   const int count = p.tb.counts[e];
   const int active = *p.tb.active;
   const int lane = threadIdx.x & 63, fr = lane & 15;
-  const int64_t N = p.H, K = p.I, n0 = (int64_t)blockIdx.x * 16;
+  const int64_t N = p.H, K = p.I, n0 = (int64_t)blockIdx.x * (16 * NF);
   if (active == 0) {  // no token chose anything: y = 0
     if (e == 0)
-      for (int q = threadIdx.x; q < p.T * 16; q += 64 * kWaves)
-        if (n0 + (q & 15) < N) p.y[(q >> 4) * N + n0 + (q & 15)] = 0;
+      for (int q = threadIdx.x; q < p.T * 16 * NF; q += 64 * kWaves)
+        if (n0 + q % (16 * NF) < N) p.y[q / (16 * NF) * N + n0 + q % (16 * NF)] = 0;
     return;
   }
   if (count == 0) return;
@@ -262,23 +274,23 @@ __global__ void __launch_bounds__(64 * kWaves) moe_down_kernel(MoeArgs p) {
   const int64_t sstep = BF == FMT_FP8 ? (K / 128) * ((N + 127) / 128) : ((K + 127) / 128) * N;
   const uint8_t* w = p.w2 + (int64_t)e * N * (BF == FMT_FP8 ? K : K / 2);
   const void* sc = static_cast<const uint32_t*>(p.s2) + e * sstep;
-  for (int c0 = 0; c0 < count; c0 += 64) {
-    const int rows = count - c0 < 64 ? count - c0 : 64;
-    with_fragments(rows, [&](auto ni) {
-      expert_tile<BF, decltype(ni)::value>(
+  for (int c0 = 0; c0 < count; c0 += 16 * MAXNI) {
+    const int rows = count - c0 < 16 * MAXNI ? count - c0 : 16 * MAXNI;
+    with_fragments<MAXNI>(rows, [&](auto ni) {
+      expert_tile<BF, decltype(ni)::value, NF, U>(
           w, sc, N, K, n0, p.h, (int64_t)p.T * p.k * K * 2,
           [&](int r) { return r < rows ? list[c0 + r] : -1; }, red,
-          [&](int i, v4f t) {
+          [&](int f, int i, v4f t) {
             const int r = 16 * i + fr;
-            const int64_t n = n0 + 4 * (lane >> 4);
+            const int64_t n = n0 + 16 * f + 4 * (lane >> 4);
             if (r < rows && n < N) publish4(p.part + list[c0 + r] * N + n, t);
           });
     });
   }
   if (!arrive_last(&p.counters[blockIdx.x], active, &s_last)) return;
-  for (int q = threadIdx.x; q < p.T * 4; q += 64 * kWaves) {
-    const int t = q >> 2;
-    const int64_t n = n0 + 4 * (q & 3);
+  for (int q = threadIdx.x; q < p.T * 4 * NF; q += 64 * kWaves) {
+    const int t = q / (4 * NF);
+    const int64_t n = n0 + 4 * (q % (4 * NF));
     if (n >= N) continue;
     v4f s = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < p.k; ++j) {
@@ -306,15 +318,35 @@ MoeLayout moe_layout(int T, int E, int k, int64_t H, int64_t I) {
   return l;
 }
 
-template <int BF>
-hipError_t launch_experts(const MoeArgs& p, hipStream_t stream) {
-  hipLaunchKernelGGL(moe_up_kernel<BF>, dim3((unsigned)((2 * p.I + 15) / 16), (unsigned)p.E),
-                     dim3(64 * kWaves), 0, stream, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_down_kernel<BF>, dim3((unsigned)((p.H + 15) / 16), (unsigned)p.E),
+int envi(const char* n, int d) { const char* e = getenv(n); return e ? atoi(e) : d; }
+
+template <int BF, int MAXNI, int NF, int U>
+hipError_t launch_up(const MoeArgs& p, hipStream_t stream) {
+  hipLaunchKernelGGL((moe_up_kernel<BF, MAXNI, NF, U>),
+                     dim3((unsigned)((2 * p.I + 16 * NF - 1) / (16 * NF)), (unsigned)p.E),
                      dim3(64 * kWaves), 0, stream, p);
   return hipGetLastError();
+}
+template <int BF, int MAXNI, int NF, int U>
+hipError_t launch_down(const MoeArgs& p, hipStream_t stream) {
+  hipLaunchKernelGGL((moe_down_kernel<BF, MAXNI, NF, U>),
+                     dim3((unsigned)((p.H + 16 * NF - 1) / (16 * NF)), (unsigned)p.E),
+                     dim3(64 * kWaves), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <int BF, int MAXNI>
+hipError_t launch_experts(const MoeArgs& p, hipStream_t stream) {
+  hipError_t e;
+  const int a = envi("DG_UP", 11), b = envi("DG_DN", 11);
+#define X(A, FN) switch (A) { case 11: e = FN<BF, MAXNI, 1, 1>(p, stream); break; \
+  case 12: e = FN<BF, MAXNI, 1, 2>(p, stream); break; case 14: e = FN<BF, MAXNI, 1, 4>(p, stream); break;\
+  case 21: e = FN<BF, MAXNI, 2, 1>(p, stream); break; case 22: e = FN<BF, MAXNI, 2, 2>(p, stream); break; \
+  case 41: e = FN<BF, MAXNI, 4, 1>(p, stream); break; default: e = FN<BF, MAXNI, 4, 2>(p, stream); }
+  X(a, launch_up)
+  if (e != hipSuccess) return e;
+  X(b, launch_down)
+  return e;
 }
 
 }  // namespace
@@ -352,8 +384,11 @@ hipError_t launch_moe_layer(const MoeProblem& q, void* workspace, hipStream_t st
   hipLaunchKernelGGL(moe_router_kernel, dim3(1), dim3(kRouterThreads), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return q.format == FMT_FP8 ? launch_experts<FMT_FP8>(p, stream)
-                             : launch_experts<FMT_MXFP4>(p, stream);
+  if (q.T <= 16)
+    return q.format == FMT_FP8 ? launch_experts<FMT_FP8, 1>(p, stream)
+                               : launch_experts<FMT_MXFP4, 1>(p, stream);
+  return q.format == FMT_FP8 ? launch_experts<FMT_FP8, 4>(p, stream)
+                             : launch_experts<FMT_MXFP4, 4>(p, stream);
 }
 
 }  // namespace dg

@@ -195,11 +195,247 @@ struct Stream {
     Buf x0, x1;
     load(o, x0, kb0, kmax);
     for (int kb = kb0; kb < kb1; kb += 2 * U) {
+      // the fences keep every load of a buffer ahead of the products of the
+      // other one; left to itself the scheduler sinks the loads among the
+      // products and the loop waits for memory with nothing in flight
       load(o, x1, kb + U, kmax);
+      __builtin_amdgcn_sched_barrier(0);
       multiply(x0, acc);
+      __builtin_amdgcn_sched_barrier(0);
       load(o, x0, kb + 2 * U, kmax);
+      __builtin_amdgcn_sched_barrier(0);
       multiply(x1, acc);
+      __builtin_amdgcn_sched_barrier(0);
     }
+  }
+};
+
+// Row r of the activations, 16-byte chunk c of its 256 (BF16) or 128 (MXFP4)
+// bytes in LDS: the slot that keeps both the fragment reads (lane 16g + r
+// reads chunk 4g + j, or 4h + g, of row r; served in the groups of lanes that
+// a 16-byte read has) and the row-wise writes off each other's banks.
+template <int AF>
+__device__ __forceinline__ int act_slot(int r, int c) {
+  if (AF == ACT_BF16) return c ^ ((r & 3) | ((r & 8) ? 12 : 0));
+  return c ^ ((r & 2) | ((r >> 1) & 4));
+}
+
+// The same product with the activations staged in LDS, for more than a few of
+// their rows: read straight into fragments they cost, per K block, NI / NF
+// times the weight's bytes and more requests than bytes (a fragment's 16 rows
+// are 16 pieces of 64 bytes).  Eight waves: WK = 4 runs of K, and in each run
+// two waves with 16 NF weight rows each, which share the run's activations.
+// A stage is KS K blocks.  Activations go memory -> registers -> LDS one stage
+// ahead of their use (full rows, 256 or 128 bytes each), weights straight into
+// registers one stage ahead.
+constexpr int kSharedThreads = 512;
+template <int AF, int BF, int NI, int NF, int KS>
+struct Shared {
+  static constexpr int WK = 4, WN = 2, BV = BF == FMT_FP8 ? 2 : 1;
+  static constexpr int MP = 16 * NI;
+  static constexpr int ROW = AF == ACT_BF16 ? 256 : 128;        // bytes of an LDS row
+  static constexpr int TILES = AF == ACT_BF16 ? KS : KS / 2;    // LDS tiles of MP rows a stage
+  static constexpr int LPR = ROW / 16;                          // lanes per row
+  static constexpr int RPI = 64 * WN / LPR;                     // rows per load of the two waves
+  static constexpr int IT = (MP + RPI - 1) / RPI;
+  static constexpr int STAGE = TILES * MP * ROW;                // bytes of a run's stage
+  static constexpr int LDS = 2 * WK * STAGE > 8 * NF * NI * 1024 ? 2 * WK * STAGE
+                                                                  : 8 * NF * NI * 1024;
+  static_assert(AF == ACT_BF16 || KS % 2 == 0, "MXFP4 stages are pairs of K blocks");
+  struct B {
+    v4i b[KS][NF][BV];
+    uint32_t sb[KS][BF == FMT_FP8 ? 1 : NF];
+    uint32_t sa[KS][AF == ACT_BF16 ? 1 : NI];
+  };
+  struct A {
+    v4i v[TILES][IT];
+  };
+  uint32_t vb[NF], vsb[NF], vsa[NI], va[IT];
+  int lane, wave, wk, wn, g;
+
+  // row_of(r): activation row of the tile's row r, or -1
+  template <class Rows>
+  __device__ __forceinline__ void init(int64_t ldb, int rows_b, int64_t lda, Rows&& row_of) {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    wn = wave & 1;
+    wk = wave >> 1;
+    g = lane >> 4;
+    const int fr = lane & 15;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const int r = 16 * (NF * wn + f) + fr;
+      vb[f] = r < rows_b ? (uint32_t)(r * ldb + 16 * BV * g) : kOob;
+      vsb[f] = r < rows_b ? (uint32_t)(4 * r) : kOob;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = row_of(16 * i + fr);
+      vsa[i] = r >= 0 ? (uint32_t)(4 * r) : kOob;
+    }
+    const int t = wn * 64 + lane;
+#pragma unroll
+    for (int j = 0; j < IT; ++j) {
+      const int r = j * RPI + t / LPR;
+      const int a = r < MP ? row_of(r) : -1;
+      va[j] = a >= 0 ? (uint32_t)(a * lda + 16 * (t % LPR)) : kOob;
+    }
+  }
+
+  __device__ __forceinline__ void load_b(const StreamOperands& o, B& x, int kb, int kmax) const {
+#pragma unroll
+    for (int u = 0; u < KS; ++u) {
+      const bool in = (kb + u) * 128 + 32 * g < kmax;
+      const uint32_t k = (uint32_t)(kb + u);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const uint32_t v = in ? vb[f] : kOob;
+#pragma unroll
+        for (int h = 0; h < BV; ++h) x.b[u][f][h] = load16(o.b, v + 16 * h, k * (64 * BV));
+        if (BF == FMT_MXFP4) x.sb[u][f] = load4(o.sb, in ? vsb[f] : kOob, k * o.sb_step);
+      }
+      if (BF == FMT_FP8) x.sb[u][0] = load4(o.sb, in ? 0u : kOob, k * o.sb_step);
+      if (AF == ACT_MXFP4) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          x.sa[u][i] = load4(o.sa, in ? vsa[i] : kOob, k * o.sa_step);
+      }
+    }
+  }
+  __device__ __forceinline__ void load_a(const StreamOperands& o, A& x, int kb, int kmax) const {
+    const int c = (wn * 64 + lane) % LPR;
+    constexpr int TK = AF == ACT_BF16 ? 128 : 256, CK = TK / LPR;  // K of a tile, of a chunk
+#pragma unroll
+    for (int u = 0; u < TILES; ++u) {
+      const bool in = kb * 128 + u * TK + c * CK < kmax;
+#pragma unroll
+      for (int j = 0; j < IT; ++j)
+        x.v[u][j] = load16(o.a, in ? va[j] : kOob,
+                           (uint32_t)kb * (AF == ACT_BF16 ? 256 : 64) + u * ROW);
+    }
+  }
+  __device__ __forceinline__ void store_a(const A& x, uint8_t* st) const {
+    const int t = wn * 64 + lane, c = t % LPR;
+#pragma unroll
+    for (int u = 0; u < TILES; ++u)
+#pragma unroll
+      for (int j = 0; j < IT; ++j) {
+        const int r = j * RPI + t / LPR;
+        if (MP % RPI == 0 || r < MP)
+          *reinterpret_cast<v4i*>(st + (u * MP + r) * ROW + 16 * act_slot<AF>(r, c)) = x.v[u][j];
+      }
+  }
+  __device__ __forceinline__ v4i frag(const uint8_t* st, int tile, int i, int c) const {
+    const int fr = lane & 15;
+    return *reinterpret_cast<const v4i*>(st + (tile * MP + 16 * i + fr) * ROW +
+                                         16 * act_slot<AF>(fr, c));
+  }
+  __device__ __forceinline__ void multiply(const B& x, const uint8_t* st,
+                                           v4f (&acc)[NF][NI]) const {
+    const int sh = 8 * g;
+#pragma unroll
+    for (int u = 0; u < KS; ++u) {
+      if constexpr (AF == ACT_MXFP4) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const v4i q = frag(st, u >> 1, i, 4 * (u & 1) + g);
+          const v8i aq = {q[0], q[1], q[2], q[3], 0, 0, 0, 0};
+#pragma unroll
+          for (int f = 0; f < NF; ++f) {
+            const v4i p = x.b[u][f][0];
+            const v8i bq = {p[0], p[1], p[2], p[3], 0, 0, 0, 0};
+            acc[f][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                bq, aq, acc[f][i], 4, 4, 0, (int)(x.sb[u][f] >> sh), 0, (int)(x.sa[u][i] >> sh));
+          }
+        }
+      } else {
+        dg_bf16x8 bw[NF][4];
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          if constexpr (BF == FMT_FP8)
+            widen_fp8(x.b[u][f][0], x.b[u][f][1], bw[f]);
+          else
+            widen_mxfp4(x.b[u][f][0], x.sb[u][f] >> sh, bw[f]);
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          dg_bf16x8 aw[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            aw[j] = __builtin_bit_cast(dg_bf16x8, frag(st, u, i, 4 * g + j));
+#pragma unroll
+          for (int f = 0; f < NF; ++f) {
+            v4f t = BF == FMT_FP8 ? v4f{0.f, 0.f, 0.f, 0.f} : acc[f][i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[f][j], aw[j], t, 0, 0, 0);
+            if constexpr (BF == FMT_FP8)
+              acc[f][i] += t * __uint_as_float(x.sb[u][0]);
+            else
+              acc[f][i] = t;
+          }
+        }
+      }
+    }
+  }
+
+  // K blocks of part wk of `parts` runs; every wave of the workgroup makes the
+  // same number of stages (the barriers), past its run on zeros.
+  // finish(f, i, quad): f in [0, WN NF), each fragment by the wave that owns it.
+  template <class Finish>
+  __device__ __forceinline__ void run(const StreamOperands& o, int64_t K, int part0, int parts,
+                                      uint8_t* lds, Finish&& finish) {
+    const int nkb = (int)((K + 127) / 128);
+    const int part = part0 + wk;
+    const int kb0 = (int)((int64_t)part * nkb / parts);
+    const int kb1 = (int)((int64_t)(part + 1) * nkb / parts);
+    const int kmax = kb1 * 128 < K ? kb1 * 128 : (int)K;
+    const int stages = ((nkb + parts - 1) / parts + KS - 1) / KS;  // of the longest run
+    uint8_t* s0 = lds + wk * (2 * STAGE);
+    uint8_t* s1 = s0 + STAGE;
+    v4f acc[NF][NI];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) acc[f][i] = v4f{0.f, 0.f, 0.f, 0.f};
+    A a;
+    B b0, b1;
+    load_a(o, a, kb0, kmax);
+    load_b(o, b0, kb0, kmax);
+    store_a(a, s0);
+    load_a(o, a, kb0 + KS, kmax);
+    __syncthreads();
+    auto stage = [&](const B& cur, B& nxt, const uint8_t* rd, uint8_t* wr, int kb) {
+      load_b(o, nxt, kb + KS, kmax);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(cur, rd, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      store_a(a, wr);
+      load_a(o, a, kb + 2 * KS, kmax);
+      __builtin_amdgcn_sched_barrier(0);
+      // the stage's LDS writes are visible before any wave reads them; loads
+      // in flight stay in flight
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    for (int s = 0; s < stages; s += 2) {
+      stage(b0, b1, s0, s1, kb0 + s * KS);
+      if (s + 1 < stages) stage(b1, b0, s1, s0, kb0 + (s + 1) * KS);
+    }
+    __syncthreads();  // the stages' room becomes the sums'
+    v4f* red = reinterpret_cast<v4f*>(lds);
+    constexpr int Q = NF * NI;
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) red[((wk * WN + wn) * Q + f * NI + i) * 64 + lane] = acc[f][i];
+    __syncthreads();
+    for (int q = wave; q < WN * Q; q += WN * WK) {
+      v4f t = red[q * 64 + lane];
+#pragma unroll
+      for (int v = 1; v < WK; ++v) t += red[(v * WN * Q + q) * 64 + lane];
+      finish(q / NI, q % NI, t);  // q / Q is the wave's half: fragment rows follow on
+    }
+    __syncthreads();
   }
 };
 

@@ -469,7 +469,8 @@ int dg_fp8_gemm_nt_noalloc(uint16_t *c, const uint8_t *a, const uint8_t *b,
  * dg_dequantize_mxfp4: the values, [rows][cols] contiguous in dtype (exact in
  * BF16 except below 2^-126, where they are BF16 subnormals, exact too).
  *
- * rows, cols >= 1, rows * ceil(cols/128) and cols * ceil(rows/128) < 2^29.
+ * rows, cols >= 1, rows <= 2^22 (quantiser), rows * ceil(cols/128) and
+ * cols * ceil(rows/128) < 2^29.
  * (OCP Microscaling Formats 1.0, MXFP4; the framework's own scale layout.)
  */
 #define DG_DTYPE_F32 0
@@ -488,9 +489,8 @@ int dg_dequantize_mxfp4(void *out, int dtype, const uint8_t *q, const int32_t *s
  *               dg_mxfp4_gemm_nt_workspace_bytes(M, N, K) bytes, as for
  *               dg_fp8_gemm_nt; without one (or with a smaller one:
  *               DG_ERR_WORKSPACE) the plan does not split K.
- * Requirements: M, N >= 1; 32 <= K <= 2^23; M * ceil(K/128) and
- * N * ceil(K/128) < 2^29; c 2-byte (8-byte if N % 4 == 0), codes 16-byte,
- * scales 4-byte aligned.  Deterministic.
+ * Requirements: M, N >= 1; M * N <= 2^44; 32 <= K <= 2^23; M * ceil(K/128) and
+ * N * ceil(K/128) < 2^29; c and codes 16-byte, scales 4-byte aligned.  Deterministic.
  */
 size_t dg_mxfp4_gemm_nt_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int dg_mxfp4_gemm_nt(uint16_t *c, const uint8_t *a, const uint8_t *b, const int32_t *sfa,
