@@ -9,7 +9,6 @@
 // arrive adds the parts in order, so the result does not depend on which one
 // that is.
 #include "mxfp4_device.hpp"
-#include <stdlib.h>
 
 namespace dg {
 namespace {
@@ -52,7 +51,7 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_mxfp4_stream_kernel(Mxfp4Arg
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15;
-  const int tile_n = blockIdx.x / p.S;
+  const int tile_n = (int)(blockIdx.x / (unsigned)p.S);
   const int split = blockIdx.x - tile_n * p.S;
   const int64_t n0 = (int64_t)tile_n * (16 * NF);
   const int rows_b = (int)(p.N - n0 < 16 * NF ? p.N - n0 : 16 * NF);
@@ -64,6 +63,7 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_mxfp4_stream_kernel(Mxfp4Arg
   o.b = buffer_of(p.b + n0 * ldb, rows_b * ldb);
   o.sb = buffer_of(p.sfb + n0, (nkb * p.N - n0) * 4);
   o.sb_step = (uint32_t)p.N * 4;
+  o.last = nkb - 1;
   o.a = buffer_of(p.a, rows_a * lda);
   if (AF == ACT_MXFP4) {
     o.sa = buffer_of(p.sfa, nkb * p.M * 4);
@@ -84,8 +84,7 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_mxfp4_stream_kernel(Mxfp4Arg
     s.vsa[i] = r < rows_a ? (uint32_t)(4 * r) : kOob;
   }
   const int parts = p.S * kWaves, part = split * kWaves + wave;
-  const int kb0 = (int)((int64_t)part * nkb / parts);
-  const int kb1 = (int)((int64_t)(part + 1) * nkb / parts);
+  const int kb0 = run_begin(part, nkb, parts), kb1 = run_begin(part + 1, nkb, parts);
   const int kmax = kb1 * 128 < p.K ? kb1 * 128 : (int)p.K;
 
   v4f acc[NF][NI];
@@ -121,83 +120,122 @@ __global__ void __launch_bounds__(64 * kWaves) gemm_mxfp4_stream_kernel(Mxfp4Arg
   for (int q = wave; q < Q; q += kWaves)
     publish4(part0 + split * (Q * 256) + (q * 64 + lane) * 4, sum_waves(q));
   if (!arrive_last(&p.counters[tile], p.S, &s_last)) return;
-  for (int q = wave; q < Q; q += kWaves) {
-    v4f t = collect4(part0 + (q * 64 + lane) * 4);
-    for (int sp = 1; sp < p.S; ++sp) t += collect4(part0 + sp * (Q * 256) + (q * 64 + lane) * 4);
-    store(q, t);
+  v4f t[(Q + kWaves - 1) / kWaves];
+#pragma unroll
+  for (int u = 0; u < (Q + kWaves - 1) / kWaves; ++u) {
+    const int q = wave + u * kWaves;
+    if (q < Q) t[u] = collect_sum(part0 + (q * 64 + lane) * 4, Q * 256, p.S);
+  }
+#pragma unroll
+  for (int u = 0; u < (Q + kWaves - 1) / kWaves; ++u) {
+    const int q = wave + u * kWaves;
+    if (q < Q) store(q, t[u]);
   }
   if (threadIdx.x == 0)  // zero again for the next call
     __hip_atomic_store(&p.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The same with the activations in LDS (Shared, mxfp4_device.hpp): 128 rows of
-// B a workgroup, eight waves.
-template <int AF, int NI, int KS>
-__global__ void __launch_bounds__(kSharedThreads) gemm_mxfp4_shared_kernel(Mxfp4Args p) {
-  constexpr int NF = 4, QT = 2 * NF * NI;
-  typedef Shared<AF, FMT_MXFP4, NI, NF, KS> S;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+// BF16 activations in LDS (Shared, mxfp4_device.hpp): 128 rows of B a
+// workgroup, eight waves.
+template <int NI>
+using SharedProduct = Shared<FMT_MXFP4, NI, shared_depth(FMT_MXFP4, NI)>;
+
+template <int NI>
+__global__ void __launch_bounds__(kSharedThreads, (SharedProduct<NI>::WAVES))
+gemm_mxfp4_shared_kernel(Mxfp4Args p) {
+  typedef SharedProduct<NI> S;
+  constexpr int QT = S::ROWS_B / 16 * NI;
+  DG_SHARED_SLOTS(S);
   __shared__ int s_last;
-  const int tile = blockIdx.x / p.S;
+  const int tile = (int)(blockIdx.x / (unsigned)p.S);
   const int split = blockIdx.x - tile * p.S;
-  const int64_t n0 = (int64_t)tile * (32 * NF);
-  const int rows_b = (int)(p.N - n0 < 32 * NF ? p.N - n0 : 32 * NF);
+  const int64_t n0 = (int64_t)tile * S::ROWS_B;
+  const int rows_b = (int)(p.N - n0 < S::ROWS_B ? p.N - n0 : S::ROWS_B);
   const int rows_a = (int)p.M;
-  const int64_t ldb = p.K / 2, lda = AF == ACT_BF16 ? p.K * 2 : p.K / 2;
+  const int64_t ldb = p.K / 2, lda = p.K * 2;
   const int nkb = (int)((p.K + 127) / 128);
   StreamOperands o;
   o.b = buffer_of(p.b + n0 * ldb, rows_b * ldb);
   o.sb = buffer_of(p.sfb + n0, (nkb * p.N - n0) * 4);
   o.sb_step = (uint32_t)p.N * 4;
+  o.last = nkb - 1;
   o.a = buffer_of(p.a, rows_a * lda);
-  if (AF == ACT_MXFP4) {
-    o.sa = buffer_of(p.sfa, nkb * p.M * 4);
-    o.sa_step = (uint32_t)p.M * 4;
-  }
   S s;
   s.init(ldb, rows_b, lda, [&](int r) { return r < rows_a ? r : -1; });
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  auto store = [&](int q, v4f t) {
-    const int f = q / NI, i = q - f * NI;
+  auto store = [&](int f, int i, v4f t) {
     const int64_t m = 16 * i + (lane & 15);
     if (m < p.M) store_quad(p.c, m, n0 + 16 * f + 4 * (lane >> 4), p.N, t);
   };
   float* part0 = p.partials + (int64_t)tile * p.S * (QT * 256);
-  s.run(o, p.K, split * S::WK, p.S * S::WK, lds, [&](int f, int i, v4f t) {
-    const int q = f * NI + i;
-    if (p.S == 1) store(q, t);
-    else publish4(part0 + split * (QT * 256) + (q * 64 + lane) * 4, t);
+  s.run(o, p.K, split * S::WK, p.S * S::WK, slots, [&](int f, int i, v4f t) {
+    if (p.S == 1) store(f, i, t);
+    else publish4(part0 + split * (QT * 256) + ((f * NI + i) * 64 + lane) * 4, t);
   });
   if (p.S == 1) return;
   if (!arrive_last(&p.counters[tile], p.S, &s_last)) return;
-  for (int q = wave; q < QT; q += 8) {
-    v4f t = collect4(part0 + (q * 64 + lane) * 4);
-    for (int sp = 1; sp < p.S; ++sp) t += collect4(part0 + sp * (QT * 256) + (q * 64 + lane) * 4);
-    store(q, t);
+  // this wave's quads of all parts, four parts in flight
+  v4f t[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) t[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  const float* mine = part0 + (wave * NI * 64 + lane) * 4;
+  for (int sp = 0; sp < p.S; sp += 4) {
+    v4f v[4][NI];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        v[u][i] = collect4(mine + (sp + u < p.S ? sp + u : sp) * (QT * 256) + i * 256);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (sp + u < p.S) t[i] += v[u][i];
   }
+#pragma unroll
+  for (int i = 0; i < NI; ++i) store(wave, i, t[i]);
   if (threadIdx.x == 0)
     __hip_atomic_store(&p.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Rows of A per workgroup, rows of B per workgroup and K parts of the stream
-// kernel for a shape.
+// Kernel, rows of A and B per workgroup and K parts for a shape.
 struct StreamPlan {
-  int ni, nf, S, u;
+  bool shared;
+  int ni, nf, S, u;  // S parts of K
   int64_t tiles_n;
 };
 
-int envi(const char* n, int d) { const char* e = getenv(n); return e ? atoi(e) : d; }
-
+// Measured on an MI355X, us with the weights from HBM (M x N x K):
+//  * BF16 activations in LDS from 17 rows on, where N gives workgroups enough:
+//    28 against 44 (33 x 7168 x 16384), 10.2 / 13.6 (20 x 24576 x 1536), 14 /
+//    26 (64 x 24576 x 1536); up to 16 rows straight into fragments: 18.7 / 44
+//    (1 x 7168 x 16384), 5.5 / 7.6 (16 x 7168 x 2048), and for few columns
+//    10.2 / 15 (64 x 512 x 8192).  MXFP4 activations are a quarter of the
+//    bytes and gain nothing from LDS (25 both ways, 33 x 7168 x 16384).
+//  * 32 rows of B a workgroup where that leaves 192 workgroups, else 16: 24.9
+//    / 33 (33 x 7168 x 16384, MXFP4), but 5.2 / 4.4 (8 x 4096 x 4096).
+//  * Two K blocks a buffer for long runs of few rows: 15.6 / 18.8 (1 x 7168 x
+//    16384, MXFP4); 13.6 / 12.7 on short ones (64 x 24576 x 1536).
+//  * K parts cost about 4 us, so they have to save more: 7.3 / 11.9 in four
+//    (64 x 512 x 8192, MXFP4); with LDS 28 / 62 in four (33 x 7168 x 16384),
+//    but 28 / 14 in two (64 x 24576 x 1536: 192 workgroups already).
 StreamPlan stream_plan(int64_t M, int64_t N, int64_t K, bool bf16_a) {
   StreamPlan s;
-  s.ni = M <= 16 ? 1 : (M <= 32 ? 2 : (M <= 48 ? 3 : 4));
-  s.nf = envi("DG_NF", 1);
-  s.u = envi("DG_U", 1);
-  s.tiles_n = (N + 16 * s.nf - 1) / (16 * s.nf);
+  const int64_t nkb = (K + 127) / 128;
+  s.ni = (int)((M + 15) / 16);
+  s.shared = bf16_a && M > 16 && N >= 2048;
   s.S = 1;
-  const int64_t tiles = s.tiles_n, nkb = (K + 127) / 128;
-  while (tiles * s.S < 512 && tiles <= kMaxCounters && nkb / (2 * s.S) >= 16 && s.S < 16) s.S *= 2;
-  s.S = envi("DG_S", s.S);
+  if (s.shared) {
+    s.nf = 8;
+    s.u = 1;
+    s.tiles_n = (N + 127) / 128;
+    while (s.tiles_n * 2 * s.S <= 256 && nkb / (4 * s.S) >= 4 && s.S < 16) s.S *= 2;
+    return s;
+  }
+  s.nf = (N + 31) / 32 >= 192 ? 2 : 1;
+  s.u = s.nf == 2 && s.ni == 1 && nkb >= 64 ? 2 : 1;
+  s.tiles_n = (N + 16 * s.nf - 1) / (16 * s.nf);
+  while (s.tiles_n * s.S < 256 && nkb / (kWaves * s.S) >= 8 && s.S < 16) s.S *= 2;
   return s;
 }
 
@@ -207,34 +245,30 @@ hipError_t launch_stream(const Mxfp4Args& p, const StreamPlan& s, hipStream_t st
                      dim3(64 * kWaves), 0, stream, p);
   return hipGetLastError();
 }
-template <int AF, int NI, int NF>
-hipError_t launch_u(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
-  if (s.u == 1) return launch_stream<AF, NI, NF, 1>(p, s, stream);
-  if (s.u == 2) return launch_stream<AF, NI, NF, 2>(p, s, stream);
-  return launch_stream<AF, NI, NF, 4>(p, s, stream);
-}
-template <int AF, int NI, int KS>
-hipError_t launch_sh(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
-  hipLaunchKernelGGL((gemm_mxfp4_shared_kernel<AF, NI, KS>), dim3((unsigned)(s.tiles_n * p.S)),
+template <int NI>
+hipError_t launch_shared(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
+  hipLaunchKernelGGL((gemm_mxfp4_shared_kernel<NI>), dim3((unsigned)(s.tiles_n * p.S)),
                      dim3(kSharedThreads), 0, stream, p);
   return hipGetLastError();
 }
 template <int AF, int NI>
-hipError_t launch_nf(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
-  if (s.nf == 8) {
-    if (s.u == 1 && AF == ACT_BF16) return launch_sh<AF, NI, AF == ACT_BF16 ? 1 : 2>(p, s, stream);
-    return launch_sh<AF, NI, (AF == ACT_BF16 && NI > 2) ? 1 : 2>(p, s, stream);
+hipError_t launch_rows(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
+  if constexpr (AF == ACT_BF16 && NI > 1) {
+    if (s.shared) return launch_shared<NI>(p, s, stream);
+    return launch_stream<AF, NI, 1, 1>(p, s, stream);
+  } else {
+    if constexpr (NI == 1)
+      if (s.u == 2) return launch_stream<AF, NI, 2, 2>(p, s, stream);
+    if (s.nf == 2) return launch_stream<AF, NI, 2, 1>(p, s, stream);
+    return launch_stream<AF, NI, 1, 1>(p, s, stream);
   }
-  if (s.nf == 1) return launch_u<AF, NI, 1>(p, s, stream);
-  if (s.nf == 2) return launch_u<AF, NI, 2>(p, s, stream);
-  return launch_u<AF, NI, 4>(p, s, stream);
 }
 template <int AF>
 hipError_t launch_ni(const Mxfp4Args& p, const StreamPlan& s, hipStream_t stream) {
-  if (s.ni == 1) return launch_nf<AF, 1>(p, s, stream);
-  if (s.ni == 2) return launch_nf<AF, 2>(p, s, stream);
-  if (s.ni == 3) return launch_nf<AF, 3>(p, s, stream);
-  return launch_nf<AF, 4>(p, s, stream);
+  if (s.ni == 1) return launch_rows<AF, 1>(p, s, stream);
+  if (s.ni == 2) return launch_rows<AF, 2>(p, s, stream);
+  if (s.ni == 3) return launch_rows<AF, 3>(p, s, stream);
+  return launch_rows<AF, 4>(p, s, stream);
 }
 
 size_t plan_bytes(const StreamPlan& s) {

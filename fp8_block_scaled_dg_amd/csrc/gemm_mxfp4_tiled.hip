@@ -77,10 +77,10 @@ struct Panel {
       off[j] = row < n ? (uint32_t)(row * ld + (((lane & 7) ^ lds_swz(lr)) * 16)) : kOob;
     }
   }
-  __device__ __forceinline__ void issue(uint8_t* lds, int wave, int j, int kb, bool in) const {
+  __device__ __forceinline__ void issue(uint8_t* lds, int wave, int j, int soff, bool in) const {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         r, (__attribute__((address_space(3))) void*)(lds + (j * NW + wave) * 1024), 16,
-        (int)(in ? off[j] : kOob), kb * 128, 0, 0);
+        (int)(in ? off[j] : kOob), soff, 0, 0);
   }
 };
 
@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_mxfp4_tile_kernel(TileArgs 
     const int kn = kb + 1;
     const bool in = kn * 256 + chunk_k < p.K;
     load_scales(sn, kn);
+    const int ko = kn < nk ? kn * 128 : 0;  // no scalar offset past a resource
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // exponent bytes of this lane's 32-block; 0 past K, where the codes are 0
@@ -188,9 +189,9 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_mxfp4_tile_kernel(TileArgs 
         if (h == 0 && (t & 1) == 1 && (t >> 1) < IA + IB) {
           const int q = t >> 1;
           if (q < IA)
-            pa.issue(nxt, wave, q, kn, in);
+            pa.issue(nxt, wave, q, ko, in);
           else
-            pb.issue(nxt + A_BYTES, wave, q - IA, kn, in);
+            pb.issue(nxt + A_BYTES, wave, q - IA, ko, in);
           __builtin_amdgcn_sched_barrier(0);
         }
       }

@@ -12,7 +12,6 @@
 // routing weight in its epilogue, and down, whose last workgroup per column
 // tile adds the k slots of each token in slot order.
 #include "mxfp4_device.hpp"
-#include <stdlib.h>
 
 namespace dg {
 namespace {
@@ -48,17 +47,20 @@ struct MoeArgs {
   float* part;     // [T k][H]
 };
 
-// max over the wave, with the lowest index among equal values
-__device__ __forceinline__ void wave_argmax(float& v, int& i) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const float ov = __shfl_xor(v, off, 64);
-    const int oi = __shfl_xor(i, off, 64);
-    if (ov > v || (ov == v && oi < i)) {
-      v = ov;
-      i = oi;
-    }
-  }
+// Largest value of the wave, in every lane (no NaN among them).
+__device__ __forceinline__ float wave_max(float v) {
+  auto join = [](float x, int y) { return fmaxf(x, __int_as_float(y)); };
+  const auto dpp = [](float x, auto ctrl) {
+    return __builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, false);
+  };
+  v = join(v, dpp(v, IntTag<0xB1>{}));   // within 4 lanes
+  v = join(v, dpp(v, IntTag<0x4E>{}));
+  v = join(v, dpp(v, IntTag<0x124>{}));  // within 16
+  v = join(v, dpp(v, IntTag<0x128>{}));
+  const int b = __float_as_int(v);
+  const float lo = join(__int_as_float(__builtin_amdgcn_readlane(b, 0)), __builtin_amdgcn_readlane(b, 16));
+  const float hi = join(__int_as_float(__builtin_amdgcn_readlane(b, 32)), __builtin_amdgcn_readlane(b, 48));
+  return fmaxf(lo, hi);
 }
 
 // Score of v relative to the largest chosen logit m: softmax e^(v - m),
@@ -69,41 +71,44 @@ __device__ __forceinline__ float relative_score(float v, float m, int scoring) {
   return expf(fminf(v, 0.0f) - fminf(m, 0.0f)) * ((1.0f + expf(-fabsf(m))) / (1.0f + expf(-fabsf(v))));
 }
 
-// One workgroup.  A wave takes a token: k rounds of argmax over its logits
-// (16 per lane at most, kMoeMaxExperts = 1024).  A logit of -inf or NaN is an
-// expert that cannot be chosen; slots left over get id -1 and weight 0.
+// One wave, one token: k rounds of the largest logit, PER consecutive experts
+// a lane, so that the lowest lane of the lanes that hold it has the lowest
+// index.  A logit of -inf or NaN is an expert that cannot be chosen; slots left
+// over get id -1 and weight 0.
 template <int PER>
 __device__ __forceinline__ void route_token(const MoeArgs& p, int t, int lane, int* s_ids) {
   float v[PER];
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
-    const int e = lane + 64 * q;
+    const int e = lane * PER + q;
     v[q] = e < p.E ? p.logits[(int64_t)t * p.E + e] : -INFINITY;
     if (v[q] != v[q]) v[q] = -INFINITY;
   }
   float m = 0.0f, sum = 0.0f, mine = 0.0f;
   int my_id = -1;
   for (int j = 0; j < p.k; ++j) {
-    float b = -INFINITY;
-    int bi = 0x7FFFFFFF;
+    float b = v[0];
+    int bi = 0;
 #pragma unroll
-    for (int q = 0; q < PER; ++q)
+    for (int q = 1; q < PER; ++q)
       if (v[q] > b) {
         b = v[q];
-        bi = lane + 64 * q;
+        bi = q;
       }
-    wave_argmax(b, bi);
-    if (b == -INFINITY) break;  // wave-uniform
-    if (j == 0) m = b;
-    const float r = relative_score(b, m, p.scoring);
+    const float top = wave_max(b);
+    if (top == -INFINITY) break;  // wave-uniform
+    const int owner = __ffsll((unsigned long long)__ballot(b == top)) - 1;
+    const int id = owner * PER + __builtin_amdgcn_readlane(bi, owner);
+    if (j == 0) m = top;
+    const float r = relative_score(top, m, p.scoring);
     sum += r;
     if (lane == j) {
       mine = r;
-      my_id = bi;
+      my_id = id;
     }
 #pragma unroll
     for (int q = 0; q < PER; ++q)
-      if (bi == lane + 64 * q) v[q] = -INFINITY;
+      if (id == lane * PER + q) v[q] = -INFINITY;
   }
   if (lane < p.k) {
     s_ids[t * p.k + lane] = my_id;
@@ -112,41 +117,60 @@ __device__ __forceinline__ void route_token(const MoeArgs& p, int t, int lane, i
   }
 }
 
+// One workgroup: a wave takes a token at a time, then every expert gets its
+// list of pairs.  The order within a list is the order of arrival at a counter
+// in LDS; it decides which row of a tile a pair takes, not its result.
 __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(MoeArgs p) {
+  constexpr int W = kRouterThreads / 64;
+  static_assert(kRouterThreads >= kMoeMaxExperts && kRouterThreads >= kMoeMaxPairs, "one each");
   __shared__ int s_ids[kMoeMaxPairs];
-  __shared__ int s_cnt[kMoeMaxExperts], s_active;
+  __shared__ int s_cnt[kRouterThreads], s_off[kRouterThreads], s_sum[W], s_active[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = p.T * p.k;
+  s_cnt[tid] = 0;
   if (p.logits) {
-    for (int t = wave; t < p.T; t += kRouterThreads / 64) {
+    for (int t = wave; t < p.T; t += W) {
       if (p.E <= 64) route_token<1>(p, t, lane, s_ids);
       else if (p.E <= 256) route_token<4>(p, t, lane, s_ids);
       else route_token<16>(p, t, lane, s_ids);
     }
-  } else {
-    for (int q = tid; q < n; q += kRouterThreads) {
-      const int id = p.ids[q];  // the caller's: an id outside [0, E) is no expert
-      s_ids[q] = id >= 0 && id < p.E ? id : -1;
-    }
-  }
-  if (tid == 0) s_active = 0;
-  __syncthreads();
-  if (tid < p.E) {
-    int c = 0;
-    for (int q = 0; q < n; ++q) c += s_ids[q] == tid;
-    s_cnt[tid] = c;
-    if (c) atomicAdd(&s_active, 1);
+  } else if (tid < n) {
+    const int id = p.ids[tid];  // the caller's: an id outside [0, E) is no expert
+    s_ids[tid] = id >= 0 && id < p.E ? id : -1;
   }
   __syncthreads();
-  if (tid < p.E) {
-    int off = 0;
-    for (int e = 0; e < tid; ++e) off += s_cnt[e];
-    p.tb.counts[tid] = s_cnt[tid];
-    p.tb.offsets[tid] = off;
-    for (int q = 0; q < n; ++q)
-      if (s_ids[q] == tid) p.tb.pairs[off++] = q;
+  const int id = tid < n ? s_ids[tid] : -1;
+  const int rank = id >= 0 ? atomicAdd(&s_cnt[id], 1) : 0;
+  __syncthreads();
+  // offsets: running sum of the counts over the wave, then over the waves
+  const int count = s_cnt[tid];
+  int sum = count;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(sum, d, 64);
+    if (lane >= d) sum += o;
   }
-  if (tid == 0) *p.tb.active = s_active;
+  const int used = __popcll(__ballot(count > 0));
+  if (lane == 63) {
+    s_sum[wave] = sum;
+    s_active[wave] = used;
+  }
+  __syncthreads();
+  int before = 0, active = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < wave) before += s_sum[w];
+    active += s_active[w];
+  }
+  const int offset = before + sum - count;
+  s_off[tid] = offset;
+  if (tid < p.E) {
+    p.tb.counts[tid] = count;
+    p.tb.offsets[tid] = offset;
+  }
+  if (tid == 0) *p.tb.active = active;
+  __syncthreads();
+  if (id >= 0) p.tb.pairs[s_off[id] + rank] = tid;
 }
 
 // f(IntTag<NI>) for the 16-row fragments that `rows` rows need, at most MAXNI
@@ -160,20 +184,15 @@ __device__ __forceinline__ void with_fragments(int rows, F&& f) {
   }
 }
 
-// Sums over the four waves of one tile of 16 NF weight rows by 16 NI
-// activation rows; finish(f, i, quad) is called for every fragment by the
-// wave that owns it.
-template <int BF, int NI, int NF, int U, class Rows, class Finish>
-__device__ __forceinline__ void expert_tile(const uint8_t* w, const void* scales, int64_t N,
-                                            int64_t K, int64_t n0, const void* act,
-                                            int64_t act_bytes, Rows&& row_of, v4f* red,
-                                            Finish&& finish) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int fr = lane & 15;
+// Operands of one expert's weight rows n0 .. n0 + 16 NF - 1 with activations
+// [..][K] in BF16.
+template <int BF>
+__device__ __forceinline__ StreamOperands expert_operands(const uint8_t* w, const void* scales,
+                                                          int64_t N, int64_t K, int64_t n0,
+                                                          int rows_b, const void* act,
+                                                          int64_t act_bytes) {
   const int nkb = (int)((K + 127) / 128);
   const int64_t ldb = BF == FMT_FP8 ? K : K / 2;
-  const int rows_b = (int)(N - n0 < 16 * NF ? N - n0 : 16 * NF);
   StreamOperands o;
   o.b = buffer_of(w + n0 * ldb, rows_b * ldb);
   if (BF == FMT_FP8) {
@@ -185,46 +204,89 @@ __device__ __forceinline__ void expert_tile(const uint8_t* w, const void* scales
     o.sb_step = (uint32_t)N * 4;
   }
   o.a = buffer_of(act, act_bytes);
-  Stream<ACT_BF16, BF, NI, NF, U> s;
-  s.g = lane >> 4;
-#pragma unroll
-  for (int f = 0; f < NF; ++f) {
-    const int r = 16 * f + fr;
-    s.vb[f] = r < rows_b ? (uint32_t)(r * ldb + (BF == FMT_FP8 ? 32 : 16) * s.g) : kOob;
-    s.vsb[f] = r < rows_b ? (uint32_t)(4 * r) : kOob;
-  }
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int r = row_of(16 * i + fr);  // row of the activations, -1: none
-    s.va[i] = r >= 0 ? (uint32_t)(r * (K * 2) + 64 * s.g) : kOob;
-  }
-  const int kb0 = wave * nkb / kWaves, kb1 = (wave + 1) * nkb / kWaves;
-  const int kmax = kb1 * 128 < K ? kb1 * 128 : (int)K;
-  v4f acc[NF][NI];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < NI; ++i) acc[f][i] = v4f{0.f, 0.f, 0.f, 0.f};
-  s.run(o, kb0, kb1, kmax, acc);
-  constexpr int Q = NF * NI;
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < NI; ++i) red[(wave * Q + f * NI + i) * 64 + lane] = acc[f][i];
-  __syncthreads();
-  for (int q = wave; q < Q; q += kWaves) {
-    v4f t = red[q * 64 + lane];
-#pragma unroll
-    for (int v = 1; v < kWaves; ++v) t += red[(v * Q + q) * 64 + lane];
-    finish(q / NI, q % NI, t);
-  }
-  __syncthreads();  // red is free again
+  o.last = nkb - 1;
+  return o;
 }
 
+// One tile of weight rows by 16 NI activation rows: finish(f, i, quad) is
+// called for every fragment, by one wave.
+//
+// Few rows (ENGINE_STREAM): four waves with a quarter of K each and the same
+// 16 NF weight rows, activations straight into fragments.
+template <int BF, int NF_>
+struct StreamEngine {
+  static constexpr int NF = NF_, ROWS_B = 16 * NF, THREADS = 64 * kWaves, WAVES = 1;
+  template <int NI, class Rows, class Finish>
+  static __device__ __forceinline__ void tile(const StreamOperands& o, int64_t K, int rows_b, Rows&& row_of, uint8_t* const (&slots)[kSharedMaxDepth],
+                                              Finish&& finish) {
+    v4f* red = reinterpret_cast<v4f*>(slots[0]);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15;
+    const int nkb = o.last + 1;
+    const int64_t ldb = BF == FMT_FP8 ? K : K / 2;
+    Stream<ACT_BF16, BF, NI, NF, 1> s;
+    s.g = lane >> 4;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const int r = 16 * f + fr;
+      s.vb[f] = r < rows_b ? (uint32_t)(r * ldb + (BF == FMT_FP8 ? 32 : 16) * s.g) : kOob;
+      s.vsb[f] = r < rows_b ? (uint32_t)(4 * r) : kOob;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = row_of(16 * i + fr);  // row of the activations, -1: none
+      s.va[i] = r >= 0 ? (uint32_t)(r * (K * 2) + 64 * s.g) : kOob;
+    }
+    const int kb0 = run_begin(wave, nkb, kWaves), kb1 = run_begin(wave + 1, nkb, kWaves);
+    const int kmax = kb1 * 128 < K ? kb1 * 128 : (int)K;
+    v4f acc[NF][NI];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) acc[f][i] = v4f{0.f, 0.f, 0.f, 0.f};
+    s.run(o, kb0, kb1, kmax, acc);
+    constexpr int Q = NF * NI;
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) red[(wave * Q + f * NI + i) * 64 + lane] = acc[f][i];
+    __syncthreads();
+    for (int q = wave; q < Q; q += kWaves) {
+      v4f t = red[q * 64 + lane];
+#pragma unroll
+      for (int v = 1; v < kWaves; ++v) t += red[(v * Q + q) * 64 + lane];
+      finish(q / NI, q % NI, t);
+    }
+    __syncthreads();  // red is free again
+  }
+  static constexpr int R = 1, SLOT = 16, SLOT0 = kWaves * NF * 1024;
+};
+
+// More rows: activations in LDS (Shared, mxfp4_device.hpp).
+template <int BF, int MAXNI>
+struct SharedEngine {
+  static constexpr int R = shared_depth(BF, MAXNI);
+  typedef Shared<BF, MAXNI, R> Largest;
+  static constexpr int ROWS_B = Largest::ROWS_B, NF = ROWS_B / 16, THREADS = kSharedThreads;
+  static constexpr int SLOT0 = Largest::SLOT0, SLOT = Largest::SLOT;
+  static constexpr int WAVES = Largest::WAVES;
+  template <int NI, class Rows, class Finish>
+  static __device__ __forceinline__ void tile(const StreamOperands& o, int64_t K, int rows_b,
+                                              Rows&& row_of,
+                                              uint8_t* const (&slots)[kSharedMaxDepth],
+                                              Finish&& finish) {
+    Shared<BF, NI, R> s;
+    s.init(BF == FMT_FP8 ? K : K / 2, rows_b, K * 2, row_of);
+    s.run(o, K, 0, s.WK, slots, finish);
+  }
+};
+
 // gate/up: rows 2i and 2i + 1 of W13 give gate and up of hidden unit i
-template <int BF, int MAXNI, int NF, int U>
-__global__ void __launch_bounds__(64 * kWaves) moe_up_kernel(MoeArgs p) {
-  __shared__ v4f red[kWaves * NF * MAXNI * 64];
+template <int BF, int MAXNI, class Engine>
+__global__ void __launch_bounds__(Engine::THREADS, Engine::WAVES) moe_up_kernel(MoeArgs p) {
+  constexpr int NF = Engine::NF;
+  DG_SHARED_SLOTS(Engine);
   const int e = blockIdx.y;
   const int count = p.tb.counts[e];
   if (count == 0) return;
@@ -234,12 +296,13 @@ __global__ void __launch_bounds__(64 * kWaves) moe_up_kernel(MoeArgs p) {
   const int64_t sstep = BF == FMT_FP8 ? (K / 128) * ((N + 127) / 128) : ((K + 127) / 128) * N;
   const uint8_t* w = p.w13 + (int64_t)e * N * (BF == FMT_FP8 ? K : K / 2);
   const void* sc = static_cast<const uint32_t*>(p.s13) + e * sstep;
+  const int rows_b = (int)(N - n0 < 16 * NF ? N - n0 : 16 * NF);
+  const StreamOperands o = expert_operands<BF>(w, sc, N, K, n0, rows_b, p.x, p.T * K * 2);
   for (int c0 = 0; c0 < count; c0 += 16 * MAXNI) {
     const int rows = count - c0 < 16 * MAXNI ? count - c0 : 16 * MAXNI;
     with_fragments<MAXNI>(rows, [&](auto ni) {
-      expert_tile<BF, decltype(ni)::value, NF, U>(
-          w, sc, N, K, n0, p.x, p.T * K * 2,
-          [&](int r) { return r < rows ? list[c0 + r] / p.k : -1; }, red,
+      Engine::template tile<decltype(ni)::value>(
+          o, K, rows_b, [&](int r) { return r < rows ? list[c0 + r] / p.k : -1; }, slots,
           [&](int f, int i, v4f t) {
             const int r = 16 * i + fr;
             if (r >= rows) return;
@@ -254,9 +317,10 @@ __global__ void __launch_bounds__(64 * kWaves) moe_up_kernel(MoeArgs p) {
   }
 }
 
-template <int BF, int MAXNI, int NF, int U>
-__global__ void __launch_bounds__(64 * kWaves) moe_down_kernel(MoeArgs p) {
-  __shared__ v4f red[kWaves * NF * MAXNI * 64];
+template <int BF, int MAXNI, class Engine>
+__global__ void __launch_bounds__(Engine::THREADS, Engine::WAVES) moe_down_kernel(MoeArgs p) {
+  constexpr int NF = Engine::NF;
+  DG_SHARED_SLOTS(Engine);
   __shared__ int s_last;
   const int e = blockIdx.y;
   const int count = p.tb.counts[e];
@@ -265,7 +329,7 @@ __global__ void __launch_bounds__(64 * kWaves) moe_down_kernel(MoeArgs p) {
   const int64_t N = p.H, K = p.I, n0 = (int64_t)blockIdx.x * (16 * NF);
   if (active == 0) {  // no token chose anything: y = 0
     if (e == 0)
-      for (int q = threadIdx.x; q < p.T * 16 * NF; q += 64 * kWaves)
+      for (int q = threadIdx.x; q < p.T * 16 * NF; q += Engine::THREADS)
         if (n0 + q % (16 * NF) < N) p.y[q / (16 * NF) * N + n0 + q % (16 * NF)] = 0;
     return;
   }
@@ -274,12 +338,14 @@ __global__ void __launch_bounds__(64 * kWaves) moe_down_kernel(MoeArgs p) {
   const int64_t sstep = BF == FMT_FP8 ? (K / 128) * ((N + 127) / 128) : ((K + 127) / 128) * N;
   const uint8_t* w = p.w2 + (int64_t)e * N * (BF == FMT_FP8 ? K : K / 2);
   const void* sc = static_cast<const uint32_t*>(p.s2) + e * sstep;
+  const int rows_b = (int)(N - n0 < 16 * NF ? N - n0 : 16 * NF);
+  const StreamOperands o =
+      expert_operands<BF>(w, sc, N, K, n0, rows_b, p.h, (int64_t)p.T * p.k * K * 2);
   for (int c0 = 0; c0 < count; c0 += 16 * MAXNI) {
     const int rows = count - c0 < 16 * MAXNI ? count - c0 : 16 * MAXNI;
     with_fragments<MAXNI>(rows, [&](auto ni) {
-      expert_tile<BF, decltype(ni)::value, NF, U>(
-          w, sc, N, K, n0, p.h, (int64_t)p.T * p.k * K * 2,
-          [&](int r) { return r < rows ? list[c0 + r] : -1; }, red,
+      Engine::template tile<decltype(ni)::value>(
+          o, K, rows_b, [&](int r) { return r < rows ? list[c0 + r] : -1; }, slots,
           [&](int f, int i, v4f t) {
             const int r = 16 * i + fr;
             const int64_t n = n0 + 16 * f + 4 * (lane >> 4);
@@ -288,14 +354,24 @@ __global__ void __launch_bounds__(64 * kWaves) moe_down_kernel(MoeArgs p) {
     });
   }
   if (!arrive_last(&p.counters[blockIdx.x], active, &s_last)) return;
-  for (int q = threadIdx.x; q < p.T * 4 * NF; q += 64 * kWaves) {
+  for (int q = threadIdx.x; q < p.T * 4 * NF; q += Engine::THREADS) {
     const int t = q / (4 * NF);
     const int64_t n = n0 + 4 * (q % (4 * NF));
     if (n >= N) continue;
     v4f s = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < p.k; ++j) {
-      const int id = p.ids[t * p.k + j];
-      if (id >= 0 && id < p.E) s += collect4(p.part + (int64_t)(t * p.k + j) * N + n);
+    for (int j = 0; j < p.k; j += 4) {  // four slots in flight: they come from beyond the L2
+      v4f v[4];
+      bool on[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int slot = t * p.k + (j + u < p.k ? j + u : j);
+        const int id = p.ids[slot];
+        on[u] = j + u < p.k && id >= 0 && id < p.E;
+        v[u] = collect4(p.part + (int64_t)slot * N + n);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (on[u]) s += v[u];
     }
     *reinterpret_cast<uint2*>(p.y + t * N + n) =
         make_uint2(bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3]));
@@ -318,35 +394,44 @@ MoeLayout moe_layout(int T, int E, int k, int64_t H, int64_t I) {
   return l;
 }
 
-int envi(const char* n, int d) { const char* e = getenv(n); return e ? atoi(e) : d; }
 
-template <int BF, int MAXNI, int NF, int U>
+template <int BF, int MAXNI, class Engine>
 hipError_t launch_up(const MoeArgs& p, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_up_kernel<BF, MAXNI, NF, U>),
-                     dim3((unsigned)((2 * p.I + 16 * NF - 1) / (16 * NF)), (unsigned)p.E),
-                     dim3(64 * kWaves), 0, stream, p);
+  hipLaunchKernelGGL((moe_up_kernel<BF, MAXNI, Engine>),
+                     dim3((unsigned)((2 * p.I + Engine::ROWS_B - 1) / Engine::ROWS_B), (unsigned)p.E),
+                     dim3(Engine::THREADS), 0, stream, p);
   return hipGetLastError();
 }
-template <int BF, int MAXNI, int NF, int U>
+template <int BF, int MAXNI, class Engine>
 hipError_t launch_down(const MoeArgs& p, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_down_kernel<BF, MAXNI, NF, U>),
-                     dim3((unsigned)((p.H + 16 * NF - 1) / (16 * NF)), (unsigned)p.E),
-                     dim3(64 * kWaves), 0, stream, p);
+  hipLaunchKernelGGL((moe_down_kernel<BF, MAXNI, Engine>),
+                     dim3((unsigned)((p.H + Engine::ROWS_B - 1) / Engine::ROWS_B), (unsigned)p.E),
+                     dim3(Engine::THREADS), 0, stream, p);
   return hipGetLastError();
 }
 
-template <int BF, int MAXNI>
+template <int BF, int MAXNI, class Engine>
+hipError_t launch_both(const MoeArgs& p, hipStream_t stream) {
+  const hipError_t e = launch_up<BF, MAXNI, Engine>(p, stream);
+  return e != hipSuccess ? e : launch_down<BF, MAXNI, Engine>(p, stream);
+}
+
+// Measured on an MI355X, us a layer with the weights from HBM:
+//  * up to four tokens 32 weight rows a workgroup, up to 16 tokens 64, whose
+//    waves read their activations half as often: 66.6 against 75.8 (1 token, 8
+//    experts of 4096 x 11008, E4M3), 79.3 / 76.2 (13 tokens, 60 of 2048 x 1408);
+//  * more tokens: activations in LDS, 160 against 191 (64 tokens, 8 experts,
+//    MXFP4), 245 / 260 (E4M3);
+//  * 32 rows of an expert at a time leave two workgroups a CU (160 against 167
+//    with 64, same layer), but an expert with more rows reads its weights again:
+//    64 at a time where the mean is above 20.
+template <int BF>
 hipError_t launch_experts(const MoeArgs& p, hipStream_t stream) {
-  hipError_t e;
-  const int a = envi("DG_UP", 11), b = envi("DG_DN", 11);
-#define X(A, FN) switch (A) { case 11: e = FN<BF, MAXNI, 1, 1>(p, stream); break; \
-  case 12: e = FN<BF, MAXNI, 1, 2>(p, stream); break; case 14: e = FN<BF, MAXNI, 1, 4>(p, stream); break;\
-  case 21: e = FN<BF, MAXNI, 2, 1>(p, stream); break; case 22: e = FN<BF, MAXNI, 2, 2>(p, stream); break; \
-  case 41: e = FN<BF, MAXNI, 4, 1>(p, stream); break; default: e = FN<BF, MAXNI, 4, 2>(p, stream); }
-  X(a, launch_up)
-  if (e != hipSuccess) return e;
-  X(b, launch_down)
-  return e;
+  if (p.T <= 4) return launch_both<BF, 1, StreamEngine<BF, 2>>(p, stream);
+  if (p.T <= 16) return launch_both<BF, 1, StreamEngine<BF, 4>>(p, stream);
+  if (p.T <= 32 || p.T * p.k <= 20 * p.E)
+    return launch_both<BF, 2, SharedEngine<BF, 2>>(p, stream);
+  return launch_both<BF, 4, SharedEngine<BF, 4>>(p, stream);
 }
 
 }  // namespace
@@ -384,11 +469,8 @@ hipError_t launch_moe_layer(const MoeProblem& q, void* workspace, hipStream_t st
   hipLaunchKernelGGL(moe_router_kernel, dim3(1), dim3(kRouterThreads), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (q.T <= 16)
-    return q.format == FMT_FP8 ? launch_experts<FMT_FP8, 1>(p, stream)
-                               : launch_experts<FMT_MXFP4, 1>(p, stream);
-  return q.format == FMT_FP8 ? launch_experts<FMT_FP8, 4>(p, stream)
-                             : launch_experts<FMT_MXFP4, 4>(p, stream);
+  return q.format == FMT_FP8 ? launch_experts<FMT_FP8>(p, stream)
+                             : launch_experts<FMT_MXFP4>(p, stream);
 }
 
 }  // namespace dg

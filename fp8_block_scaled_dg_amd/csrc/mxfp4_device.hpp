@@ -31,36 +31,27 @@ __device__ __forceinline__ uint32_t load4(__amdgpu_buffer_rsrc_t r, uint32_t vof
   return __builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, (int)soff, 0);
 }
 
-// 32 E2M1 codes (16 bytes) times 2^(e - 127), e the low byte of `e`, as 4 x 8
-// BF16: exact (at most two significant bits) down to BF16's subnormals; e =
-// 255 gives NaN.  The conversion reads only the exponent field of its scale
-// operand, so the E8M0 byte goes there as it is (checked on an MI355X for all
-// 256 code pairs at scales 2^-127, 2^-126, 1, 2^127 and NaN).
-__device__ __forceinline__ void widen_mxfp4(v4i q, uint32_t e, dg_bf16x8 (&out)[4]) {
+// Eight E2M1 codes times 2^(e - 127), e the low byte of `e`, as BF16: exact
+// (at most two significant bits) down to BF16's subnormals; e = 255 gives NaN.
+// The conversion reads only the exponent field of its scale operand, so the
+// E8M0 byte goes there as it is (checked on an MI355X for all 256 code pairs
+// at scales 2^-127, 2^-126, 1, 2^127 and NaN).
+__device__ __forceinline__ dg_bf16x8 widen8_mxfp4(uint32_t w, uint32_t e) {
   const float s = __uint_as_float((e & 0xFFu) << 23);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t w = (uint32_t)q[j];
-    const dg_bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
-    const dg_bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
-    const dg_bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
-    const dg_bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
-    out[j] = dg_bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-  }
+  const dg_bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+  const dg_bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+  const dg_bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+  const dg_bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+  return dg_bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// 32 E4M3 codes (32 bytes) as 4 x 8 BF16: exact (four significant bits).
-__device__ __forceinline__ void widen_fp8(v4i lo, v4i hi, dg_bf16x8 (&out)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t w0 = (uint32_t)(j < 2 ? lo[2 * j] : hi[2 * j - 4]);
-    const uint32_t w1 = (uint32_t)(j < 2 ? lo[2 * j + 1] : hi[2 * j - 3]);
-    const dg_bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
-    const dg_bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
-    const dg_bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
-    const dg_bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
-    out[j] = dg_bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-  }
+// Eight E4M3 codes as BF16: exact (four significant bits).
+__device__ __forceinline__ dg_bf16x8 widen8_fp8(uint32_t w0, uint32_t w1) {
+  const dg_bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
+  const dg_bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
+  const dg_bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
+  const dg_bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+  return dg_bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
 // FP32 quads published to, and read from, the level that all XCDs share (each
@@ -81,6 +72,21 @@ __device__ __forceinline__ v4f collect4(const float* s) {
              __uint_as_float((uint32_t)hi), __uint_as_float((uint32_t)(hi >> 32))};
 }
 
+// Sum of the quads at s, s + step, ... (S of them), in that order.  They come
+// from beyond the L2, so four are asked for at a time.
+__device__ __forceinline__ v4f collect_sum(const float* s, int64_t step, int S) {
+  v4f t = {0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < S; p += 4) {
+    v4f v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = collect4(s + (p + u < S ? p + u : p) * step);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (p + u < S) t += v[u];
+  }
+  return t;
+}
+
 // True in the workgroup that arrives last of `count` at *counter (zero before
 // the first arrival; the caller resets it).  Every wave's stores are complete
 // before its workgroup arrives.
@@ -94,6 +100,11 @@ __device__ __forceinline__ bool arrive_last(int* counter, int count, int* s_last
   return *s_last != 0;
 }
 
+// First K block of part `part` of `parts` (nkb <= 2^16, parts <= 2^8).
+__device__ __forceinline__ int run_begin(int part, int nkb, int parts) {
+  return (int)((uint32_t)part * (uint32_t)nkb / (uint32_t)parts);
+}
+
 // What one wave multiplies: 16 NF rows of a weight matrix with 16 NI rows of
 // activations over a run of 128-wide K blocks.  Rows of the weight start at
 // resource b (row stride b_ld bytes), its scales at sb.
@@ -101,6 +112,8 @@ struct StreamOperands {
   __amdgpu_buffer_rsrc_t b, sb, a, sa;
   uint32_t sb_step;  // bytes between the scales of one K block and the next
   uint32_t sa_step;
+  int last;          // the last K block: blocks past it are addressed as it, with
+                     // every lane masked, so no scalar offset passes a resource
 };
 
 // Both operands go from memory straight into the matrix instruction's layout
@@ -129,7 +142,7 @@ struct Stream {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool in = (kb + u) * 128 + 32 * g < kmax;
-      const uint32_t k = (uint32_t)(kb + u);
+      const uint32_t k = (uint32_t)min(kb + u, o.last);
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
         const uint32_t v = in ? vb[f] : kOob;
@@ -169,10 +182,14 @@ struct Stream {
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
           dg_bf16x8 bw[4];
-          if constexpr (BF == FMT_FP8)
-            widen_fp8(x.b[u][f][0], x.b[u][f][1], bw);
-          else
-            widen_mxfp4(x.b[u][f][0], x.sb[u][f] >> sh, bw);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (BF == FMT_FP8)
+              bw[j] = widen8_fp8((uint32_t)x.b[u][f][j >> 1][2 * (j & 1)],
+                                 (uint32_t)x.b[u][f][j >> 1][2 * (j & 1) + 1]);
+            else
+              bw[j] = widen8_mxfp4((uint32_t)x.b[u][f][0][j], x.sb[u][f] >> sh);
+          }
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
             v4f t = BF == FMT_FP8 ? v4f{0.f, 0.f, 0.f, 0.f} : acc[f][i];
@@ -210,230 +227,216 @@ struct Stream {
   }
 };
 
-// Row r of the activations, 16-byte chunk c of its 256 (BF16) or 128 (MXFP4)
-// bytes in LDS: the slot that keeps both the fragment reads (lane 16g + r
-// reads chunk 4g + j, or 4h + g, of row r; served in the groups of lanes that
-// a 16-byte read has) and the row-wise writes off each other's banks.
-template <int AF>
-__device__ __forceinline__ int act_slot(int r, int c) {
-  if (AF == ACT_BF16) return c ^ ((r & 3) | ((r & 8) ? 12 : 0));
-  return c ^ ((r & 2) | ((r >> 1) & 4));
+// The same product with BF16 activations in LDS, for more than a few of their
+// rows.  A fragment load that goes straight to registers makes neighbouring
+// lanes read different rows, and activations in BF16 are 4 NI / NF times (E4M3
+// weights: 2 NI / NF) the weights' bytes.  By LDS DMA they come in full rows of
+// 256 bytes, once for the four waves that multiply them with 32 weight rows
+// each.
+//
+// Eight waves: WK = 2 runs of K, four waves of 16 NF weight rows in each.  A
+// stage is one K block of each run.  Stages are R deep, the weights' in
+// registers, the activations' in R LDS slots, so R - 1 are in flight while one
+// is multiplied; one barrier a stage tells that every wave's DMA of it has
+// landed and that the slot of the stage before is free.
+constexpr int kSharedThreads = 512;
+constexpr int kSharedMaxDepth = 6;
+
+// Depth for NI fragments of activation rows: what the slots leave room for in
+// LDS (two workgroups a CU up to NI = 2 and for E4M3 up to 3, else one) and in
+// registers.  Weight bytes in flight a stage and workgroup: 16 KB in 4 bits,
+// 32 KB in 8.
+constexpr int shared_depth(int bf, int ni) {
+  if (bf == FMT_FP8) return 3;
+  return ni == 1 ? 5 : (ni == 3 ? 6 : 4);
 }
 
-// The same product with the activations staged in LDS, for more than a few of
-// their rows: read straight into fragments they cost, per K block, NI / NF
-// times the weight's bytes and more requests than bytes (a fragment's 16 rows
-// are 16 pieces of 64 bytes).  Eight waves: WK = 4 runs of K, and in each run
-// two waves with 16 NF weight rows each, which share the run's activations.
-// A stage is KS K blocks.  Activations go memory -> registers -> LDS one stage
-// ahead of their use (full rows, 256 or 128 bytes each), weights straight into
-// registers one stage ahead.
-constexpr int kSharedThreads = 512;
-template <int AF, int BF, int NI, int NF, int KS>
+// LDS of a workgroup: every slot is a variable of its own, so that a read of
+// one is not taken to depend on a transfer into another.
+#define DG_SHARED_SLOTS(S)                                                              \
+  __shared__ __attribute__((aligned(1024))) uint8_t slot0[S::SLOT0];                    \
+  __shared__ __attribute__((aligned(1024))) uint8_t slot1[S::R > 1 ? S::SLOT : 16];     \
+  __shared__ __attribute__((aligned(1024))) uint8_t slot2[S::R > 2 ? S::SLOT : 16];     \
+  __shared__ __attribute__((aligned(1024))) uint8_t slot3[S::R > 3 ? S::SLOT : 16];     \
+  __shared__ __attribute__((aligned(1024))) uint8_t slot4[S::R > 4 ? S::SLOT : 16];     \
+  __shared__ __attribute__((aligned(1024))) uint8_t slot5[S::R > 5 ? S::SLOT : 16];     \
+  uint8_t* const slots[kSharedMaxDepth] = {slot0, slot1, slot2, slot3, slot4, slot5}
+
+template <int BF, int NI, int R_>
 struct Shared {
-  static constexpr int WK = 4, WN = 2, BV = BF == FMT_FP8 ? 2 : 1;
-  static constexpr int MP = 16 * NI;
-  static constexpr int ROW = AF == ACT_BF16 ? 256 : 128;        // bytes of an LDS row
-  static constexpr int TILES = AF == ACT_BF16 ? KS : KS / 2;    // LDS tiles of MP rows a stage
-  static constexpr int LPR = ROW / 16;                          // lanes per row
-  static constexpr int RPI = 64 * WN / LPR;                     // rows per load of the two waves
-  static constexpr int IT = (MP + RPI - 1) / RPI;
-  static constexpr int STAGE = TILES * MP * ROW;                // bytes of a run's stage
-  static constexpr int LDS = 2 * WK * STAGE > 8 * NF * NI * 1024 ? 2 * WK * STAGE
-                                                                  : 8 * NF * NI * 1024;
-  static_assert(AF == ACT_BF16 || KS % 2 == 0, "MXFP4 stages are pairs of K blocks");
-  struct B {
-    v4i b[KS][NF][BV];
-    uint32_t sb[KS][BF == FMT_FP8 ? 1 : NF];
-    uint32_t sa[KS][AF == ACT_BF16 ? 1 : NI];
+  static constexpr int R = R_;
+  static constexpr int WN = 4, WK = 2, NF = 2, BV = BF == FMT_FP8 ? 2 : 1;
+  static constexpr int ROWS_B = 16 * NF * WN;     // weight rows of a workgroup
+  static constexpr int ROW = 256;                 // bytes of an LDS row: a K block in BF16
+  static constexpr int IT = NI;                   // DMA instructions a wave and stage, 4 rows each
+  static constexpr int RUN = IT * WN * 1024;      // bytes of a run's stage
+  static constexpr int SLOT = WK * RUN, SLOT0 = SLOT;
+  static constexpr int SUMS = WK * WN * NI * 1024;  // the runs' sums meet in slot 0
+  static_assert(SUMS <= SLOT, "room for the sums");
+  static constexpr int WAVES = R * SLOT <= 79 << 10 ? 4 : 2;  // a SIMD's, as the LDS allows
+  static constexpr int LOADS = IT + NF * BV + (BF == FMT_FP8 ? 1 : NF);  // a wave's of a stage
+  struct W {
+    v4i b[NF][BV];
+    uint32_t sb[BF == FMT_FP8 ? 1 : NF];
   };
-  struct A {
-    v4i v[TILES][IT];
-  };
-  uint32_t vb[NF], vsb[NF], vsa[NI], va[IT];
-  int lane, wave, wk, wn, g;
+  uint32_t vb[NF], vsb[NF], va[IT];
+  int lane, wave, wk, wn, g, ck;
+
+  // A 16-byte LDS read is served 16 lanes at a time: lanes 0-3, 12-15 and
+  // 20-27, then the other 16 of the half wave.  These put the 16 rows of each
+  // such group on the 16 different 16-byte slots of a row, which is one sweep
+  // of the banks, when lane 16g + r reads chunk 4g + j (MXFP4 weights) or
+  // 8h + 2g + j (E4M3) of row r.
+  static __device__ __forceinline__ int swz(int r) {
+    if (BF == FMT_FP8) return r & 15;
+    return (r & 3) | ((r & 8) ? 12 : 0);
+  }
 
   // row_of(r): activation row of the tile's row r, or -1
   template <class Rows>
   __device__ __forceinline__ void init(int64_t ldb, int rows_b, int64_t lda, Rows&& row_of) {
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    wn = wave & 1;
-    wk = wave >> 1;
+    wn = wave % WN;
+    wk = wave / WN;
     g = lane >> 4;
     const int fr = lane & 15;
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
       const int r = 16 * (NF * wn + f) + fr;
-      vb[f] = r < rows_b ? (uint32_t)(r * ldb + 16 * BV * g) : kOob;
+      vb[f] = r < rows_b ? (uint32_t)(r * ldb + 16 * g) : kOob;
       vsb[f] = r < rows_b ? (uint32_t)(4 * r) : kOob;
     }
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int r = row_of(16 * i + fr);
-      vsa[i] = r >= 0 ? (uint32_t)(4 * r) : kOob;
-    }
-    const int t = wn * 64 + lane;
+    // DMA: 1 KB of consecutive LDS rows an instruction, the lane's chunk chosen
+    // by the row (rows of a wave's instructions agree modulo 16)
+    const int r0 = wn * 4 + (lane >> 4);
+    ck = (lane & 15) ^ swz(r0);
 #pragma unroll
     for (int j = 0; j < IT; ++j) {
-      const int r = j * RPI + t / LPR;
-      const int a = r < MP ? row_of(r) : -1;
-      va[j] = a >= 0 ? (uint32_t)(a * lda + 16 * (t % LPR)) : kOob;
+      const int a = row_of(16 * j + r0);
+      va[j] = a >= 0 ? (uint32_t)(a * lda + 16 * ck) : kOob;
     }
   }
 
-  __device__ __forceinline__ void load_b(const StreamOperands& o, B& x, int kb, int kmax) const {
+  __device__ __forceinline__ void load(const StreamOperands& o, uint8_t* slot, W& x, int kb,
+                                       int kmax) const {
+    const uint32_t k = (uint32_t)min(kb, o.last);
+    const bool in_a = kb * 128 + ck * 8 < kmax;
 #pragma unroll
-    for (int u = 0; u < KS; ++u) {
-      const bool in = (kb + u) * 128 + 32 * g < kmax;
-      const uint32_t k = (uint32_t)(kb + u);
+    for (int j = 0; j < IT; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          o.a, (__attribute__((address_space(3))) void*)(slot + wk * RUN + (j * WN + wn) * 1024), 16,
+          (int)(in_a ? va[j] : kOob), (int)(k * ROW), 0, 0);
+    // E4M3: a lane's two pieces of 16 are 64 apart, so that an instruction
+    // reads 64 bytes of each row
+    const bool in = kb * 128 + (BF == FMT_FP8 ? 16 : 32) * g < kmax;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+#pragma unroll
+      for (int h = 0; h < BV; ++h)
+        x.b[f][h] = load16(o.b, (in ? vb[f] : kOob) + 64 * h, k * (64 * BV));
+      if (BF == FMT_MXFP4) x.sb[f] = load4(o.sb, in ? vsb[f] : kOob, k * o.sb_step);
+    }
+    if (BF == FMT_FP8) x.sb[0] = load4(o.sb, in ? 0u : kOob, k * o.sb_step);
+  }
+
+  __device__ __forceinline__ v4i frag(const uint8_t* st, int i, int c) const {
+    const int fr = lane & 15;
+    return *reinterpret_cast<const v4i*>(st + (16 * i + fr) * ROW + 16 * (c ^ swz(fr)));
+  }
+  __device__ __forceinline__ void multiply(const W& x, const uint8_t* slot,
+                                           v4f (&acc)[NF][NI]) const {
+    const uint8_t* st = slot + wk * RUN;
+    const int sh = 8 * g;
+    // eight K values of a lane at a time, so that few widened weights and
+    // activations are live; E4M3 sums a block before its scale is applied
+    v4f t[NF][NI];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) t[f][i] = BF == FMT_FP8 ? v4f{0.f, 0.f, 0.f, 0.f} : acc[f][i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      dg_bf16x8 bw[NF];
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        const uint32_t v = in ? vb[f] : kOob;
-#pragma unroll
-        for (int h = 0; h < BV; ++h) x.b[u][f][h] = load16(o.b, v + 16 * h, k * (64 * BV));
-        if (BF == FMT_MXFP4) x.sb[u][f] = load4(o.sb, in ? vsb[f] : kOob, k * o.sb_step);
+        if constexpr (BF == FMT_FP8)
+          bw[f] = widen8_fp8((uint32_t)x.b[f][j >> 1][2 * (j & 1)],
+                             (uint32_t)x.b[f][j >> 1][2 * (j & 1) + 1]);
+        else
+          bw[f] = widen8_mxfp4((uint32_t)x.b[f][0][j], x.sb[f] >> sh);
       }
-      if (BF == FMT_FP8) x.sb[u][0] = load4(o.sb, in ? 0u : kOob, k * o.sb_step);
-      if (AF == ACT_MXFP4) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-          x.sa[u][i] = load4(o.sa, in ? vsa[i] : kOob, k * o.sa_step);
-      }
-    }
-  }
-  __device__ __forceinline__ void load_a(const StreamOperands& o, A& x, int kb, int kmax) const {
-    const int c = (wn * 64 + lane) % LPR;
-    constexpr int TK = AF == ACT_BF16 ? 128 : 256, CK = TK / LPR;  // K of a tile, of a chunk
+      for (int i = 0; i < NI; ++i) {
+        const dg_bf16x8 aw = __builtin_bit_cast(
+            dg_bf16x8,
+            frag(st, i, BF == FMT_FP8 ? 8 * (j >> 1) + 2 * g + (j & 1) : 4 * g + j));
 #pragma unroll
-    for (int u = 0; u < TILES; ++u) {
-      const bool in = kb * 128 + u * TK + c * CK < kmax;
-#pragma unroll
-      for (int j = 0; j < IT; ++j)
-        x.v[u][j] = load16(o.a, in ? va[j] : kOob,
-                           (uint32_t)kb * (AF == ACT_BF16 ? 256 : 64) + u * ROW);
-    }
-  }
-  __device__ __forceinline__ void store_a(const A& x, uint8_t* st) const {
-    const int t = wn * 64 + lane, c = t % LPR;
-#pragma unroll
-    for (int u = 0; u < TILES; ++u)
-#pragma unroll
-      for (int j = 0; j < IT; ++j) {
-        const int r = j * RPI + t / LPR;
-        if (MP % RPI == 0 || r < MP)
-          *reinterpret_cast<v4i*>(st + (u * MP + r) * ROW + 16 * act_slot<AF>(r, c)) = x.v[u][j];
-      }
-  }
-  __device__ __forceinline__ v4i frag(const uint8_t* st, int tile, int i, int c) const {
-    const int fr = lane & 15;
-    return *reinterpret_cast<const v4i*>(st + (tile * MP + 16 * i + fr) * ROW +
-                                         16 * act_slot<AF>(fr, c));
-  }
-  __device__ __forceinline__ void multiply(const B& x, const uint8_t* st,
-                                           v4f (&acc)[NF][NI]) const {
-    const int sh = 8 * g;
-#pragma unroll
-    for (int u = 0; u < KS; ++u) {
-      if constexpr (AF == ACT_MXFP4) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const v4i q = frag(st, u >> 1, i, 4 * (u & 1) + g);
-          const v8i aq = {q[0], q[1], q[2], q[3], 0, 0, 0, 0};
-#pragma unroll
-          for (int f = 0; f < NF; ++f) {
-            const v4i p = x.b[u][f][0];
-            const v8i bq = {p[0], p[1], p[2], p[3], 0, 0, 0, 0};
-            acc[f][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                bq, aq, acc[f][i], 4, 4, 0, (int)(x.sb[u][f] >> sh), 0, (int)(x.sa[u][i] >> sh));
-          }
-        }
-      } else {
-        dg_bf16x8 bw[NF][4];
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          if constexpr (BF == FMT_FP8)
-            widen_fp8(x.b[u][f][0], x.b[u][f][1], bw[f]);
-          else
-            widen_mxfp4(x.b[u][f][0], x.sb[u][f] >> sh, bw[f]);
-        }
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          dg_bf16x8 aw[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            aw[j] = __builtin_bit_cast(dg_bf16x8, frag(st, u, i, 4 * g + j));
-#pragma unroll
-          for (int f = 0; f < NF; ++f) {
-            v4f t = BF == FMT_FP8 ? v4f{0.f, 0.f, 0.f, 0.f} : acc[f][i];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[f][j], aw[j], t, 0, 0, 0);
-            if constexpr (BF == FMT_FP8)
-              acc[f][i] += t * __uint_as_float(x.sb[u][0]);
-            else
-              acc[f][i] = t;
-          }
-        }
+        for (int f = 0; f < NF; ++f)
+          t[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[f], aw, t[f][i], 0, 0, 0);
       }
     }
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        if constexpr (BF == FMT_FP8)
+          acc[f][i] += t[f][i] * __uint_as_float(x.sb[0]);
+        else
+          acc[f][i] = t[f][i];
+      }
   }
 
-  // K blocks of part wk of `parts` runs; every wave of the workgroup makes the
+  // Parts part0 + wk of `parts` of K; every wave of the workgroup makes the
   // same number of stages (the barriers), past its run on zeros.
-  // finish(f, i, quad): f in [0, WN NF), each fragment by the wave that owns it.
+  // finish(f, i, quad): f in [0, WN NF), each fragment by one wave.
   template <class Finish>
   __device__ __forceinline__ void run(const StreamOperands& o, int64_t K, int part0, int parts,
-                                      uint8_t* lds, Finish&& finish) {
-    const int nkb = (int)((K + 127) / 128);
+                                      uint8_t* const (&slots)[kSharedMaxDepth], Finish&& finish) {
+    const int nkb = o.last + 1;
     const int part = part0 + wk;
-    const int kb0 = (int)((int64_t)part * nkb / parts);
-    const int kb1 = (int)((int64_t)(part + 1) * nkb / parts);
+    const int kb0 = run_begin(part, nkb, parts), kb1 = run_begin(part + 1, nkb, parts);
     const int kmax = kb1 * 128 < K ? kb1 * 128 : (int)K;
-    const int stages = ((nkb + parts - 1) / parts + KS - 1) / KS;  // of the longest run
-    uint8_t* s0 = lds + wk * (2 * STAGE);
-    uint8_t* s1 = s0 + STAGE;
+    const int stages = (nkb + parts - 1) / parts;  // of the longest run
     v4f acc[NF][NI];
 #pragma unroll
     for (int f = 0; f < NF; ++f)
 #pragma unroll
       for (int i = 0; i < NI; ++i) acc[f][i] = v4f{0.f, 0.f, 0.f, 0.f};
-    A a;
-    B b0, b1;
-    load_a(o, a, kb0, kmax);
-    load_b(o, b0, kb0, kmax);
-    store_a(a, s0);
-    load_a(o, a, kb0 + KS, kmax);
-    __syncthreads();
-    auto stage = [&](const B& cur, B& nxt, const uint8_t* rd, uint8_t* wr, int kb) {
-      load_b(o, nxt, kb + KS, kmax);
+    W w[R];
+    static_for<R - 1>([&](auto j) {
+      load(o, slots[decltype(j)::value], w[decltype(j)::value], kb0 + decltype(j)::value, kmax);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(cur, rd, acc);
+    });
+    static_assert((R - 1) * LOADS <= 63, "range of the counter");
+    auto stage = [&](auto jc, int kb) {
+      constexpr int j = decltype(jc)::value, nx = (j + R - 1) % R;
       __builtin_amdgcn_sched_barrier(0);
-      store_a(a, wr);
-      load_a(o, a, kb + 2 * KS, kmax);
+      // all but the loads of the R - 2 newest stages, which were issued last
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((R - 2) * LOADS) : "memory");
       __builtin_amdgcn_sched_barrier(0);
-      // the stage's LDS writes are visible before any wave reads them; loads
-      // in flight stay in flight
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      load(o, slots[nx], w[nx], kb + R - 1, kmax);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(w[j], slots[j], acc);
     };
-    for (int s = 0; s < stages; s += 2) {
-      stage(b0, b1, s0, s1, kb0 + s * KS);
-      if (s + 1 < stages) stage(b1, b0, s1, s0, kb0 + (s + 1) * KS);
-    }
-    __syncthreads();  // the stages' room becomes the sums'
-    v4f* red = reinterpret_cast<v4f*>(lds);
-    constexpr int Q = NF * NI;
+    int s = 0;
+    for (; s + R <= stages; s += R)
+      static_for<R>([&](auto j) { stage(j, kb0 + s + decltype(j)::value); });
+    static_for<R - 1>([&](auto j) {
+      if (s + decltype(j)::value < stages) stage(j, kb0 + s + decltype(j)::value);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    v4f* red = reinterpret_cast<v4f*>(slots[0]);
+    // run wk keeps fragment f = wk of its waves and hands over the other
+    static_assert(WK == 2 && NF == 2, "each run finishes one fragment row");
 #pragma unroll
-    for (int f = 0; f < NF; ++f)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) red[((wk * WN + wn) * Q + f * NI + i) * 64 + lane] = acc[f][i];
+    for (int i = 0; i < NI; ++i) red[(wave * NI + i) * 64 + lane] = wk ? acc[0][i] : acc[1][i];
     __syncthreads();
-    for (int q = wave; q < WN * Q; q += WN * WK) {
-      v4f t = red[q * 64 + lane];
 #pragma unroll
-      for (int v = 1; v < WK; ++v) t += red[(v * WN * Q + q) * 64 + lane];
-      finish(q / NI, q % NI, t);  // q / Q is the wave's half: fragment rows follow on
+    for (int i = 0; i < NI; ++i) {
+      const v4f other = red[((wave ^ 4) * NI + i) * 64 + lane];
+      finish(NF * wn + wk, i, wk ? other + acc[1][i] : acc[0][i] + other);
     }
     __syncthreads();
   }
