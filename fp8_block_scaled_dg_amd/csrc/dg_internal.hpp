@@ -129,8 +129,10 @@ struct Mxfp4Problem {
   int64_t M, N, K;
 };
 size_t mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K, bool bf16_a);
-// Large-tile kernel (A in MXFP4, any M; no workspace).
-hipError_t launch_gemm_mxfp4_tiled(const Mxfp4Problem& p, hipStream_t stream);
+// Tiled kernel (A in MXFP4, any M).
+size_t mxfp4_tiled_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gemm_mxfp4_tiled(const Mxfp4Problem& p, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
 hipError_t launch_gemm_mxfp4(const Mxfp4Problem& p, void* workspace, size_t workspace_bytes,
                              hipStream_t stream);
 

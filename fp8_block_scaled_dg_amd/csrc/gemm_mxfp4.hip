@@ -29,18 +29,18 @@ struct Mxfp4Args {
 };
 
 // Four consecutive outputs of row m from column n (n % 4 == 0), as far as the
-// row goes; rows of C start 8-byte aligned only if N % 4 == 0.
+// row goes.  A row of C starts at any element, so the wide store is not aligned
+// to its size (the memory path takes that).
 __device__ __forceinline__ void store_quad(uint16_t* c, int64_t m, int64_t n, int64_t N, v4f t) {
-  const uint32_t lo = bf16x2_rne(t[0], t[1]), hi = bf16x2_rne(t[2], t[3]);
+  const uint32_t v[2] = {bf16x2_rne(t[0], t[1]), bf16x2_rne(t[2], t[3])};
   uint16_t* d = c + m * N + n;
-  if ((N & 3) == 0) {
-    if (n < N) *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+  if (n + 4 <= N) {
+    __builtin_memcpy(__builtin_assume_aligned(d, 2), v, 8);
     return;
   }
-  if (n < N) d[0] = (uint16_t)lo;
-  if (n + 1 < N) d[1] = (uint16_t)(lo >> 16);
-  if (n + 2 < N) d[2] = (uint16_t)hi;
-  if (n + 3 < N) d[3] = (uint16_t)(hi >> 16);
+  if (n < N) d[0] = (uint16_t)v[0];
+  if (n + 1 < N) d[1] = (uint16_t)(v[0] >> 16);
+  if (n + 2 < N) d[2] = (uint16_t)v[1];
 }
 
 template <int AF, int NI, int NF, int U>
@@ -279,13 +279,13 @@ size_t plan_bytes(const StreamPlan& s) {
 }  // namespace
 
 size_t mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K, bool bf16_a) {
-  if (M > 64) return 0;
+  if (M > 64) return bf16_a ? 0 : mxfp4_tiled_workspace_bytes(M, N, K);
   return plan_bytes(stream_plan(M, N, K, bf16_a));
 }
 
 hipError_t launch_gemm_mxfp4(const Mxfp4Problem& q, void* workspace, size_t workspace_bytes,
                              hipStream_t stream) {
-  if (q.M > 64) return launch_gemm_mxfp4_tiled(q, stream);
+  if (q.M > 64) return launch_gemm_mxfp4_tiled(q, workspace, workspace_bytes, stream);
   Mxfp4Args p;
   p.c = q.c;
   p.a = static_cast<const uint8_t*>(q.a);

@@ -103,8 +103,12 @@ PRODUCTS = [(1, 1, 32), (1, 128, 128), (2, 7, 96), (16, 16, 512), (17, 130, 160)
             (513, 2049, 160), (2001, 384, 1024), (300, 1000, 2016)]
 
 
+# few tiles and a long K: parts of K meet in the workspace
+SPLIT_PRODUCTS = [(130, 7, 16384), (65, 129, 6176), (257, 300, 12320), (600, 500, 6400)]
+
+
 @pytest.mark.parametrize("ws", [True, False])
-@pytest.mark.parametrize("M,N,K", PRODUCTS)
+@pytest.mark.parametrize("M,N,K", PRODUCTS + SPLIT_PRODUCTS)
 def test_product(dg, M, N, K, ws):
     qa, sa = operand(M, K, M + K)
     qb, sb = operand(N, K, N + K + 1, 0.02)
