@@ -104,7 +104,9 @@ PRODUCTS = [(1, 1, 32), (1, 128, 128), (2, 7, 96), (16, 16, 512), (17, 130, 160)
 
 
 # few tiles and a long K: parts of K meet in the workspace
-SPLIT_PRODUCTS = [(130, 7, 16384), (65, 129, 6176), (257, 300, 12320), (600, 500, 6400)]
+# (long rows of B and 16 to 64 rows of A: rings in LDS, runs of unequal length)
+SPLIT_PRODUCTS = [(1, 3201, 4000), (16, 3300, 4128), (31, 3203, 4512), (48, 3201, 4064), (64, 3333, 6880),
+                  (130, 7, 16384), (65, 129, 6176), (257, 300, 12320), (600, 500, 6400)]
 
 
 @pytest.mark.parametrize("ws", [True, False])
