@@ -2,6 +2,7 @@
 //   ids, p  = the k largest router logits of a token (ties: the lowest index)
 //             and their softmax or sigmoid scores, normalised to sum 1
 //   h[t,j]  = p[t,j] silu(x[t] . Wg^T) (x[t] . Wu^T)      Wg, Wu of expert ids[t,j]
+//             (held as the sum of two BF16 numbers)
 //   y[t]    = sum_j h[t,j] . W2^T                         W2 of expert ids[t,j]
 // with the expert weights in E4M3 (128 x 128 FP32 scales) or MXFP4 and the
 // activations in BF16.
@@ -43,7 +44,7 @@ struct MoeArgs {
   int64_t H, I;
   MoeTables tb;
   int* counters;   // per column tile of the down launch (zero between calls)
-  uint16_t* h;     // [T k][I] BF16
+  uint16_t* h;     // [T k][2][I] BF16: the value's two parts
   float* part;     // [T k][H]
 };
 
@@ -213,7 +214,7 @@ __device__ __forceinline__ StreamOperands expert_operands(const uint8_t* w, cons
 //
 // Few rows (ENGINE_STREAM): four waves with a quarter of K each and the same
 // 16 NF weight rows, activations straight into fragments.
-template <int BF, int NF_>
+template <int BF, int NF_, int MAXNI>
 struct StreamEngine {
   static constexpr int NF = NF_, ROWS_B = 16 * NF, THREADS = 64 * kWaves, WAVES = 1;
   template <int NI, class Rows, class Finish>
@@ -260,7 +261,7 @@ struct StreamEngine {
     }
     __syncthreads();  // red is free again
   }
-  static constexpr int R = 1, SLOT = 16, SLOT0 = kWaves * NF * 1024;
+  static constexpr int R = 1, SLOT = 16, SLOT0 = kWaves * NF * MAXNI * 1024;
 };
 
 // More rows: activations in LDS (Shared, mxfp4_device.hpp).
@@ -310,8 +311,18 @@ __global__ void __launch_bounds__(Engine::THREADS, Engine::WAVES) moe_up_kernel(
             const float wt = p.weights[pair];
             const int64_t u = (n0 + 16 * f + 4 * (lane >> 4)) / 2;  // units u, u + 1 (I is even)
             if (u >= p.I) return;
-            *reinterpret_cast<uint32_t*>(p.h + pair * p.I + u) =
-                bf16x2_rne(silu_f(t[0]) * t[1] * wt, silu_f(t[2]) * t[3] * wt);
+            // two BF16 parts, 16 significant bits together: rounded to one, h
+            // would add as much to y's error as y's own rounding (rms 2.4e-3
+            // against 1.7e-3)
+            const float h0 = silu_f(t[0]) * t[1] * wt, h1 = silu_f(t[2]) * t[3] * wt;
+            const uint32_t hi = bf16x2_rne(h0, h1);
+            const float r0 = h0 - __uint_as_float(hi << 16);
+            const float r1 = h1 - __uint_as_float(hi & 0xFFFF0000u);
+            uint16_t* d = p.h + (int64_t)pair * 2 * p.I + u;
+            *reinterpret_cast<uint32_t*>(d) = hi;
+            // infinite and NaN values have no second part
+            *reinterpret_cast<uint32_t*>(d + p.I) =
+                bf16x2_rne(fabsf(r0) < INFINITY ? r0 : 0.0f, fabsf(r1) < INFINITY ? r1 : 0.0f);
           });
     });
   }
@@ -340,16 +351,23 @@ __global__ void __launch_bounds__(Engine::THREADS, Engine::WAVES) moe_down_kerne
   const void* sc = static_cast<const uint32_t*>(p.s2) + e * sstep;
   const int rows_b = (int)(N - n0 < 16 * NF ? N - n0 : 16 * NF);
   const StreamOperands o =
-      expert_operands<BF>(w, sc, N, K, n0, rows_b, p.h, (int64_t)p.T * p.k * K * 2);
-  for (int c0 = 0; c0 < count; c0 += 16 * MAXNI) {
-    const int rows = count - c0 < 16 * MAXNI ? count - c0 : 16 * MAXNI;
+      expert_operands<BF>(w, sc, N, K, n0, rows_b, p.h, (int64_t)p.T * p.k * K * 4);
+  // a pair takes two neighbouring rows, its h's parts; their sums are added
+  // before they leave
+  for (int c0 = 0; c0 < count; c0 += 8 * MAXNI) {
+    const int rows = 2 * (count - c0 < 8 * MAXNI ? count - c0 : 8 * MAXNI);
     with_fragments<MAXNI>(rows, [&](auto ni) {
       Engine::template tile<decltype(ni)::value>(
-          o, K, rows_b, [&](int r) { return r < rows ? list[c0 + r] : -1; }, slots,
-          [&](int f, int i, v4f t) {
+          o, K, rows_b, [&](int r) { return r < rows ? 2 * list[c0 + (r >> 1)] + (r & 1) : -1; },
+          slots, [&](int f, int i, v4f t) {
             const int r = 16 * i + fr;
             const int64_t n = n0 + 16 * f + 4 * (lane >> 4);
-            if (r < rows && n < N) publish4(p.part + list[c0 + r] * N + n, t);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)  // the neighbouring lane's
+              t[q] += __int_as_float(
+                  __builtin_amdgcn_mov_dpp(__float_as_int(t[q]), 0xB1, 0xF, 0xF, false));
+            if ((r & 1) == 0 && r < rows && n < N)
+              publish4(p.part + (int64_t)list[c0 + (r >> 1)] * N + n, t);
           });
     });
   }
@@ -389,7 +407,7 @@ MoeLayout moe_layout(int T, int E, int k, int64_t H, int64_t I) {
   MoeLayout l;
   l.tables = kSplitkCounterBytes;
   l.h = l.tables + up16((size_t)(4 + 2 * E + T * k) * 4);
-  l.part = l.h + up16((size_t)T * k * I * 2);
+  l.part = l.h + up16((size_t)T * k * I * 4);
   l.total = l.part + (size_t)T * k * H * 4;
   return l;
 }
@@ -410,28 +428,33 @@ hipError_t launch_down(const MoeArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int BF, int MAXNI, class Engine>
-hipError_t launch_both(const MoeArgs& p, hipStream_t stream) {
-  const hipError_t e = launch_up<BF, MAXNI, Engine>(p, stream);
-  return e != hipSuccess ? e : launch_down<BF, MAXNI, Engine>(p, stream);
-}
-
 // Measured on an MI355X, us a layer with the weights from HBM:
 //  * up to four tokens 32 weight rows a workgroup, up to 16 tokens 64, whose
 //    waves read their activations half as often: 66.6 against 75.8 (1 token, 8
 //    experts of 4096 x 11008, E4M3), 79.3 / 76.2 (13 tokens, 60 of 2048 x 1408);
 //  * more tokens: activations in LDS, 160 against 191 (64 tokens, 8 experts,
 //    MXFP4), 245 / 260 (E4M3);
-//  * 32 rows of an expert at a time leave two workgroups a CU (160 against 167
+//  * 32 activation rows at a time leave two workgroups a CU (160 against 167
 //    with 64, same layer), but an expert with more rows reads its weights again:
 //    64 at a time where the mean is above 20.
 template <int BF>
 hipError_t launch_experts(const MoeArgs& p, hipStream_t stream) {
-  if (p.T <= 4) return launch_both<BF, 1, StreamEngine<BF, 2>>(p, stream);
-  if (p.T <= 16) return launch_both<BF, 1, StreamEngine<BF, 4>>(p, stream);
-  if (p.T <= 32 || p.T * p.k <= 20 * p.E)
-    return launch_both<BF, 2, SharedEngine<BF, 2>>(p, stream);
-  return launch_both<BF, 4, SharedEngine<BF, 4>>(p, stream);
+  const int pairs = p.T * p.k;
+  hipError_t e;
+  if (p.T <= 4)
+    e = launch_up<BF, 1, StreamEngine<BF, 2, 1>>(p, stream);
+  else if (p.T <= 16)
+    e = launch_up<BF, 1, StreamEngine<BF, 4, 1>>(p, stream);
+  else if (p.T <= 32 || pairs <= 20 * p.E)
+    e = launch_up<BF, 2, SharedEngine<BF, 2>>(p, stream);
+  else
+    e = launch_up<BF, 4, SharedEngine<BF, 4>>(p, stream);
+  if (e != hipSuccess) return e;
+  // two rows a pair
+  if (p.T <= 4) return launch_down<BF, 1, StreamEngine<BF, 2, 1>>(p, stream);
+  if (p.T <= 16) return launch_down<BF, 2, StreamEngine<BF, 4, 2>>(p, stream);
+  if (pairs <= 10 * p.E) return launch_down<BF, 2, SharedEngine<BF, 2>>(p, stream);
+  return launch_down<BF, 4, SharedEngine<BF, 4>>(p, stream);
 }
 
 }  // namespace

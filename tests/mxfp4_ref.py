@@ -101,8 +101,9 @@ def route(logits, k, scoring):
 
 def moe(x, w13, w2, ids, weights):
     """x [T][H], w13 [E][2I][H], w2 [E][H][I] float64 -> y and its error bound
-    before the last rounding: h is rounded to BF16 (2^-8), the sums as in
-    product(), and the FP32 SwiGLU (expf, division, products: 2^-20 with
+    before the last rounding: h is held in two BF16 parts (the second one's
+    rounding: 2^-8 of 2^-8), whose products are summed as in product() and
+    added, and the FP32 SwiGLU (expf, division, products: 2^-20 with
     room) and weight (given as FP32)."""
     T, H = x.shape
     E, _, I = w2.shape
@@ -118,8 +119,8 @@ def moe(x, w13, w2, ids, weights):
             h = g * sig * u * weights[t, j]
             # |silu'| <= 1.1
             dh = np.abs(weights[t, j]) * (1.1 * dg * (np.abs(u) + du) + np.abs(g * sig) * du)
-            dh = dh + (2.0 ** -8 + 2.0 ** -20) * (np.abs(h) + dh)
+            dh = dh + (2.0 ** -16 + 2.0 ** -20) * (np.abs(h) + dh)
             y[t] += w2[e] @ h
-            bound[t] += np.abs(w2[e]) @ (dh + I * 2.0 ** -23 * (np.abs(h) + dh))
+            bound[t] += np.abs(w2[e]) @ (dh + (I + 1) * 2.0 ** -23 * (1 + 2.0 ** -7) * (np.abs(h) + dh))
         bound[t] += 2.0 ** -23 * len(ids[t]) * np.abs(y[t])
     return y, bound

@@ -74,6 +74,7 @@ def test_moe_layer(dg):
     assert f(T=0) == f(T=65) == f(E=0) == f(E=1025) == f(k=0) == f(k=9) == f(E=32, k=17) == 2
     assert f(H=0) == f(H=272) == f(I=16) == f(H=131104) == f(I=(1 << 20) + 32) == 2
     assert f(fmt=1, H=160) == f(fmt=1, I=160) == 2       # 128 x 128 blocks
+    assert f(T=64, E=16, k=16, H=32, I=1 << 19) == 2     # hidden values of 2^31 bytes
     assert f(ws=None) == 5
     need = dg.dg_moe_layer_workspace_bytes(4, 8, 2, 256, 128)
     assert f(n=need - 1) == 5
