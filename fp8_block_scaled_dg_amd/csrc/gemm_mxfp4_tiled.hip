@@ -23,6 +23,14 @@
 //  * Workgroup ids are dealt round-robin to the 8 XCDs; they are remapped so
 //    that each XCD gets a contiguous run of tiles in groups of 4 tile rows
 //    swept along N, whose A and B panels its L2 holds.
+//
+// MI355X: 8192^3 261 us (4.2 PFLOP/s), 4096 x 7168 x 2048 41 us.  A loop of
+// nothing but these instructions on random codes reaches 7.1 PFLOP/s (9.7 on
+// zeros: the clock gives way to power), and in the 8192^3 product the clock is
+// near 1.9 GHz with the matrix cores busy 52 % of the cycles.  L2 requests fell
+// by half with 128-byte rows (34 to 18 million, 298 to 273 us); deeper rings of
+// 64-byte rows, smaller tiles side by side and four waves of 128 x 128 (512
+// registers, spilling) were slower.
 #include "mxfp4_device.hpp"
 
 namespace dg {

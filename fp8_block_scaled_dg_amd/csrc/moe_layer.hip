@@ -12,6 +12,11 @@
 // expert the list of its (token, slot) pairs), gate/up with the SwiGLU and the
 // routing weight in its epilogue, and down, whose last workgroup per column
 // tile adds the k slots of each token in slot order.
+//
+// MI355X, kernels alone (router, up, down): 1 token on 8 experts of 4096 x
+// 11008 in E4M3 4.5 + 36 + 22 us (180 MB at 5.0 TB/s, 90 MB at 4.1); 64 tokens
+// on the same experts in MXFP4 6 + 95 + 65 us (383 MB at 4.0 TB/s, 191 MB at
+// 2.9: 256 workgroups, one round, whose start and end nothing hides).
 #include "mxfp4_device.hpp"
 
 namespace dg {
@@ -436,7 +441,8 @@ hipError_t launch_down(const MoeArgs& p, hipStream_t stream) {
 //    MXFP4), 245 / 260 (E4M3);
 //  * 32 activation rows at a time leave two workgroups a CU (160 against 167
 //    with 64, same layer), but an expert with more rows reads its weights again:
-//    64 at a time where the mean is above 20.
+//    64 at a time where the mean is above 20 rows.
+//  (one BF16 part a hidden value then; with two, 169 us for 64 tokens in MXFP4)
 template <int BF>
 hipError_t launch_experts(const MoeArgs& p, hipStream_t stream) {
   const int pairs = p.T * p.k;

