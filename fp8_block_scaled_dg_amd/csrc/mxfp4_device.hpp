@@ -411,24 +411,38 @@ struct Shared {
       __builtin_amdgcn_sched_barrier(0);
     });
     static_assert((R - 1) * LOADS <= 63, "range of the counter");
-    auto stage = [&](auto jc, int kb) {
-      constexpr int j = decltype(jc)::value, nx = (j + R - 1) % R;
+    // This wave's transfers of the stage to multiply have landed, all but the
+    // loads of the `newer` stages issued after it; the barrier tells so of every
+    // wave's, and that the slot of the stage before is free.  The count stands
+    // for what was issued, so every load of a newer stage has to be one that the
+    // compiler keeps: the loop's are multiplied by a later pass or by the tail,
+    // and the tail, whose loads nothing would read, makes none.
+    auto landed = [&](auto newer) {
       __builtin_amdgcn_sched_barrier(0);
-      // all but the loads of the R - 2 newest stages, which were issued last
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((R - 2) * LOADS) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier ; stage of %1 transfers" ::"n"(
+                       decltype(newer)::value * LOADS),
+                   "n"(IT)
+                   : "memory");
       __builtin_amdgcn_sched_barrier(0);
-      load(o, slots[nx], w[nx], kb + R - 1, kmax);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(w[j], slots[j], acc);
     };
     int s = 0;
     for (; s + R <= stages; s += R)
-      static_for<R>([&](auto j) { stage(j, kb0 + s + decltype(j)::value); });
-    static_for<R - 1>([&](auto j) {
-      if (s + decltype(j)::value < stages) stage(j, kb0 + s + decltype(j)::value);
+      static_for<R>([&](auto jc) {
+        constexpr int j = decltype(jc)::value, nx = (j + R - 1) % R;
+        landed(IntTag<R - 2>{});
+        load(o, slots[nx], w[nx], kb0 + s + j + R - 1, kmax);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(w[j], slots[j], acc);
+      });
+    static_while<R - 1>([&](auto jc) {
+      constexpr int j = decltype(jc)::value;
+      if (s + j >= stages) return false;
+      landed(IntTag<R - 2 - j>{});
+      multiply(w[j], slots[j], acc);
+      return true;
     });
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier ; end of stages" ::: "memory");
     v4f* red = reinterpret_cast<v4f*>(slots[0]);
     // run wk keeps fragment f = wk of its waves and hands over the other
     static_assert(WK == 2 && NF == 2, "each run finishes one fragment row");
