@@ -327,9 +327,11 @@ gemm_mxfp4_shared_kernel(Mxfp4Args p) {
     if (m < p.M) store_quad(p.c, m, n0 + 16 * f + 4 * (lane >> 4), p.N, t);
   };
   float* part0 = p.partials + (int64_t)tile * p.S * (QT * 256);
-  s.run(o, p.K, split * S::WK, p.S * S::WK, slots, [&](int f, int i, v4f t) {
-    if (p.S == 1) store(f, i, t);
-    else publish4(part0 + split * (QT * 256) + ((f * NI + i) * 64 + lane) * 4, t);
+  s.run(o, p.K, split * S::WK, p.S * S::WK, slots, [&](int f, const v4f (&t)[NI]) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (p.S == 1) store(f, i, t[i]);
+      else publish4(part0 + split * (QT * 256) + ((f * NI + i) * 64 + lane) * 4, t[i]);
   });
   if (p.S == 1) return;
   if (!arrive_last(&p.counters[tile], p.S, &s_last)) return;

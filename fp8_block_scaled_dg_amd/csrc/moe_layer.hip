@@ -2,7 +2,7 @@
 //   ids, p  = the k largest router logits of a token (ties: the lowest index)
 //             and their softmax or sigmoid scores, normalised to sum 1
 //   h[t,j]  = p[t,j] silu(x[t] . Wg^T) (x[t] . Wu^T)      Wg, Wu of expert ids[t,j]
-//             (held as the sum of two BF16 numbers)
+//             (held in FP32's 24 bits, as the sum of three BF16 numbers)
 //   y[t]    = sum_j h[t,j] . W2^T                         W2 of expert ids[t,j]
 // with the expert weights in E4M3 (128 x 128 FP32 scales) or MXFP4 and the
 // activations in BF16.
@@ -11,12 +11,16 @@
 // each read once.  Three launches: the router (one workgroup: top-k, and per
 // expert the list of its (token, slot) pairs), gate/up with the SwiGLU and the
 // routing weight in its epilogue, and down, whose last workgroup per column
-// tile adds the k slots of each token in slot order.
+// tile adds the k slots of each token in slot order.  Where the hidden values of
+// all pairs would take more than kMaxHidden, gate/up and down take the hidden
+// units in chunks, down adding to what it has.
 //
 // MI355X, kernels alone (router, up, down): 1 token on 8 experts of 4096 x
 // 11008 in E4M3 4.5 + 36 + 22 us (180 MB at 5.0 TB/s, 90 MB at 4.1); 64 tokens
-// on the same experts in MXFP4 6 + 95 + 65 us (383 MB at 4.0 TB/s, 191 MB at
-// 2.9: 256 workgroups, one round, whose start and end nothing hides).
+// on the same experts in MXFP4 9 + 98 + 80 us (383 MB at 3.9 TB/s, 191 MB at
+// 2.4: 256 workgroups of 128 weight rows, one a CU, whose LDS reads and products
+// for 20 pairs, 60 rows, no longer hide behind the weights; 65 us when h had two
+// parts and a pair two rows).
 #include "mxfp4_device.hpp"
 
 namespace dg {
@@ -24,6 +28,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kRouterThreads = 1024;
+constexpr int kParts = 3;  // BF16 numbers that hold a hidden value
 
 // Routing tables in the workspace: counts [E], then per expert a list of
 // pairs t * k + j (ascending), offsets [E] into one array of T k entries.
@@ -49,8 +54,9 @@ struct MoeArgs {
   int64_t H, I;
   MoeTables tb;
   int* counters;   // per column tile of the down launch (zero between calls)
-  uint16_t* h;     // [T k][2][I] BF16: the value's two parts
+  uint16_t* h;     // [T k][3][chunk] BF16: the value's three parts
   float* part;     // [T k][H]
+  int64_t u0, chunk;  // the hidden units of this launch: u0 .. u0 + chunk - 1
 };
 
 // Largest value of the wave, in every lane (no NaN among them).
@@ -190,23 +196,24 @@ __device__ __forceinline__ void with_fragments(int rows, F&& f) {
   }
 }
 
-// Operands of one expert's weight rows n0 .. n0 + 16 NF - 1 with activations
-// [..][K] in BF16.
+// Operands of weight rows n0 .. n0 + rows_b - 1 of one expert's [N][ld] matrix,
+// its columns k0 .. k0 + K - 1 (k0 a multiple of 128), with activations in BF16.
 template <int BF>
 __device__ __forceinline__ StreamOperands expert_operands(const uint8_t* w, const void* scales,
-                                                          int64_t N, int64_t K, int64_t n0,
-                                                          int rows_b, const void* act,
-                                                          int64_t act_bytes) {
+                                                          int64_t N, int64_t ld, int64_t k0,
+                                                          int64_t K, int64_t n0, int rows_b,
+                                                          const void* act, int64_t act_bytes) {
   const int nkb = (int)((K + 127) / 128);
-  const int64_t ldb = BF == FMT_FP8 ? K : K / 2;
+  const int64_t ldb = BF == FMT_FP8 ? ld : ld / 2, off = BF == FMT_FP8 ? k0 : k0 / 2;
   StreamOperands o;
-  o.b = buffer_of(w + n0 * ldb, rows_b * ldb);
+  o.b = buffer_of(w + n0 * ldb + off, rows_b * ldb - off);
   if (BF == FMT_FP8) {
     const int64_t nb = (N + 127) / 128;
-    o.sb = buffer_of(static_cast<const float*>(scales) + n0 / 128, (nkb * nb - n0 / 128) * 4);
+    o.sb = buffer_of(static_cast<const float*>(scales) + k0 / 128 * nb + n0 / 128,
+                     (nkb * nb - n0 / 128) * 4);
     o.sb_step = (uint32_t)nb * 4;
   } else {
-    o.sb = buffer_of(static_cast<const uint32_t*>(scales) + n0, (nkb * N - n0) * 4);
+    o.sb = buffer_of(static_cast<const uint32_t*>(scales) + k0 / 128 * N + n0, (nkb * N - n0) * 4);
     o.sb_step = (uint32_t)N * 4;
   }
   o.a = buffer_of(act, act_bytes);
@@ -214,23 +221,25 @@ __device__ __forceinline__ StreamOperands expert_operands(const uint8_t* w, cons
   return o;
 }
 
-// One tile of weight rows by 16 NI activation rows: finish(f, i, quad) is
-// called for every fragment, by one wave.
+// One tile of weight rows (ldb bytes apart) by 16 NI activation rows:
+// finish(f, quads) is called for every 16 weight rows with the NI quads of their
+// outputs, by one wave.
 //
-// Few rows (ENGINE_STREAM): four waves with a quarter of K each and the same
-// 16 NF weight rows, activations straight into fragments.
+// Few rows: four waves with a quarter of K each and the same 16 NF weight rows,
+// activations straight into fragments.
 template <int BF, int NF_, int MAXNI>
 struct StreamEngine {
   static constexpr int NF = NF_, ROWS_B = 16 * NF, THREADS = 64 * kWaves, WAVES = 1;
   template <int NI, class Rows, class Finish>
-  static __device__ __forceinline__ void tile(const StreamOperands& o, int64_t K, int rows_b, Rows&& row_of, uint8_t* const (&slots)[kSharedMaxDepth],
+  static __device__ __forceinline__ void tile(const StreamOperands& o, int64_t K, int64_t ldb,
+                                              int rows_b, Rows&& row_of,
+                                              uint8_t* const (&slots)[kSharedMaxDepth],
                                               Finish&& finish) {
     v4f* red = reinterpret_cast<v4f*>(slots[0]);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15;
     const int nkb = o.last + 1;
-    const int64_t ldb = BF == FMT_FP8 ? K : K / 2;
     Stream<ACT_BF16, BF, NI, NF, 1> s;
     s.g = lane >> 4;
 #pragma unroll
@@ -258,11 +267,15 @@ struct StreamEngine {
 #pragma unroll
       for (int i = 0; i < NI; ++i) red[(wave * Q + f * NI + i) * 64 + lane] = acc[f][i];
     __syncthreads();
-    for (int q = wave; q < Q; q += kWaves) {
-      v4f t = red[q * 64 + lane];
+    for (int f = wave; f < NF; f += kWaves) {
+      v4f t[NI];
 #pragma unroll
-      for (int v = 1; v < kWaves; ++v) t += red[(v * Q + q) * 64 + lane];
-      finish(q / NI, q % NI, t);
+      for (int i = 0; i < NI; ++i) {
+        t[i] = red[(f * NI + i) * 64 + lane];
+#pragma unroll
+        for (int v = 1; v < kWaves; ++v) t[i] += red[(v * Q + f * NI + i) * 64 + lane];
+      }
+      finish(f, t);
     }
     __syncthreads();  // red is free again
   }
@@ -270,20 +283,20 @@ struct StreamEngine {
 };
 
 // More rows: activations in LDS (Shared, mxfp4_device.hpp).
-template <int BF, int MAXNI>
+template <int BF, int MAXNI, int R_ = shared_depth(BF, MAXNI)>
 struct SharedEngine {
-  static constexpr int R = shared_depth(BF, MAXNI);
+  static constexpr int R = R_;
   typedef Shared<BF, MAXNI, R> Largest;
   static constexpr int ROWS_B = Largest::ROWS_B, NF = ROWS_B / 16, THREADS = kSharedThreads;
   static constexpr int SLOT0 = Largest::SLOT0, SLOT = Largest::SLOT;
   static constexpr int WAVES = Largest::WAVES;
   template <int NI, class Rows, class Finish>
-  static __device__ __forceinline__ void tile(const StreamOperands& o, int64_t K, int rows_b,
-                                              Rows&& row_of,
+  static __device__ __forceinline__ void tile(const StreamOperands& o, int64_t K, int64_t ldb,
+                                              int rows_b, Rows&& row_of,
                                               uint8_t* const (&slots)[kSharedMaxDepth],
                                               Finish&& finish) {
     Shared<BF, NI, R> s;
-    s.init(BF == FMT_FP8 ? K : K / 2, rows_b, K * 2, row_of);
+    s.init(ldb, rows_b, K * 2, row_of);
     s.run(o, K, 0, s.WK, slots, finish);
   }
 };
@@ -297,40 +310,57 @@ __global__ void __launch_bounds__(Engine::THREADS, Engine::WAVES) moe_up_kernel(
   const int count = p.tb.counts[e];
   if (count == 0) return;
   const int lane = threadIdx.x & 63, fr = lane & 15;
-  const int64_t N = 2 * p.I, K = p.H, n0 = (int64_t)blockIdx.x * (16 * NF);
+  const int64_t N = 2 * p.I, K = p.H, n0 = 2 * p.u0 + (int64_t)blockIdx.x * (16 * NF);
+  const int64_t end = 2 * (p.u0 + p.chunk), ldb = BF == FMT_FP8 ? K : K / 2;
   const int* list = p.tb.pairs + p.tb.offsets[e];
   const int64_t sstep = BF == FMT_FP8 ? (K / 128) * ((N + 127) / 128) : ((K + 127) / 128) * N;
-  const uint8_t* w = p.w13 + (int64_t)e * N * (BF == FMT_FP8 ? K : K / 2);
+  const uint8_t* w = p.w13 + e * N * ldb;
   const void* sc = static_cast<const uint32_t*>(p.s13) + e * sstep;
-  const int rows_b = (int)(N - n0 < 16 * NF ? N - n0 : 16 * NF);
-  const StreamOperands o = expert_operands<BF>(w, sc, N, K, n0, rows_b, p.x, p.T * K * 2);
+  const int rows_b = (int)(end - n0 < 16 * NF ? end - n0 : 16 * NF);
+  const StreamOperands o = expert_operands<BF>(w, sc, N, K, 0, K, n0, rows_b, p.x, p.T * K * 2);
   for (int c0 = 0; c0 < count; c0 += 16 * MAXNI) {
     const int rows = count - c0 < 16 * MAXNI ? count - c0 : 16 * MAXNI;
     with_fragments<MAXNI>(rows, [&](auto ni) {
-      Engine::template tile<decltype(ni)::value>(
-          o, K, rows_b, [&](int r) { return r < rows ? list[c0 + r] / p.k : -1; }, slots,
-          [&](int f, int i, v4f t) {
-            const int r = 16 * i + fr;
-            if (r >= rows) return;
-            const int pair = list[c0 + r];
-            const float wt = p.weights[pair];
-            const int64_t u = (n0 + 16 * f + 4 * (lane >> 4)) / 2;  // units u, u + 1 (I is even)
-            if (u >= p.I) return;
-            // two BF16 parts, 16 significant bits together: rounded to one, h
-            // would add as much to y's error as y's own rounding (rms 2.4e-3
-            // against 1.7e-3)
-            const float h0 = silu_f(t[0]) * t[1] * wt, h1 = silu_f(t[2]) * t[3] * wt;
-            const uint32_t hi = bf16x2_rne(h0, h1);
-            const float r0 = h0 - __uint_as_float(hi << 16);
-            const float r1 = h1 - __uint_as_float(hi & 0xFFFF0000u);
-            uint16_t* d = p.h + (int64_t)pair * 2 * p.I + u;
-            *reinterpret_cast<uint32_t*>(d) = hi;
-            // infinite and NaN values have no second part
-            *reinterpret_cast<uint32_t*>(d + p.I) =
-                bf16x2_rne(fabsf(r0) < INFINITY ? r0 : 0.0f, fabsf(r1) < INFINITY ? r1 : 0.0f);
+      constexpr int NI = decltype(ni)::value;
+      Engine::template tile<NI>(
+          o, K, ldb, rows_b, [&](int r) { return r < rows ? list[c0 + r] / p.k : -1; }, slots,
+          [&](int f, const v4f (&t)[NI]) {
+            // units u, u + 1 (the chunk is even)
+            const int64_t u = (n0 + 16 * f + 4 * (lane >> 4)) / 2 - p.u0;
+            if (u >= p.chunk) return;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              const int r = 16 * i + fr;
+              if (r >= rows) continue;
+              const int pair = list[c0 + r];
+              const float wt = p.weights[pair];
+              // Three parts, each the leading BF16 of what is left (exact, so they
+              // hold FP32's 24 bits).  With two, 16 bits, the rounding of h was all
+              // of y's error before its own: 2.4e-6 of rms, the sums' 1e-7 to 3e-7.
+              float h0 = silu_f(t[i][0]) * t[i][1] * wt, h1 = silu_f(t[i][2]) * t[i][3] * wt;
+              uint16_t* d = p.h + pair * kParts * p.chunk + u;
+#pragma unroll
+              for (int part = 0; part < kParts; ++part) {
+                const uint32_t v = bf16x2_rne(h0, h1);
+                *reinterpret_cast<uint32_t*>(d + part * p.chunk) = v;
+                h0 -= __uint_as_float(v << 16);
+                h1 -= __uint_as_float(v & 0xFFFF0000u);
+                // infinite and NaN values are their first part
+                h0 = fabsf(h0) < INFINITY ? h0 : 0.0f;
+                h1 = fabsf(h1) < INFINITY ? h1 : 0.0f;
+              }
+            }
           });
     });
   }
+}
+
+// v of the lane D after this one among 16, of `next` where that is past the 16th
+template <int D>
+__device__ __forceinline__ float after(float v, float next, int fr) {
+  const int a = __builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + 16 - D, 0xF, 0xF, false);
+  const int b = __builtin_amdgcn_mov_dpp(__float_as_int(next), 0x120 + 16 - D, 0xF, 0xF, false);
+  return __int_as_float(fr + D < 16 ? a : b);
 }
 
 template <int BF, int MAXNI, class Engine>
@@ -342,8 +372,9 @@ __global__ void __launch_bounds__(Engine::THREADS, Engine::WAVES) moe_down_kerne
   const int count = p.tb.counts[e];
   const int active = *p.tb.active;
   const int lane = threadIdx.x & 63, fr = lane & 15;
-  const int64_t N = p.H, K = p.I, n0 = (int64_t)blockIdx.x * (16 * NF);
-  if (active == 0) {  // no token chose anything: y = 0
+  const int64_t N = p.H, K = p.chunk, n0 = (int64_t)blockIdx.x * (16 * NF);
+  const int64_t ldb = BF == FMT_FP8 ? p.I : p.I / 2;
+  if (active == 0) {  // no token chose anything: y = 0 (in every chunk's launch)
     if (e == 0)
       for (int q = threadIdx.x; q < p.T * 16 * NF; q += Engine::THREADS)
         if (n0 + q % (16 * NF) < N) p.y[q / (16 * NF) * N + n0 + q % (16 * NF)] = 0;
@@ -351,31 +382,41 @@ __global__ void __launch_bounds__(Engine::THREADS, Engine::WAVES) moe_down_kerne
   }
   if (count == 0) return;
   const int* list = p.tb.pairs + p.tb.offsets[e];
-  const int64_t sstep = BF == FMT_FP8 ? (K / 128) * ((N + 127) / 128) : ((K + 127) / 128) * N;
-  const uint8_t* w = p.w2 + (int64_t)e * N * (BF == FMT_FP8 ? K : K / 2);
+  const int64_t sstep = (p.I + 127) / 128 * (BF == FMT_FP8 ? (N + 127) / 128 : N);
+  const uint8_t* w = p.w2 + e * N * ldb;
   const void* sc = static_cast<const uint32_t*>(p.s2) + e * sstep;
   const int rows_b = (int)(N - n0 < 16 * NF ? N - n0 : 16 * NF);
-  const StreamOperands o =
-      expert_operands<BF>(w, sc, N, K, n0, rows_b, p.h, (int64_t)p.T * p.k * K * 4);
-  // a pair takes two neighbouring rows, its h's parts; their sums are added
-  // before they leave
-  for (int c0 = 0; c0 < count; c0 += 8 * MAXNI) {
-    const int rows = 2 * (count - c0 < 8 * MAXNI ? count - c0 : 8 * MAXNI);
+  const StreamOperands o = expert_operands<BF>(w, sc, N, p.I, p.u0, K, n0, rows_b, p.h,
+                                               (int64_t)p.T * p.k * kParts * K * 2);
+  // a pair takes three neighbouring rows, its h's parts, without gaps between
+  // pairs; their sums are added before they leave
+  constexpr int kPairs = 16 * MAXNI / kParts;
+  for (int c0 = 0; c0 < count; c0 += kPairs) {
+    const int rows = kParts * (count - c0 < kPairs ? count - c0 : kPairs);
     with_fragments<MAXNI>(rows, [&](auto ni) {
-      Engine::template tile<decltype(ni)::value>(
-          o, K, rows_b, [&](int r) { return r < rows ? 2 * list[c0 + (r >> 1)] + (r & 1) : -1; },
-          slots, [&](int f, int i, v4f t) {
-            const int r = 16 * i + fr;
+      constexpr int NI = decltype(ni)::value;
+      Engine::template tile<NI>(
+          o, K, ldb, rows_b,
+          [&](int r) { return r < rows ? kParts * list[c0 + r / kParts] + r % kParts : -1; }, slots,
+          [&](int f, const v4f (&t)[NI]) {
             const int64_t n = n0 + 16 * f + 4 * (lane >> 4);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)  // the neighbouring lane's
-              t[q] += __int_as_float(
-                  __builtin_amdgcn_mov_dpp(__float_as_int(t[q]), 0xB1, 0xF, 0xF, false));
-            if ((r & 1) == 0 && r < rows && n < N)
-              publish4(p.part + (int64_t)list[c0 + (r >> 1)] * N + n, t);
+            for (int i = 0; i < NI; ++i) {
+              const int r = 16 * i + fr;
+              const v4f next = t[i + 1 < NI ? i + 1 : i];
+              v4f s = t[i];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                s[q] += after<1>(t[i][q], next[q], fr) + after<2>(t[i][q], next[q], fr);
+              if (r % kParts != 0 || r >= rows || n >= N) continue;
+              float* d = p.part + (int64_t)list[c0 + r / kParts] * N + n;
+              if (p.u0 > 0) s += *reinterpret_cast<const v4f*>(d);  // of the launch before
+              publish4(d, s);
+            }
           });
     });
   }
+  if (p.u0 + K < p.I) return;
   if (!arrive_last(&p.counters[blockIdx.x], active, &s_last)) return;
   for (int q = threadIdx.x; q < p.T * 4 * NF; q += Engine::THREADS) {
     const int t = q / (4 * NF);
@@ -405,23 +446,32 @@ __global__ void __launch_bounds__(Engine::THREADS, Engine::WAVES) moe_down_kerne
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
+// Bytes of hidden values at a time: with the down product's sums they stay in
+// the L2s (32 MiB together), and the workspace of 512 pairs of 4096 x 11008
+// stays below 32 MiB.  A chunk then has thousands of units, beside whose weights
+// two more launches are little.
+constexpr int64_t kMaxHidden = 20 << 20;
+
 struct MoeLayout {
+  int64_t chunk;  // hidden units at a time: all, or whole K blocks
   size_t tables, h, part, total;
 };
 MoeLayout moe_layout(int T, int E, int k, int64_t H, int64_t I) {
   MoeLayout l;
+  const int64_t pairs = (int64_t)T * k, bytes = pairs * I * kParts * 2;
+  const int64_t chunks = (bytes + kMaxHidden - 1) / kMaxHidden;
+  l.chunk = chunks == 1 ? I : ((I + chunks - 1) / chunks + 127) / 128 * 128;
   l.tables = kSplitkCounterBytes;
-  l.h = l.tables + up16((size_t)(4 + 2 * E + T * k) * 4);
-  l.part = l.h + up16((size_t)T * k * I * 4);
-  l.total = l.part + (size_t)T * k * H * 4;
+  l.h = l.tables + up16((size_t)(4 + 2 * E + pairs) * 4);
+  l.part = l.h + up16((size_t)pairs * l.chunk * kParts * 2);
+  l.total = l.part + (size_t)pairs * H * 4;
   return l;
 }
-
 
 template <int BF, int MAXNI, class Engine>
 hipError_t launch_up(const MoeArgs& p, hipStream_t stream) {
   hipLaunchKernelGGL((moe_up_kernel<BF, MAXNI, Engine>),
-                     dim3((unsigned)((2 * p.I + Engine::ROWS_B - 1) / Engine::ROWS_B), (unsigned)p.E),
+                     dim3((unsigned)((2 * p.chunk + Engine::ROWS_B - 1) / Engine::ROWS_B), (unsigned)p.E),
                      dim3(Engine::THREADS), 0, stream, p);
   return hipGetLastError();
 }
@@ -433,16 +483,34 @@ hipError_t launch_down(const MoeArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Measured on an MI355X, us a layer with the weights from HBM:
-//  * up to four tokens 32 weight rows a workgroup, up to 16 tokens 64, whose
-//    waves read their activations half as often: 66.6 against 75.8 (1 token, 8
-//    experts of 4096 x 11008, E4M3), 79.3 / 76.2 (13 tokens, 60 of 2048 x 1408);
-//  * more tokens: activations in LDS, 160 against 191 (64 tokens, 8 experts,
-//    MXFP4), 245 / 260 (E4M3);
-//  * 32 activation rows at a time leave two workgroups a CU (160 against 167
-//    with 64, same layer), but an expert with more rows reads its weights again:
-//    64 at a time where the mean is above 20 rows.
-//  (one BF16 part a hidden value then; with two, 169 us for 64 tokens in MXFP4)
+// Measured on an MI355X, us a layer with the weights from HBM (E4M3, then MXFP4;
+// experts as number of H x I), every alternative of a launch with the best of the
+// other one.
+//
+// gate/up: a row a pair.
+//  * up to four tokens 32 weight rows a workgroup, up to 16 tokens 64, whose waves
+//    read their activations half as often: 125 against 128 (two tokens, 8 of
+//    4096 x 11008, E4M3), 77.9 / 77.6 (13 tokens, 60 of 2048 x 1408);
+//  * more tokens: activations in LDS, 260 / 273 and 179 / 198 (64 tokens, 8 of
+//    4096 x 11008) against two fragments straight from memory; with many small
+//    experts that is no loss to speak of (132 / 134, 64 tokens on 60);
+//  * 32 rows at a time leave two workgroups a CU (260 / 263, 179 / 187, same
+//    layer), but an expert with more rows reads its weights again: 64 at a time
+//    where the mean is above 20 rows (260 / 279, 223 / 227 with 64 rows).
+//
+// down: three rows a pair.
+//  * one or two tokens: 32 weight rows a workgroup (68 / 94 and 51 / 69 for one
+//    token on 8 of 4096 x 11008); with three or four there are experts enough for
+//    128 rows a workgroup, one a CU: 189 / 192 and 131 / 137, 57 / 61 and 44 / 49
+//    (four tokens, 32 of 2048 x 2816);
+//  * up to six pairs an expert in the mean: 10 at a time, two workgroups a CU or
+//    more: 80 / 85 and 60 / 63 (13 tokens, 60 of 2048 x 1408), 160 / 173 and 120 /
+//    134 (64 tokens, top 8 of 128 of 2048 x 768), 224 / 224 and 152 / 151 (16
+//    tokens, 8 of 4096 x 11008);
+//  * more: 32 at a time, 254 / 311 and 166 / 189 (48 tokens, 8 of 4096 x 11008);
+//    in MXFP4 up to ten in the mean 16 at a time, which still leaves two
+//    workgroups a CU: 99 / 104 (64 tokens, top 4 of 32 of 2048 x 2816), but 200 /
+//    179 with 16 in the mean (64 tokens, 8 of 4096 x 11008).
 template <int BF>
 hipError_t launch_experts(const MoeArgs& p, hipStream_t stream) {
   const int pairs = p.T * p.k;
@@ -456,11 +524,11 @@ hipError_t launch_experts(const MoeArgs& p, hipStream_t stream) {
   else
     e = launch_up<BF, 4, SharedEngine<BF, 4>>(p, stream);
   if (e != hipSuccess) return e;
-  // two rows a pair
-  if (p.T <= 4) return launch_down<BF, 1, StreamEngine<BF, 2, 1>>(p, stream);
-  if (p.T <= 16) return launch_down<BF, 2, StreamEngine<BF, 4, 2>>(p, stream);
-  if (pairs <= 10 * p.E) return launch_down<BF, 2, SharedEngine<BF, 2>>(p, stream);
-  return launch_down<BF, 4, SharedEngine<BF, 4>>(p, stream);
+  if (p.T <= 2) return launch_down<BF, 1, StreamEngine<BF, 2, 1>>(p, stream);
+  if (p.T > 4 && pairs <= 6 * p.E) return launch_down<BF, 2, SharedEngine<BF, 2>>(p, stream);
+  if constexpr (BF == FMT_MXFP4)
+    if (p.T > 4 && pairs <= 10 * p.E) return launch_down<BF, 3, SharedEngine<BF, 3, 3>>(p, stream);
+  return launch_down<BF, 6, SharedEngine<BF, 6>>(p, stream);
 }
 
 }  // namespace
@@ -496,10 +564,15 @@ hipError_t launch_moe_layer(const MoeProblem& q, void* workspace, hipStream_t st
   p.h = reinterpret_cast<uint16_t*>(ws + l.h);
   p.part = reinterpret_cast<float*>(ws + l.part);
   hipLaunchKernelGGL(moe_router_kernel, dim3(1), dim3(kRouterThreads), 0, stream, p);
-  const hipError_t e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return q.format == FMT_FP8 ? launch_experts<FMT_FP8>(p, stream)
-                             : launch_experts<FMT_MXFP4>(p, stream);
+  for (p.u0 = 0; p.u0 < p.I; p.u0 += l.chunk) {
+    p.chunk = p.I - p.u0 < l.chunk ? p.I - p.u0 : l.chunk;
+    e = q.format == FMT_FP8 ? launch_experts<FMT_FP8>(p, stream)
+                            : launch_experts<FMT_MXFP4>(p, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace dg

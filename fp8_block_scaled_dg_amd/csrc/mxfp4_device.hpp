@@ -245,11 +245,10 @@ constexpr int kSharedThreads = 512;
 constexpr int kSharedMaxDepth = 6;
 
 // Depth for NI fragments of activation rows: what the slots leave room for in
-// LDS (two workgroups a CU up to NI = 2 and for E4M3 up to 3, else one) and in
-// registers.  Weight bytes in flight a stage and workgroup: 16 KB in 4 bits,
+// LDS (two workgroups a CU up to NI = 2, else one) and in registers.  Weight bytes in flight a stage and workgroup: 16 KB in 4 bits,
 // 32 KB in 8.
 constexpr int shared_depth(int bf, int ni) {
-  if (bf == FMT_FP8) return 3;
+  if (bf == FMT_FP8 || ni > 4) return 3;
   return ni == 1 ? 5 : (ni == 3 ? 6 : 4);
 }
 
@@ -391,7 +390,7 @@ struct Shared {
 
   // Parts part0 + wk of `parts` of K; every wave of the workgroup makes the
   // same number of stages (the barriers), past its run on zeros.
-  // finish(f, i, quad): f in [0, WN NF), each fragment by one wave.
+  // finish(f, quads): f in [0, WN NF), the NI quads of its rows, by one wave.
   template <class Finish>
   __device__ __forceinline__ void run(const StreamOperands& o, int64_t K, int part0, int parts,
                                       uint8_t* const (&slots)[kSharedMaxDepth], Finish&& finish) {
@@ -449,11 +448,13 @@ struct Shared {
 #pragma unroll
     for (int i = 0; i < NI; ++i) red[(wave * NI + i) * 64 + lane] = wk ? acc[0][i] : acc[1][i];
     __syncthreads();
+    v4f t[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const v4f other = red[((wave ^ 4) * NI + i) * 64 + lane];
-      finish(NF * wn + wk, i, wk ? other + acc[1][i] : acc[0][i] + other);
+      t[i] = wk ? other + acc[1][i] : acc[0][i] + other;
     }
+    finish(NF * wn + wk, t);
     __syncthreads();
   }
 };

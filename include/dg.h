@@ -530,9 +530,8 @@ int dg_mxfp4_gemm_nt_bf16a(uint16_t *c, const uint16_t *a, const uint8_t *b, con
  *   A token without an expert gets y = 0.
  *   workspace: dg_moe_layer_workspace_bytes bytes, required, 16-byte aligned,
  *             counter region as for the split-K workspaces.
- * The hidden values h (with their weight) are held as the sum of two BF16
- * numbers, 2^-16 of the value; y is rounded once; all sums
- * are FP32.  Requirements: 1 <= T <= DG_MOE_MAX_TOKENS, 1 <= E <=
+ * The hidden values h (with their weight) keep FP32's 24 bits, as the sum of
+ * three BF16 numbers; y is rounded once; all sums are FP32.  Requirements: 1 <= T <= DG_MOE_MAX_TOKENS, 1 <= E <=
  * DG_MOE_MAX_EXPERTS, 1 <= k <= min(E, DG_MOE_MAX_SLOTS), H <= 131072,
  * I <= 2^20, T * k * I < 2^29; x, y, codes 16-byte, the rest 4-byte aligned.  Deterministic.
  */

@@ -1,0 +1,115 @@
+"""The mixture-of-experts layer keeps its hidden values in FP32: inputs whose
+sums are exact in FP32, whatever their order, have to give y exactly.
+
+The gate of every unit is 32, whose silu is 32 in FP32 (e^-32 is below half a
+step of 1).  up is a sum of a few integers below 2^24, so h = 32 up w (w a power
+of two) is exact and has up to 24 significant bits.  Two neighbouring units
+differ in one small term, and each row of W2 takes the difference of such a
+pair: a multiple of 16 below 256 * 16, which BF16 holds.  Fewer bits of h
+anywhere show in full."""
+import numpy as np
+import pytest
+import torch
+
+import mxfp4_ref as ref
+from gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dg():
+    need_gpu()
+    import fp8_block_scaled_dg_amd as m
+    return m
+
+
+E4M3 = {0: 0x00, 1: 0x38, 2: 0x40, 3: 0x44}
+
+
+def encode(w, fmt):
+    """w [E][N][K] of integers -3 .. 3 -> codes and scales, exactly."""
+    if fmt == "fp8":
+        code = np.vectorize(E4M3.get)(np.abs(w)).astype(np.uint8) | np.where(w < 0, 0x80, 0).astype(np.uint8)
+        E, N, K = w.shape
+        return code, np.ones((E, K // 128, -(-N // 128)), dtype=np.float32)
+    pairs = [ref.quantize(m) for m in w]
+    assert all(np.array_equal(ref.values(q, s), m) for (q, s), m in zip(pairs, w))
+    return np.stack([p[0] for p in pairs]), np.stack([p[1] for p in pairs])
+
+
+def call(dg, x, w13, w2, ids, weights, fmt):
+    (c13, s13), (c2, s2) = encode(w13, fmt), encode(w2, fmt)
+    dev = [torch.from_numpy(np.ascontiguousarray(t)).cuda() for t in (c13, c2, s13, s2, ids, weights)]
+    T, H = x.shape
+    ws = dg.alloc_workspace(dg.dg_moe_layer_workspace_bytes(T, w13.shape[0], ids.shape[1], H, w2.shape[2]))
+    y = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_moe_layer(y, torch.from_numpy(x).to(torch.bfloat16).cuda(), *dev[:4], *dev[4:], workspace=ws)
+    assert not ws[:dg.WORKSPACE_COUNTER_BYTES].any()
+    return y.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp4"])
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 2, 1, 128, 128), (3, 3, 2, 256, 384), (4, 1, 1, 128, 640),
+                                       (8, 4, 2, 256, 256), (16, 1, 1, 128, 384), (17, 3, 2, 128, 1152),
+                                       (40, 2, 2, 256, 640), (64, 8, 2, 128, 896), (64, 2, 2, 256, 1408),
+                                       # hidden units in two chunks and in three
+                                       (64, 8, 8, 128, 7040), (64, 16, 16, 128, 7040)])
+def test_h_is_not_rounded(dg, T, E, k, H, I, fmt):
+    if fmt == "mxfp4":
+        H, I = H + 32, I - 32
+    rng = np.random.default_rng(T * H + I)
+    x = np.zeros((T, H))
+    x[:, 0] = 32
+    x[:, 1:9] = rng.integers(1, 10, (T, 8)) if k <= 2 else 1
+    x[:, 9:] = rng.integers(-255, 256, (T, H - 9)) * 2.0 ** (4 * rng.integers(0, 4, H - 9))
+    w13 = np.zeros((E, 2 * I, H))
+    w13[:, 0::2, 0] = 1
+    for e in range(E):
+        for i in range(0, I, 2):
+            cols = rng.choice(np.arange(9, H), 3, replace=False)
+            w13[e, [2 * i + 1, 2 * i + 3], :] = 0
+            for c, v in zip(cols, rng.choice([-3, -2, -1, 1, 2, 3], 3)):
+                w13[e, [2 * i + 1, 2 * i + 3], c] = v
+            w13[e, 2 * i + 1, rng.integers(1, 9)] = rng.choice([-3, -2, -1, 1, 2, 3])
+    w2 = np.zeros((E, H, I))
+    for e in range(E):
+        i = 2 * rng.integers(0, I // 2, H)
+        i[:min(H, I // 2)] = 2 * rng.permutation(I // 2)[:H]
+        sign = rng.choice([-1, 1], H)
+        w2[e, np.arange(H), i], w2[e, np.arange(H), i + 1] = sign, -sign
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    weights = rng.choice([0.5, 1.0, 2.0], (T, k)).astype(np.float32)
+    want = np.zeros((T, H))
+    for t in range(T):
+        for j, e in enumerate(ids[t]):
+            up = w13[e, 1::2] @ x[t]
+            assert np.abs(up).max() < 2 ** 24
+            want[t] += w2[e] @ (32 * up * weights[t, j])
+    assert np.array_equal(want, np.round(want / 16) * 16) and np.abs(want).max() < 4096
+    assert np.array_equal(call(dg, x, w13, w2, ids, weights, fmt), want)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp4"])
+@pytest.mark.parametrize("T", [2, 16, 40])
+def test_infinite_and_largest_h(dg, T, fmt):
+    """h that overflows FP32 is infinite and makes y infinite (not NaN) where
+    its weight is not 0; NaN stays NaN; the largest h below that stays finite."""
+    E, H, I = 1, 128, 128
+    x = np.zeros((T, H))
+    x[0, 0] = x[0, 1] = 2.0 ** 70             # unit 0: 2^140
+    x[1, 2] = x[1, 3] = 2.0 ** 63             # unit 1: 2^126 (e^-2^63 is 0), three times
+    w13, w2 = np.zeros((E, 2 * I, H)), np.zeros((E, H, I))
+    w13[0, 0, 0] = w13[0, 1, 1] = w13[0, 2, 2] = 1
+    w13[0, 3, 3] = 3
+    n = np.arange(H)
+    w2[0, :, 0] = np.where(n % 2, -1, 1)
+    w2[0, :, 1] = np.where(n % 3, -1, 1)
+    ids, weights = np.zeros((T, 1), dtype=np.int32), np.ones((T, 1), dtype=np.float32)
+    y = call(dg, x, w13, w2, ids, weights, fmt)
+    assert np.array_equal(y[0], np.where(n % 2, -np.inf, np.inf))
+    assert np.array_equal(y[1], np.where(n % 3, -1, 1) * 3 * 2.0 ** 126)
+    assert not y[2:].any()
+    x[0, 1] = np.nan
+    y = call(dg, x, w13, w2, ids, weights, fmt)
+    assert np.isnan(y[0]).all() and np.isfinite(y[1:]).all()
