@@ -49,12 +49,22 @@ def call(dg, x, w13, w2, ids, weights, fmt):
     return y.double().cpu().numpy()
 
 
+SHORT = [(1, 2, 1, 128, 128), (3, 3, 2, 256, 384), (4, 1, 1, 128, 640), (8, 4, 2, 256, 256),
+         (16, 1, 1, 128, 384), (17, 3, 2, 128, 1152), (40, 2, 2, 256, 640), (64, 8, 2, 128, 896),
+         (64, 2, 2, 256, 1408)]
+# hidden units in two chunks and in three
+CHUNKS = [(64, 8, 8, 128, 7040), (64, 16, 16, 128, 7040)]
+# K blocks of gate/up and of down in every remainder by the depths of the LDS
+# rings (a stage is two blocks), from below one round to several; each pair of
+# tokens and experts gets other kernels
+LONG = [(T, E, k, 128 * n, 128 * m) for T, E, k in ((2, 2, 2), (3, 2, 2), (13, 4, 2), (17, 8, 2), (24, 6, 2),
+                                                    (64, 2, 2))
+        for n, m in ((2, 17), (3, 16), (5, 14), (7, 12), (9, 9), (11, 7), (13, 5), (15, 4))]
+LAYERS = SHORT + CHUNKS + LONG
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "mxfp4"])
-@pytest.mark.parametrize("T,E,k,H,I", [(1, 2, 1, 128, 128), (3, 3, 2, 256, 384), (4, 1, 1, 128, 640),
-                                       (8, 4, 2, 256, 256), (16, 1, 1, 128, 384), (17, 3, 2, 128, 1152),
-                                       (40, 2, 2, 256, 640), (64, 8, 2, 128, 896), (64, 2, 2, 256, 1408),
-                                       # hidden units in two chunks and in three
-                                       (64, 8, 8, 128, 7040), (64, 16, 16, 128, 7040)])
+@pytest.mark.parametrize("T,E,k,H,I", LAYERS)
 def test_h_is_not_rounded(dg, T, E, k, H, I, fmt):
     if fmt == "mxfp4":
         H, I = H + 32, I - 32
@@ -113,3 +123,36 @@ def test_infinite_and_largest_h(dg, T, fmt):
     x[0, 1] = np.nan
     y = call(dg, x, w13, w2, ids, weights, fmt)
     assert np.isnan(y[0]).all() and np.isfinite(y[1:]).all()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp4"])
+@pytest.mark.parametrize("T,E", [(2, 2), (4, 2), (13, 4), (17, 8), (24, 6), (64, 2)])
+def test_nan_weights(dg, T, E, fmt):
+    """A NaN in an expert's W13 (E4M3: a code, MXFP4: a scale byte) makes y NaN
+    for the tokens that chose it, one in W2 its column of y for them; nothing
+    else changes."""
+    k, H, I = 2, 256, 384
+    rng = np.random.default_rng(T)
+    w13, w2 = rng.integers(-3, 4, (E, 2 * I, H)), rng.integers(-3, 4, (E, H, I))
+    (c13, s13), (c2, s2) = encode(w13, fmt), encode(w2, fmt)
+    x = torch.from_numpy(rng.integers(-4, 5, (T, H)) / 256).to(torch.bfloat16).cuda()
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    if E > 2:
+        ids[0] = (2, 3)
+    ws = dg.alloc_workspace(dg.dg_moe_layer_workspace_bytes(T, E, k, H, I))
+
+    def run():
+        d = [torch.from_numpy(np.ascontiguousarray(t)).cuda() for t in (c13, c2, s13, s2, ids)]
+        y = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+        dg.dg_moe_layer(y, x, *d, torch.ones(T, k, device="cuda"), workspace=ws)
+        return y.double().cpu().numpy()
+    want = run()
+    assert np.isfinite(want).all()
+    if fmt == "fp8":
+        c13[0, 2 * 100 + 1, 130], c2[1, 77, 300] = 0x7F, 0xFF
+    else:
+        s13.view(np.uint8).reshape(E, 2, 2 * I, 4)[0, 1, 2 * 100 + 1, 0] = 255
+        s2.view(np.uint8).reshape(E, 3, H, 4)[1, 2, 77, 1] = 255
+    want[(ids == 1).any(1), 77] = np.nan
+    want[(ids == 0).any(1)] = np.nan
+    assert np.array_equal(run(), want, equal_nan=True)
