@@ -3,7 +3,7 @@
 // B in MXFP4 (mxfp4_device.hpp), A in MXFP4 or in BF16.
 //
 // Three kernels for up to 64 rows of A, whose time is the stream of B from HBM
-// (1 x 7168 x 16384 in 13.9 us: 4.5 TB/s with the launch in it); larger M goes
+// (1 x 7168 x 16384 in 12.9 us: 4.8 TB/s with the launch in it); larger M goes
 // to gemm_mxfp4_tiled.hip.
 //
 // gemm_mxfp4_stream_kernel: a workgroup's four waves take the same 16 NF rows
@@ -17,7 +17,6 @@
 namespace dg {
 namespace {
 
-constexpr int kMaxCounters = (int)(kSplitkCounterBytes / 4);
 constexpr int kWaves = 4;
 
 struct Mxfp4Args {
@@ -367,24 +366,25 @@ struct StreamPlan {
   int64_t tiles_n;
 };
 
-// Measured on an MI355X, us with the weights from HBM (M x N x K):
+// Measured on an MI355X, us, every call with weights of its own, 1.2 GB in all
+// (M x N x K):
 //  * MXFP4 activations, K from 16 stages of 256 on and 100 workgroups: rings in
-//    LDS, 13.9 against 19.5 (1 x 7168 x 16384), 18.5 / 28.9 (33) and 22.5 / 36
-//    (64), 11.3 / 14.2 (64 x 4096 x 8192); shorter runs do not pay for one
-//    workgroup a CU: 7.0 / 5.8 (40 x 16384 x 1024), 3.7 / 3.4 (4 x 2048 x
-//    2048), nor do few columns: 8.7 / 7.3 (64 x 512 x 8192, which splits K).
+//    LDS, 12.9 against 15.9 (1 x 7168 x 16384), 17.8 / 24.6 (33) and 22.0 / 31
+//    (64), 11.1 / 13.8 (64 x 4096 x 8192); shorter runs do not pay for one
+//    workgroup a CU: 7.6 / 6.1 (40 x 16384 x 1024), 3.4 / 3.2 (4 x 2048 x
+//    2048), nor do few columns: 8.4 / 7.0 (64 x 512 x 8192, which splits K).
 //  * BF16 activations in LDS from 17 rows on, where N gives workgroups enough:
-//    28 against 44 (33 x 7168 x 16384), 10.2 / 13.6 (20 x 24576 x 1536), 14 /
-//    26 (64 x 24576 x 1536); up to 16 rows straight into fragments: 18.7 / 44
-//    (1 x 7168 x 16384), 5.5 / 7.6 (16 x 7168 x 2048), and for few columns
-//    10.2 / 15 (64 x 512 x 8192).
-//  * 32 rows of B a workgroup where that leaves 192 workgroups, else 16: 5.6 /
-//    7.3 (16 x 7168 x 2048, BF16), but 5.2 / 4.4 (8 x 4096 x 4096).
-//  * BF16, two K blocks a buffer for long runs of few rows: 18.7 / 19.9 (1 x
-//    7168 x 16384); 9.0 / 8.5 on short ones (1 x 24576 x 1536).
-//  * K parts cost about 4 us, so they have to save more: 7.3 / 11.9 in four
-//    (64 x 512 x 8192, MXFP4); with LDS 28 / 62 in four (33 x 7168 x 16384),
-//    but 28 / 14 in two (64 x 24576 x 1536: 192 workgroups already).
+//    27 against 73 (33 x 7168 x 16384), 9.7 / 13.4 (20 x 24576 x 1536), 13.6 /
+//    43 (64 x 24576 x 1536); up to 16 rows straight into fragments: 18.7 / 22
+//    (1 x 7168 x 16384), 5.9 / 7.8 (16 x 7168 x 2048), and for few columns
+//    9.9 / 15.8 (64 x 512 x 8192).
+//  * 32 rows of B a workgroup where that leaves 192 workgroups, else 16: 5.9 /
+//    7.5 (16 x 7168 x 2048, BF16), but 7.1 / 6.2 (8 x 4096 x 4096, BF16).
+//  * BF16, two K blocks a buffer for long runs of few rows: 18.7 / 19.6 (1 x
+//    7168 x 16384); 8.9 / 8.3 on short ones (1 x 24576 x 1536).
+//  * K parts cost about 4 us, so they have to save more: 7.0 / 11.6 in four
+//    (64 x 512 x 8192, MXFP4); with LDS 27 / 61 in four (33 x 7168 x 16384),
+//    but 26.5 / 13.6 in two (64 x 24576 x 1536: 192 workgroups already).
 StreamPlan stream_plan(int64_t M, int64_t N, int64_t K, bool bf16_a) {
   StreamPlan s;
   const int64_t nkb = (K + 127) / 128;

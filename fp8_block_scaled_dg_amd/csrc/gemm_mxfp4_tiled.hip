@@ -26,8 +26,10 @@
 //
 // MI355X: 8192^3 261 us (4.2 PFLOP/s), 4096 x 7168 x 2048 41 us.  A loop of
 // nothing but these instructions on random codes reaches 7.1 PFLOP/s (9.7 on
-// zeros: the clock gives way to power), and in the 8192^3 product the clock is
-// near 1.9 GHz with the matrix cores busy 52 % of the cycles.  L2 requests fell
+// zeros: the clock gives way to power).  What holds the 8192^3 product is LDS: a
+// CU reads 96 KB of fragments and takes in 32 KB per 128 K values, 1024 cycles at
+// 128 bytes each, as many as its matrix instructions last; the two overlap in
+// part, and the matrix cores are busy 52 % of the cycles, at 1.9 GHz.  L2 requests fell
 // by half with 128-byte rows (34 to 18 million, 298 to 273 us); deeper rings of
 // 64-byte rows, smaller tiles side by side and four waves of 128 x 128 (512
 // registers, spilling) were slower.
@@ -315,18 +317,19 @@ hipError_t launch(TileArgs p, hipStream_t stream) {
 
 // One 256 x 256 tile a CU or two of 128 x 128.  The large one moves half as
 // much per product, but needs tiles enough for whole rounds of the 256 CUs:
-// 273 against 319 us (8192^3), 27 / 32 (4096 x 4096 x 2016: one round), 45 /
-// 47 (4096 x 7168 x 2048: 1.75 rounds), but 29.5 / 27.8 (3000 x 8192 x 1024:
-// 1.5) and 33 / 25 (2001 x 4096 x 4096: half a round).
+// 263 against 326 us (8192^3), 26 / 30.5 (4096 x 4096 x 2016: one round), 43 /
+// 44 (4096 x 7168 x 2048: 1.75 rounds), but 28.4 / 26.1 (3000 x 8192 x 1024:
+// 1.5) and 32 / 26 (2001 x 4096 x 4096: half a round).
 bool large_tiles(int64_t M, int64_t N) {
   const int64_t t = ((M + 255) / 256) * ((N + 255) / 256), rounds = (t + 255) / 256;
   return 5 * t >= 4 * 256 * rounds;
 }
 
 // Parts of K for few small tiles.  A 256-wide stage takes 0.7 us here, meeting
-// in the workspace 6 to 8 us, so a part keeps 12 stages: 30 against 47 us (128
-// x 7168 x 16384 in four), 17 / 20 (128 x 1024 x 8192), but 15.1 / 12.3 (65 x
-// 4096 x 4096 in two of 8 stages).
+// in the workspace 6 to 8 us, so a part keeps 12 stages: 35 against 64 us (128
+// x 7168 x 16384 in four; 31 / 49 with the operands in the 256 MB cache, as a
+// quantiser leaves them), 23 / 31 (19.5 / 24.4) (128 x 1024 x 8192 in two).  Of
+// 8 stages: 16.8 / 18.4, but 15.1 / 14.3 from the cache (65 x 4096 x 4096 in two).
 int tile_split(int64_t M, int64_t N, int64_t K) {
   if (large_tiles(M, N)) return 1;
   const int64_t t = ((M + 127) / 128) * ((N + 127) / 128), nk = (K + 255) / 256;

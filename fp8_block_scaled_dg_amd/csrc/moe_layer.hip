@@ -16,7 +16,7 @@
 // units in chunks, down adding to what it has.
 //
 // MI355X, kernels alone (router, up, down): 1 token on 8 experts of 4096 x
-// 11008 in E4M3 4.5 + 36 + 22 us (180 MB at 5.0 TB/s, 90 MB at 4.1); 64 tokens
+// 11008 in E4M3 4.7 + 37 + 23 us at best (180 MB at 4.9 TB/s, 90 MB at 4.0); 64 tokens
 // on the same experts in MXFP4 9 + 98 + 80 us (383 MB at 3.9 TB/s, 191 MB at
 // 2.4: 256 workgroups of 128 weight rows, one a CU, whose LDS reads and products
 // for 20 pairs, 60 rows, no longer hide behind the weights; 65 us when h had two
@@ -30,8 +30,8 @@ constexpr int kWaves = 4;
 constexpr int kRouterThreads = 1024;
 constexpr int kParts = 3;  // BF16 numbers that hold a hidden value
 
-// Routing tables in the workspace: counts [E], then per expert a list of
-// pairs t * k + j (ascending), offsets [E] into one array of T k entries.
+// Routing tables in the workspace: counts [E], offsets [E] into one array of T k
+// entries, and there each expert's list of pairs t * k + j, in any order.
 struct MoeTables {
   int* active;    // workgroups of the down launch that have work, per column tile
   int* counts;    // [E]
@@ -60,7 +60,7 @@ struct MoeArgs {
 };
 
 // Largest value of the wave, in every lane (no NaN among them).
-__device__ __forceinline__ float wave_max(float v) {
+__device__ __forceinline__ float wave_top(float v) {
   auto join = [](float x, int y) { return fmaxf(x, __int_as_float(y)); };
   const auto dpp = [](float x, auto ctrl) {
     return __builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, false);
@@ -107,7 +107,7 @@ __device__ __forceinline__ void route_token(const MoeArgs& p, int t, int lane, i
         b = v[q];
         bi = q;
       }
-    const float top = wave_max(b);
+    const float top = wave_top(b);
     if (top == -INFINITY) break;  // wave-uniform
     const int owner = __ffsll((unsigned long long)__ballot(b == top)) - 1;
     const int id = owner * PER + __builtin_amdgcn_readlane(bi, owner);

@@ -239,8 +239,8 @@ struct Stream {
 // registers, the activations' in R LDS slots, so R - 1 are in flight while one
 // is multiplied; one barrier a stage tells that every wave's DMA of it has
 // landed and that the slot of the stage before is free.
-// MI355X: BF16 A 33 x 7168 x 16384 24.7 us, of which about 6 are the K parts
-// meeting in memory; the layer's gate/up 95 us for 383 MB.
+// MI355X: BF16 A 33 x 7168 x 16384 27 us with the weights from HBM, of which
+// about 6 are the K parts meeting in memory; the layer's gate/up 98 us for 383 MB.
 constexpr int kSharedThreads = 512;
 constexpr int kSharedMaxDepth = 6;
 

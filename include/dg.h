@@ -487,8 +487,8 @@ int dg_dequantize_mxfp4(void *out, int dtype, const uint8_t *q, const int32_t *s
  * makes its row's (column's) outputs NaN.
  *   workspace : optional split-K scratch of
  *               dg_mxfp4_gemm_nt_workspace_bytes(M, N, K) bytes, as for
- *               dg_fp8_gemm_nt; without one (or with a smaller one:
- *               DG_ERR_WORKSPACE) the plan does not split K.
+ *               dg_fp8_gemm_nt; without one (NULL or 0 bytes) the plan does
+ *               not split K, a smaller one is refused (DG_ERR_WORKSPACE).
  * Requirements: M, N >= 1; M * N <= 2^44; 32 <= K <= 2^23; M * ceil(K/128) and
  * N * ceil(K/128) < 2^29; c and codes 16-byte, scales 4-byte aligned.  Deterministic.
  */
