@@ -599,6 +599,15 @@ def mxfp4_shapes(rows: int, cols: int):
     return (rows, cdiv(cols, 32) * 16), (cdiv(cols, 128), rows)
 
 
+def _mxfp4_matrix(q, what):
+    """(rows, values a row) of a matrix of codes."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % what)
+    if q.dim() != 2:
+        raise ValueError("%s must be a matrix of codes" % what)
+    return q.shape[0], 2 * q.shape[1]
+
+
 def _mxfp4_pair(q, sf, rows, cols, what):
     _require(q, torch.uint8, what)
     _require(sf, torch.int32, "scales of " + what)
@@ -651,8 +660,8 @@ def dg_mxfp4_gemm_nt(c, a, b, sfa, sfb, workspace=None, stream=None) -> None:
     """C[M,N] (bf16) = A . B^T, both MXFP4 (codes [M, K/2] and [N, K/2])."""
     c = _bf16(c, "c")
     M, N = c.shape
-    K = 2 * a.shape[1]
-    if a.shape[0] != M or b.shape != (N, K // 2):
+    rows, K = _mxfp4_matrix(a, "a")
+    if rows != M or _mxfp4_matrix(b, "b") != (N, K):
         raise ValueError("shape mismatch: a %s, b %s, c %s" % (tuple(a.shape), tuple(b.shape),
                                                               tuple(c.shape)))
     _mxfp4_pair(a, sfa, M, K, "a")
@@ -675,8 +684,8 @@ def dg_mxfp4_gemm_nt_bf16a(c, a, b, sfb, workspace=None, stream=None) -> None:
     c = _bf16(c, "c")
     a = _bf16(a, "a")
     M, K = a.shape
-    N = b.shape[0]
-    if b.shape != (N, K // 2) or c.shape != (M, N):
+    N, per_row = _mxfp4_matrix(b, "b")
+    if per_row != K or c.shape != (M, N):
         raise ValueError("shape mismatch: a %s, b %s, c %s" % (tuple(a.shape), tuple(b.shape),
                                                               tuple(c.shape)))
     _mxfp4_pair(b, sfb, N, K, "b")
@@ -713,10 +722,12 @@ def dg_moe_layer(y, x, w13, w2, s13, s2, ids, weights, logits=None, scoring: str
     _require(s2, s13.dtype, "s2")
     _require(ids, torch.int32, "ids")
     _require(weights, torch.float32, "weights")
+    if w13.dim() != 3 or ids.dim() != 2:
+        raise ValueError("w13 must be [E, 2I, ..] and ids [T, k]")
     T, H = x.shape
     E = w13.shape[0]
     I = w13.shape[1] // 2
-    k = ids.shape[-1]
+    k = ids.shape[1]
     per = 1 if fp8 else 2
     scales = (((E, cdiv(H, 128), cdiv(2 * I, 128)), (E, cdiv(I, 128), cdiv(H, 128))) if fp8 else
               ((E, cdiv(H, 128), 2 * I), (E, cdiv(I, 128), H)))
@@ -802,14 +813,15 @@ def to_mxfp4_both(x):
 
 def from_mxfp4(q, sf, cols: int, dtype=torch.bfloat16):
     """The values [rows, cols] of MXFP4 codes q and scales sf."""
-    out = torch.empty((q.shape[0], cols), dtype=dtype, device=q.device)
+    out = torch.empty((_mxfp4_matrix(q, "q")[0], cols), dtype=dtype, device=q.device)
     dg_dequantize_mxfp4(out, q, sf)
     return out
 
 
 def mxfp4_gemm_nt(a, b, sfa, sfb, workspace=None):
     """A . B^T of two MXFP4 matrices -> bfloat16 [M, N]."""
-    c = torch.empty((a.shape[0], b.shape[0]), dtype=torch.bfloat16, device=a.device)
+    M, N = _mxfp4_matrix(a, "a")[0], _mxfp4_matrix(b, "b")[0]
+    c = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     dg_mxfp4_gemm_nt(c, a, b, sfa, sfb, workspace)
     return c
 
