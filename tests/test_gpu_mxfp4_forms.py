@@ -27,7 +27,8 @@ PRODUCTS = LARGE_TILES + WIDE_STREAM + RINGS + [(100, 129, 2016), (257, 300, 123
 WIDE_STREAM_BF16A = [(1, 6113, 544), (16, 8201, 1056), (3, 6113, 8224), (16, 8200, 8160)]
 # activations in LDS: stages of every remainder by the depth, with and without
 # a whole round of the ring, N and K with tails
-SHARED_BF16A = [(M, 2049 + 2 * s, 256 * s - 96 + 32 * (s % 3)) for M in (17, 33, 49) for s in range(1, 14)]
+SHARED_BF16A = [(M, 2049 + 2 * s, 256 * s - 96 + 32 * (s % 3))
+                for M, last in ((17, 9), (33, 13), (49, 9)) for s in range(1, last + 1)]
 BF16A = WIDE_STREAM_BF16A + SHARED_BF16A + [(16, 300, 2080), (48, 65, 544)]
 # row direction, four passes a workgroup (from 2^24 values on)
 MANY_ROWS = [(4101, 4111), (131075, 131)]
