@@ -551,7 +551,7 @@ static_assert(131072 / 16 * 4 <= DG_WORKSPACE_COUNTER_BYTES, "counters of the la
 bool moe_shape_ok(int T, int E, int k, int64_t H, int64_t I) {
   return T >= 1 && T <= DG_MOE_MAX_TOKENS && E >= 1 && E <= DG_MOE_MAX_EXPERTS && k >= 1 &&
          k <= E && k <= DG_MOE_MAX_SLOTS && H >= 32 && H <= 131072 && I >= 32 &&
-         I <= (int64_t(1) << 20) && int64_t(T) * k * I < (int64_t(1) << 29) &&  // h: below 2^31 bytes
+         I <= (int64_t(1) << 20) && int64_t(T) * k * I < (int64_t(1) << 29) &&  // as dg.h says
          scale_words_ok(2 * I, H) && scale_words_ok(H, I);
 }
 

@@ -525,7 +525,8 @@ int dg_mxfp4_gemm_nt_bf16a(uint16_t *c, const uint16_t *a, const uint8_t *b, con
  *             in descending order (ties: lowest index) and their scores
  *             (scoring DG_MOE_SOFTMAX or DG_MOE_SIGMOID) divided by their sum.
  *             Logits of -inf or NaN are never chosen; slots without an expert
- *             get id -1 and weight 0.  NULL: ids and weights are inputs, an
+ *             get id -1 and weight 0.  With the softmax, +inf makes its token's
+ *             weights NaN, as e^(inf - inf) is.  NULL: ids and weights are inputs, an
  *             id outside [0, E) is an empty slot, scoring is ignored.
  *   A token without an expert gets y = 0.
  *   workspace: dg_moe_layer_workspace_bytes bytes, required, 16-byte aligned,
