@@ -13,6 +13,9 @@ Entry points (same names as the C ABI):
     dg_quantize_mxfp4(x, q, sf, qt, sft), dg_dequantize_mxfp4(out, q, sf)
     dg_mxfp4_gemm_nt(c, a, b, sfa, sfb), dg_mxfp4_gemm_nt_bf16a(c, a, b, sfb)
     dg_moe_layer(y, x, w13, w2, s13, s2, ids, weights, logits)
+    dg_moe_route(ids, weights, logits), dg_moe_plan(rows, pairs, m_indices, offsets, counts, ids),
+    dg_moe_dispatch_fp8(a, sa, x, rows, pairs), dg_moe_combine(y, c, rows, weights),
+    dg_swiglu_fp8(h, sh, gu), dg_transpose_fp8_blocks(qt, st, q, s), and the backward calls
     (and the UE8M0, fused-A, epilogue, layout and K-grouped entry points)
 Conveniences mirroring the DeepGEMM page's Python API (pzsr.cn, s4.1):
     to_fp8(x, block_rows=128) -> (q, scales)
@@ -20,6 +23,7 @@ Conveniences mirroring the DeepGEMM page's Python API (pzsr.cn, s4.1):
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -125,6 +129,32 @@ def _load():
     lib.dg_moe_layer.restype = i32
     lib.dg_moe_layer.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i64,
                                  i64, vp, sz, vp]
+    f32 = ctypes.c_float
+    lib.dg_moe_route.restype = i32
+    lib.dg_moe_route.argtypes = [vp, vp, vp, i32, i64, vp, i32, i32, i32, i32, i32, f32, i64, i32,
+                                 i32, vp]
+    lib.dg_moe_route_backward.restype = i32
+    lib.dg_moe_route_backward.argtypes = [vp, i64, vp, vp, vp, i32, i64, i32, i32, f32, i64, i32,
+                                          i32, vp]
+    lib.dg_moe_plan_rows.restype = i64
+    lib.dg_moe_plan_rows.argtypes = [i64, i32, i32]
+    lib.dg_moe_plan_workspace_bytes.restype = sz
+    lib.dg_moe_plan_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.dg_moe_plan.restype = i32
+    lib.dg_moe_plan.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, vp, sz, vp]
+    lib.dg_moe_dispatch_fp8.restype = i32
+    lib.dg_moe_dispatch_fp8.argtypes = [vp, vp, vp, i32, i64, vp, vp, vp, i64, i32, i64, i64, vp]
+    lib.dg_moe_combine.restype = i32
+    lib.dg_moe_combine.argtypes = [vp, vp, vp, vp, vp, i64, i32, i64, i64, vp]
+    lib.dg_moe_combine_backward.restype = i32
+    lib.dg_moe_combine_backward.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp, vp, i64, i32, i64,
+                                            i64, vp]
+    lib.dg_swiglu_fp8.restype = i32
+    lib.dg_swiglu_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, vp]
+    lib.dg_swiglu_fp8_backward.restype = i32
+    lib.dg_swiglu_fp8_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp]
+    lib.dg_transpose_fp8_blocks.restype = i32
+    lib.dg_transpose_fp8_blocks.argtypes = [vp, vp, i32, vp, vp, vp, i64, i64, vp]
     if lib.dg_abi_version() != ABI_VERSION:
         raise ImportError("libdg ABI %d != binding ABI %d" % (lib.dg_abi_version(), ABI_VERSION))
     return lib
@@ -746,6 +776,249 @@ def dg_moe_layer(y, x, w13, w2, s13, s2, ids, weights, logits=None, scoring: str
 
 
 # ---------------------------------------------------------------------------
+# Around the grouped products: routing, layout, dispatch, combine, SwiGLU
+# ---------------------------------------------------------------------------
+
+def _shaped(t, dtype, shape, name):
+    _require(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _fp8_pair(q, s, rows, cols, name):
+    """Codes [rows, cols] and their 1 x 128 scales."""
+    _codes(q, name)
+    if q.shape != (rows, cols):
+        raise ValueError("%s must be %s, got %s" % (name, (rows, cols), tuple(q.shape)))
+    _shaped(s, torch.float32, (cdiv(cols, 128), rows), "scales of " + name)
+
+
+def _rows_of_any_stride(x, name, dtypes=_DTYPES):
+    """(rows, columns, row stride) of a device matrix with contiguous rows."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in dtypes:
+        raise TypeError("%s must be a tensor of %s" % (name, " or ".join(map(str, dtypes))))
+    if not x.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if x.dim() != 2:
+        raise ValueError("%s must be a matrix" % name)
+    rows, cols = x.shape
+    ld, one = x.stride()
+    if cols > 1 and one != 1 or rows > 1 and ld < cols:
+        raise ValueError("the rows of %s must be contiguous and must not overlap" % name)
+    return rows, cols, ld if rows > 1 else cols
+
+
+def _same_device(first, *others):
+    """The launch goes to the current device: its tensors have to be there."""
+    if first.device.index != torch._C._cuda_getDevice():
+        raise ValueError("the tensors are on %s, which is not the current device" % first.device)
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("tensors on %s and %s" % (first.device, t.device))
+
+
+def dg_moe_route(ids, weights, logits, bias=None, scoring: str = "softmax", groups: int = 1,
+                 top_groups=None, group_best: int = 1, renormalise: bool = True,
+                 scale: float = 1.0, stream=None) -> None:
+    """ids int32 [T, k], weights float32 [T, k] = the k experts of each token
+    and their weights from logits [T, E] (float32 or bfloat16, any row
+    stride).  bias float32 [E] is added to the scores for the choice alone;
+    of `groups` groups of experts the top_groups (default: all) with the
+    largest sums of their group_best largest choice values stay."""
+    T, E, ld = _rows_of_any_stride(logits, "logits")
+    _require(ids, torch.int32, "ids")
+    _require(weights, torch.float32, "weights")
+    if ids.dim() != 2 or ids.shape[0] != T or weights.shape != ids.shape:
+        raise ValueError("ids and weights must be [T, k]")
+    if bias is not None:
+        _shaped(bias, torch.float32, (E,), "bias")
+    _same_device(logits, ids, weights, bias)
+    _check(lib.dg_moe_route(_ptr(ids), _ptr(weights), _ptr(logits), _DTYPES[logits.dtype], ld,
+                            _ptr(bias), MOE_SCORINGS[scoring], groups,
+                            groups if top_groups is None else top_groups, group_best,
+                            bool(renormalise), scale, T, E, ids.shape[1], _stream(stream)),
+           "dg_moe_route")
+
+
+def dg_moe_route_backward(dlogits, dweights, ids, logits, scoring: str = "softmax",
+                          renormalise: bool = True, scale: float = 1.0, stream=None) -> None:
+    """dlogits [T, E] (the type of logits, any row stride) from dweights
+    float32 [T, k] and the forward call's ids, logits and settings."""
+    T, E, ld = _rows_of_any_stride(logits, "logits")
+    if _rows_of_any_stride(dlogits, "dlogits", (logits.dtype,))[:2] != (T, E):
+        raise ValueError("dlogits must be [T, E]")
+    _require(ids, torch.int32, "ids")
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError("ids must be [T, k]")
+    _shaped(dweights, torch.float32, ids.shape, "dweights")
+    _same_device(logits, dlogits, ids, dweights)
+    _check(lib.dg_moe_route_backward(_ptr(dlogits), dlogits.stride(0) if T > 1 else E,
+                                     _ptr(dweights), _ptr(ids), _ptr(logits),
+                                     _DTYPES[logits.dtype], ld, MOE_SCORINGS[scoring],
+                                     bool(renormalise), scale, T, E, ids.shape[1],
+                                     _stream(stream)), "dg_moe_route_backward")
+
+
+def dg_moe_plan_rows(T: int, E: int, k: int) -> int:
+    return lib.dg_moe_plan_rows(T, E, k)
+
+
+def dg_moe_plan_workspace_bytes(T: int, E: int, k: int) -> int:
+    return lib.dg_moe_plan_workspace_bytes(T, E, k)
+
+
+def dg_moe_plan(rows, pairs, m_indices, offsets, counts, ids, workspace=None, stream=None) -> None:
+    """The grouped products' layout from ids int32 [T, k] (the experts of each
+    token, < 0 or >= E: none): rows int32 [T, k], pairs and m_indices int32 [M],
+    offsets int64 [E + 1], counts int32 [E]; M a multiple of 128, at least
+    dg_moe_plan_rows(T, E, k).  workspace: dg_moe_plan_workspace_bytes(T, E, k)
+    bytes of any contents."""
+    for t, name in ((ids, "ids"), (pairs, "pairs"), (counts, "counts")):
+        _require(t, torch.int32, name)
+    if ids.dim() != 2 or pairs.dim() != 1 or counts.dim() != 1:
+        raise ValueError("ids must be [T, k], pairs [M] and counts [E]")
+    (T, k), M, E = ids.shape, pairs.numel(), counts.numel()
+    _shaped(rows, torch.int32, ids.shape, "rows")
+    _shaped(m_indices, torch.int32, pairs.shape, "m_indices")
+    _shaped(offsets, torch.int64, (E + 1,), "offsets")
+    _same_device(ids, rows, pairs, m_indices, offsets, counts, workspace)
+    _check(lib.dg_moe_plan(_ptr(rows), _ptr(pairs), _ptr(m_indices), _ptr(offsets), _ptr(counts),
+                           _ptr(ids), T, E, k, M, _ptr(workspace), _workspace_bytes(workspace),
+                           _stream(stream)), "dg_moe_plan")
+
+
+def _slots(rows, weights, T):
+    _require(rows, torch.int32, "rows")
+    if rows.dim() != 2 or rows.shape[0] != T:
+        raise ValueError("rows must be [T, k]")
+    if weights is not None:
+        _shaped(weights, torch.float32, rows.shape, "weights")
+    return rows.shape[1]
+
+
+def dg_moe_dispatch_fp8(a, sa, x, rows, pairs, weights=None, stream=None) -> None:
+    """a (codes [M, H]) and sa float32 [H/128, M] = the rows of x [T, H]
+    (float32 or bfloat16, any row stride), times weights float32 [T, k] if
+    given, quantised with 1 x 128 scales, at the rows of a dg_moe_plan."""
+    T, H, ld = _rows_of_any_stride(x, "x")
+    k = _slots(rows, weights, T)
+    _require(pairs, torch.int32, "pairs")
+    M = pairs.numel()
+    _fp8_pair(a, sa, M, H, "a")
+    _same_device(x, a, sa, rows, pairs, weights)
+    _check(lib.dg_moe_dispatch_fp8(_ptr(a), _ptr(sa), _ptr(x), _DTYPES[x.dtype], ld, _ptr(rows),
+                                   _ptr(pairs), _ptr(weights), T, k, M, H, _stream(stream)),
+           "dg_moe_dispatch_fp8")
+
+
+def dg_moe_combine(y, c, rows, weights=None, residual=None, stream=None) -> None:
+    """y [T, H] (bf16) = sum over the slots of weights (float32 [T, k], or all
+    1) times the rows of c [M, H] (bf16), plus residual [T, H] (bf16)."""
+    _bf16(y, "y")
+    _bf16(c, "c")
+    if y.dim() != 2 or c.dim() != 2 or c.shape[1] != y.shape[1]:
+        raise ValueError("y must be [T, H] and c [M, H]")
+    T, H = y.shape
+    k = _slots(rows, weights, T)
+    if residual is not None:
+        _bf16(residual, "residual")
+        if residual.shape != y.shape:
+            raise ValueError("residual must be [T, H]")
+    _same_device(y, c, rows, weights, residual)
+    _check(lib.dg_moe_combine(_ptr(y), _ptr(c), _ptr(rows), _ptr(weights), _ptr(residual), T, k,
+                              c.shape[0], H, _stream(stream)), "dg_moe_combine")
+
+
+def dg_moe_combine_backward(dc, sdc, dweights, dy, c, rows, pairs, weights=None,
+                            stream=None) -> None:
+    """From dy [T, H] (bf16, any row stride): dc (codes [M, H]) and sdc float32
+    [H/128, M], the gradient of c quantised as dg_moe_dispatch_fp8 does with
+    weights, and dweights float32 [T, k]; dc and sdc, or dweights, may be
+    None."""
+    T, H, ld = _rows_of_any_stride(dy, "dy", (torch.bfloat16,))
+    k = _slots(rows, weights, T)
+    _require(pairs, torch.int32, "pairs")
+    M = pairs.numel()
+    if dc is not None or sdc is not None:
+        _fp8_pair(dc, sdc, M, H, "dc")
+    if dweights is not None:
+        _shaped(dweights, torch.float32, rows.shape, "dweights")
+        _bf16(c, "c")
+        if c.shape != (M, H):
+            raise ValueError("c must be [M, H]")
+    _same_device(dy, dc, sdc, dweights, c, rows, pairs, weights)
+    _check(lib.dg_moe_combine_backward(_ptr(dc), _ptr(sdc), _ptr(dweights), _ptr(dy), ld, _ptr(c),
+                                       _ptr(rows), _ptr(pairs), _ptr(weights), T, k, M, H,
+                                       _stream(stream)), "dg_moe_combine_backward")
+
+
+def _layout_rows(m_indices, M):
+    if m_indices is not None:
+        _shaped(m_indices, torch.int32, (M,), "m_indices")
+
+
+def dg_swiglu_fp8(h, sh, gu, kept=None, skept=None, m_indices=None, stream=None) -> None:
+    """h (codes [M, I]) and sh float32 [I/128, M] = silu(gate) * up of gu [M, 2I]
+    (bf16, column 2i gate, 2i+1 up), and kept (codes [M, 2I]), skept float32
+    [2I/128, M] = gu itself in 8 bits for dg_swiglu_fp8_backward.  m_indices
+    int32 [M]: the rows of the grouped layout that are real."""
+    _bf16(gu, "gu")
+    if gu.dim() != 2:
+        raise ValueError("gu must be [M, 2I]")
+    M, I = gu.shape[0], gu.shape[1] // 2
+    _fp8_pair(h, sh, M, I, "h")
+    if gu.shape[1] != 2 * I:
+        raise ValueError("gu must be [M, 2I]")
+    if kept is not None or skept is not None:
+        _fp8_pair(kept, skept, M, 2 * I, "kept")
+    _layout_rows(m_indices, M)
+    _same_device(gu, h, sh, kept, skept, m_indices)
+    _check(lib.dg_swiglu_fp8(_ptr(h), _ptr(sh), _ptr(kept), _ptr(skept), _ptr(gu),
+                             _ptr(m_indices), M, I, _stream(stream)), "dg_swiglu_fp8")
+
+
+def dg_swiglu_fp8_backward(dgu, sdgu, dh, kept, skept, h=None, sh=None, m_indices=None,
+                           stream=None) -> None:
+    """dgu (codes [M, 2I]) and sdgu from dh [M, I] (bf16) and the checkpoint
+    kept, skept; with h (codes [M, I]) and sh also silu(gate) * up of the
+    checkpoint's values."""
+    _bf16(dh, "dh")
+    if dh.dim() != 2:
+        raise ValueError("dh must be [M, I]")
+    M, I = dh.shape
+    _fp8_pair(dgu, sdgu, M, 2 * I, "dgu")
+    _fp8_pair(kept, skept, M, 2 * I, "kept")
+    if h is not None or sh is not None:
+        _fp8_pair(h, sh, M, I, "h")
+    _layout_rows(m_indices, M)
+    _same_device(dh, dgu, sdgu, kept, skept, h, sh, m_indices)
+    _check(lib.dg_swiglu_fp8_backward(_ptr(dgu), _ptr(sdgu), _ptr(h), _ptr(sh), _ptr(dh),
+                                      _ptr(kept), _ptr(skept), _ptr(m_indices), M, I,
+                                      _stream(stream)), "dg_swiglu_fp8_backward")
+
+
+def dg_transpose_fp8_blocks(qt, st, q, s, block_rows: int = 128, m_indices=None,
+                            stream=None) -> None:
+    """qt (codes [C, M]) and st float32 [M/128, C] (block_rows 1) or [M/128,
+    C/128] (block_rows 128) = the transpose of q (codes [M, C], 1 x 128 scales
+    s float32 [C/128, M]), quantised anew along the rows of q."""
+    _codes(q, "q")
+    if q.dim() != 2:
+        raise ValueError("q must be [M, C]")
+    M, C = q.shape
+    _fp8_pair(q, s, M, C, "q")
+    _codes(qt, "qt")
+    if qt.shape != (C, M):
+        raise ValueError("qt must be [C, M]")
+    _shaped(st, torch.float32, (cdiv(M, 128), cdiv(C, block_rows) if block_rows > 0 else 0), "st")
+    _layout_rows(m_indices, M)
+    _same_device(q, s, qt, st, m_indices)
+    _check(lib.dg_transpose_fp8_blocks(_ptr(qt), _ptr(st), block_rows, _ptr(q), _ptr(s),
+                                       _ptr(m_indices), M, C, _stream(stream)),
+           "dg_transpose_fp8_blocks")
+
+
+# ---------------------------------------------------------------------------
 # Conveniences (allocate outputs with torch)
 # ---------------------------------------------------------------------------
 
@@ -826,6 +1099,79 @@ def mxfp4_gemm_nt(a, b, sfa, sfb, workspace=None):
     return c
 
 
+def moe_route(logits, k: int, bias=None, scoring: str = "softmax", groups: int = 1,
+              top_groups=None, group_best: int = 1, renormalise: bool = True, scale: float = 1.0):
+    """The k experts of each token and their weights: int32, float32 [T, k]."""
+    T = logits.shape[0]
+    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    dg_moe_route(ids, weights, logits, bias, scoring, groups, top_groups, group_best, renormalise,
+                 scale)
+    return ids, weights
+
+
+#: The layout that dg_moe_plan writes.
+MoePlan = collections.namedtuple("MoePlan", "rows pairs m_indices offsets counts")
+
+
+def moe_plan(ids, experts: int):
+    """The grouped products' layout of the experts ids int32 [T, k]."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise TypeError("ids must be an int32 tensor [T, k]")
+    T, k = ids.shape
+    M, n = dg_moe_plan_rows(T, experts, k), dg_moe_plan_workspace_bytes(T, experts, k)
+    if M == 0:
+        raise ValueError("no layout for %d tokens, %d experts, %d slots" % (T, experts, k))
+    new = dict(dtype=torch.int32, device=ids.device)
+    plan = MoePlan(torch.empty((T, k), **new), torch.empty(M, **new), torch.empty(M, **new),
+                   torch.empty(experts + 1, dtype=torch.int64, device=ids.device),
+                   torch.empty(experts, **new))
+    ws = torch.empty(n, dtype=torch.uint8, device=ids.device) if n else None
+    dg_moe_plan(*plan, ids, workspace=ws)
+    return plan
+
+
+def _fp8_empty(rows, cols, device):
+    return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
+            torch.empty((cdiv(cols, 128), rows), dtype=torch.float32, device=device))
+
+
+def moe_dispatch_fp8(x, plan, weights=None):
+    """x [T, H] into the layout -> (codes [M, H], scales [H/128, M]).  Blocks
+    of 128 rows without an expert keep what the memory held."""
+    a, sa = _fp8_empty(plan.pairs.numel(), x.shape[1], x.device)
+    dg_moe_dispatch_fp8(a, sa, x, plan.rows, plan.pairs, weights)
+    return a, sa
+
+
+def moe_combine(c, plan, weights=None, residual=None):
+    """The rows c [M, H] of the layout summed per token -> bfloat16 [T, H]."""
+    y = torch.empty((plan.rows.shape[0], c.shape[1]), dtype=torch.bfloat16, device=c.device)
+    dg_moe_combine(y, c, plan.rows, weights, residual)
+    return y
+
+
+def swiglu_fp8(gu, m_indices=None, keep: bool = False):
+    """silu(gate) * up of gu [M, 2I] -> (codes [M, I], scales [I/128, M]), and
+    with keep the checkpoint (codes [M, 2I], scales) after them."""
+    M, two = gu.shape
+    h, sh = _fp8_empty(M, two // 2, gu.device)
+    kept, skept = _fp8_empty(M, two, gu.device) if keep else (None, None)
+    dg_swiglu_fp8(h, sh, gu, kept, skept, m_indices)
+    return (h, sh, kept, skept) if keep else (h, sh)
+
+
+def transpose_fp8_blocks(q, s, block_rows: int = 128, m_indices=None):
+    """Codes [M, C] with 1 x 128 scales -> (codes [C, M], scales over 128 rows
+    of one column (block_rows 1) or of 128)."""
+    M, C = q.shape
+    qt = torch.empty((C, M), dtype=torch.uint8, device=q.device)
+    st = torch.empty((cdiv(M, 128), C if block_rows == 1 else cdiv(C, 128)), dtype=torch.float32,
+                     device=q.device)
+    dg_transpose_fp8_blocks(qt, st, q, s, block_rows, m_indices)
+    return qt, st
+
+
 __all__ = [
     "lib", "LIB_PATH", "DGError", "status_string", "get_mk_alignment_for_contiguous_layout",
     "dg_quantize_fp8_block", "dg_fp8_gemm_nt_workspace_bytes", "dg_fp8_gemm_nt",
@@ -840,6 +1186,11 @@ __all__ = [
     "from_mxfp4", "dg_mxfp4_gemm_nt_workspace_bytes", "dg_mxfp4_gemm_nt", "mxfp4_gemm_nt",
     "dg_mxfp4_gemm_nt_bf16a_workspace_bytes", "dg_mxfp4_gemm_nt_bf16a", "MXFP4_BF16A_MAX_M",
     "dg_moe_layer_workspace_bytes", "dg_moe_layer", "MOE_SCORINGS",
+    "dg_moe_route", "dg_moe_route_backward", "moe_route", "dg_moe_plan_rows",
+    "dg_moe_plan_workspace_bytes", "dg_moe_plan", "MoePlan", "moe_plan", "dg_moe_dispatch_fp8",
+    "moe_dispatch_fp8", "dg_moe_combine", "dg_moe_combine_backward", "moe_combine",
+    "dg_swiglu_fp8", "dg_swiglu_fp8_backward", "swiglu_fp8", "dg_transpose_fp8_blocks",
+    "transpose_fp8_blocks",
 ]
 # (the _epilogue C entry points are reached through the act / residual
 # arguments of dg_fp8_grouped_gemm_contig and dg_fp8_grouped_gemm_masked)

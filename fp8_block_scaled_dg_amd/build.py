@@ -19,7 +19,8 @@ OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "libdg.so")
 SOURCES = ["quantize.hip", "gemm_tiled.hip", "gemm_skinny.hip", "gemm_stream.hip", "transpose.hip",
            "noalloc.hip", "mxfp4_quantize.hip", "gemm_mxfp4.hip",
-           "gemm_mxfp4_tiled.hip", "moe_layer.hip", "api.cpp"]
+           "gemm_mxfp4_tiled.hip", "moe_layer.hip", "route.hip", "plan.hip",
+           "dispatch.hip", "swiglu_fp8.hip", "api.cpp"]
 # measurement probe (its own library; not part of the C ABI in include/dg.h)
 PROBE_LIB = os.path.join(LIBDIR, "libdg_probe.so")
 PROBE_SOURCES = ["probe/peak.hip", "probe/hbm_read.hip"]

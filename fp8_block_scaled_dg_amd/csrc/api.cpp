@@ -580,4 +580,219 @@ int dg_moe_layer(uint16_t* y, const uint16_t* x, const uint8_t* w13, const uint8
   return from_hip(dg::launch_moe_layer(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
+// ---- around the grouped products ----
+
+namespace {
+
+bool dtype_ok(int dtype) { return dtype == DG_DTYPE_F32 || dtype == DG_DTYPE_BF16; }
+size_t dtype_size(int dtype) { return dtype == DG_DTYPE_BF16 ? 2 : 4; }
+
+static_assert(DG_MOE_SOFTMAX == dg::ROUTE_SOFTMAX && DG_MOE_SIGMOID == dg::ROUTE_SIGMOID &&
+              DG_MOE_MAX_SLOTS == dg::kMoeMaxSlots && DG_MOE_MAX_EXPERTS == dg::kMoeMaxExperts,
+              "constants of dg.h and of the kernels");
+
+// Tokens, experts and slots.
+bool experts_ok(int64_t T, int E, int k, int64_t most) {
+  return T >= 1 && T <= most && E >= 1 && E <= DG_MOE_MAX_EXPERTS && k >= 1 && k <= E &&
+         k <= DG_MOE_MAX_SLOTS;
+}
+bool plan_ok(int64_t T, int E, int k) {
+  return experts_ok(T, E, k, int64_t(1) << 27) && T * k <= (int64_t(1) << 27);
+}
+
+int check_route(const void* ids, const void* weights, const void* logits, int dtype, int64_t ldl,
+                int scoring, int64_t T, int E, int k) {
+  if (!ids || !weights || !logits) return DG_ERR_NULL;
+  if (!dtype_ok(dtype) || (scoring != DG_MOE_SOFTMAX && scoring != DG_MOE_SIGMOID))
+    return DG_ERR_UNSUPPORTED;
+  if (!experts_ok(T, E, k, int64_t(1) << 25) || ldl < E || ldl > INT64_MAX / 4 / T)
+    return DG_ERR_SHAPE;
+  if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(logits, dtype_size(dtype)))
+    return DG_ERR_ALIGN;
+  return DG_OK;
+}
+
+// Tokens and rows of `cols` columns in the layout (multiples of `step`).
+bool layout_ok(int64_t T, int k, int64_t M, int64_t cols, int64_t step) {
+  if (T < 1 || k < 1 || k > DG_MOE_MAX_SLOTS || M < 128 || M % 128 != 0 || cols < step ||
+      cols % step != 0 || cols > (int64_t(1) << 34))
+    return false;
+  const int64_t parts = (cols + 511) / 512;
+  return T <= (int64_t(1) << 25) / parts && M <= (int64_t(1) << 29) / parts;
+}
+
+int check_swiglu(const int32_t* m_indices, int64_t M, int64_t I) {
+  if (M < 1 || I < 128 || I % 128 != 0 || I > (int64_t(1) << 34)) return DG_ERR_SHAPE;
+  if (M > (int64_t(1) << 25) / ((I + 511) / 512)) return DG_ERR_SHAPE;
+  if (m_indices && M % 128 != 0) return DG_ERR_SHAPE;
+  return aligned(m_indices, 4) ? DG_OK : DG_ERR_ALIGN;
+}
+
+}  // namespace
+
+int dg_moe_route(int32_t* ids, float* weights, const void* logits, int dtype, int64_t ldl,
+                 const float* bias, int scoring, int groups, int top_groups, int group_best,
+                 int renormalise, float scale, int64_t T, int E, int k, void* stream) {
+  const int st = check_route(ids, weights, logits, dtype, ldl, scoring, T, E, k);
+  if (st != DG_OK) return st;
+  if (group_best != 1 && group_best != 2) return DG_ERR_UNSUPPORTED;
+  if (groups < 1 || groups > DG_ROUTE_MAX_GROUPS || E % groups != 0 || top_groups < 1 ||
+      top_groups > groups || E / groups < group_best)
+    return DG_ERR_SHAPE;
+  if (!aligned(bias, 4)) return DG_ERR_ALIGN;
+  dg::RouteArgs p{};
+  p.ids = ids;
+  p.weights = weights;
+  p.logits = logits;
+  p.bias = bias;
+  p.bf16 = dtype == DG_DTYPE_BF16;
+  p.renormalise = renormalise != 0;
+  p.scoring = scoring;
+  p.groups = groups;
+  p.top_groups = top_groups;
+  p.best = group_best;
+  p.scale = scale;
+  p.T = T;
+  p.ldl = ldl;
+  p.E = E;
+  p.k = k;
+  return from_hip(dg::launch_route(p, static_cast<hipStream_t>(stream)));
+}
+
+int dg_moe_route_backward(void* dlogits, int64_t ldd, const float* dweights, const int32_t* ids,
+                          const void* logits, int dtype, int64_t ldl, int scoring,
+                          int renormalise, float scale, int64_t T, int E, int k, void* stream) {
+  if (!dlogits) return DG_ERR_NULL;
+  const int st = check_route(ids, dweights, logits, dtype, ldl, scoring, T, E, k);
+  if (st != DG_OK) return st;
+  if (ldd < E || ldd > INT64_MAX / 4 / T) return DG_ERR_SHAPE;
+  if (!aligned(dlogits, dtype_size(dtype))) return DG_ERR_ALIGN;
+  dg::RouteArgs p{};
+  p.ids = const_cast<int32_t*>(ids);
+  p.dlogits = dlogits;
+  p.dweights = dweights;
+  p.logits = logits;
+  p.bf16 = dtype == DG_DTYPE_BF16;
+  p.renormalise = renormalise != 0;
+  p.scoring = scoring;
+  p.scale = scale;
+  p.T = T;
+  p.ldl = ldl;
+  p.ldd = ldd;
+  p.E = E;
+  p.k = k;
+  return from_hip(dg::launch_route_backward(p, static_cast<hipStream_t>(stream)));
+}
+
+int64_t dg_moe_plan_rows(int64_t T, int E, int k) {
+  return plan_ok(T, E, k) ? dg::plan_rows(T, E, k) : 0;
+}
+
+size_t dg_moe_plan_workspace_bytes(int64_t T, int E, int k) {
+  return plan_ok(T, E, k) ? dg::plan_workspace_bytes(T, E, k) : 0;
+}
+
+int dg_moe_plan(int32_t* rows, int32_t* pairs, int32_t* m_indices, int64_t* offsets,
+                int32_t* counts, const int32_t* ids, int64_t T, int E, int k, int64_t M,
+                void* workspace, size_t workspace_bytes, void* stream) {
+  if (!rows || !pairs || !m_indices || !offsets || !counts || !ids) return DG_ERR_NULL;
+  if (!plan_ok(T, E, k) || M % 128 != 0 || M < dg::plan_rows(T, E, k) || M > (int64_t(1) << 30))
+    return DG_ERR_SHAPE;
+  const size_t need = dg::plan_workspace_bytes(T, E, k);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return DG_ERR_WORKSPACE;
+  if (!aligned(rows, 4) || !aligned(pairs, 4) || !aligned(m_indices, 4) || !aligned(offsets, 8) ||
+      !aligned(counts, 4) || !aligned(ids, 4) || !aligned(workspace, 4))
+    return DG_ERR_ALIGN;
+  dg::PlanArgs p{rows, pairs, m_indices, offsets, counts, ids, T * k, M, E, 0, 0, nullptr};
+  return from_hip(dg::launch_plan(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int dg_moe_dispatch_fp8(uint8_t* a, float* sa, const void* x, int dtype, int64_t ldx,
+                        const int32_t* rows, const int32_t* pairs, const float* weights,
+                        int64_t T, int k, int64_t M, int64_t H, void* stream) {
+  if (!a || !sa || !x || !rows || !pairs) return DG_ERR_NULL;
+  if (!dtype_ok(dtype)) return DG_ERR_UNSUPPORTED;
+  if (!layout_ok(T, k, M, H, 128) || ldx < H || ldx > INT64_MAX / 4 / T) return DG_ERR_SHAPE;
+  if (!aligned(a, 16) || !aligned(sa, 4) || !aligned(x, dtype_size(dtype)) || !aligned(rows, 4) ||
+      !aligned(pairs, 4) || !aligned(weights, 4))
+    return DG_ERR_ALIGN;
+  dg::DispatchArgs p{a, sa, x, dtype == DG_DTYPE_BF16, rows, pairs, weights, T, ldx, M, H, k, 0};
+  return from_hip(dg::launch_dispatch(p, static_cast<hipStream_t>(stream)));
+}
+
+int dg_moe_combine(uint16_t* y, const uint16_t* c, const int32_t* rows, const float* weights,
+                   const uint16_t* residual, int64_t T, int k, int64_t M, int64_t H,
+                   void* stream) {
+  if (!y || !c || !rows) return DG_ERR_NULL;
+  if (!layout_ok(T, k, M, H, 8)) return DG_ERR_SHAPE;
+  if (!aligned(y, 16) || !aligned(c, 16) || !aligned(residual, 16) || !aligned(rows, 4) ||
+      !aligned(weights, 4))
+    return DG_ERR_ALIGN;
+  const dg::CombineArgs p{y, c, rows, weights, residual, nullptr, nullptr, T, M, H, 0, k};
+  return from_hip(dg::launch_combine(p, static_cast<hipStream_t>(stream)));
+}
+
+int dg_moe_combine_backward(uint8_t* dc, float* sdc, float* dweights, const uint16_t* dy,
+                            int64_t lddy, const uint16_t* c, const int32_t* rows,
+                            const int32_t* pairs, const float* weights, int64_t T, int k,
+                            int64_t M, int64_t H, void* stream) {
+  if (!dy || !rows || (!dc && !dweights) || !dc != !sdc || (dc && !pairs) || (dweights && !c))
+    return DG_ERR_NULL;
+  if (!layout_ok(T, k, M, H, 128) || lddy < H || lddy > INT64_MAX / 4 / T) return DG_ERR_SHAPE;
+  if (!aligned(dc, 16) || !aligned(c, 16) || !aligned(dy, 2) || !aligned(sdc, 4) ||
+      !aligned(dweights, 4) || !aligned(rows, 4) || !aligned(pairs, 4) || !aligned(weights, 4))
+    return DG_ERR_ALIGN;
+  if (dc) {
+    dg::DispatchArgs p{dc, sdc, dy, true, rows, pairs, weights, T, lddy, M, H, k, 0};
+    const int st = from_hip(dg::launch_dispatch(p, static_cast<hipStream_t>(stream)));
+    if (st != DG_OK) return st;
+  }
+  if (!dweights) return DG_OK;
+  const dg::CombineArgs p{nullptr, c, rows, weights, nullptr, dweights, dy, T, M, H, lddy, k};
+  return from_hip(dg::launch_combine_dot(p, static_cast<hipStream_t>(stream)));
+}
+
+int dg_swiglu_fp8(uint8_t* h, float* sh, uint8_t* kept, float* skept, const uint16_t* gu,
+                  const int32_t* m_indices, int64_t M, int64_t I, void* stream) {
+  if (!h || !sh || !gu || !kept != !skept) return DG_ERR_NULL;
+  const int st = check_swiglu(m_indices, M, I);
+  if (st != DG_OK) return st;
+  if (!aligned(h, 16) || !aligned(kept, 16) || !aligned(gu, 16) || !aligned(sh, 4) ||
+      !aligned(skept, 4))
+    return DG_ERR_ALIGN;
+  const dg::SwigluArgs p{h, sh, kept, skept, gu, nullptr, nullptr, nullptr, m_indices, M, I};
+  return from_hip(dg::launch_swiglu(p, false, static_cast<hipStream_t>(stream)));
+}
+
+int dg_swiglu_fp8_backward(uint8_t* dgu, float* sdgu, uint8_t* h, float* sh, const uint16_t* dh,
+                           const uint8_t* kept, const float* skept, const int32_t* m_indices,
+                           int64_t M, int64_t I, void* stream) {
+  if (!dgu || !sdgu || !dh || !kept || !skept || !h != !sh) return DG_ERR_NULL;
+  const int st = check_swiglu(m_indices, M, I);
+  if (st != DG_OK) return st;
+  if (!aligned(dgu, 16) || !aligned(h, 16) || !aligned(dh, 16) || !aligned(kept, 16) ||
+      !aligned(sdgu, 4) || !aligned(sh, 4) || !aligned(skept, 4))
+    return DG_ERR_ALIGN;
+  const dg::SwigluArgs p{h, sh, const_cast<uint8_t*>(kept), const_cast<float*>(skept),
+                         nullptr, dh, dgu, sdgu, m_indices, M, I};
+  return from_hip(dg::launch_swiglu(p, true, static_cast<hipStream_t>(stream)));
+}
+
+int dg_transpose_fp8_blocks(uint8_t* qt, float* st, int block_rows, const uint8_t* q,
+                            const float* s, const int32_t* m_indices, int64_t M, int64_t C,
+                            void* stream) {
+  if (!qt || !st || !q || !s) return DG_ERR_NULL;
+  if (block_rows != 1 && block_rows != 128) return DG_ERR_UNSUPPORTED;
+  if (M < 128 || C < 128 || M % 128 != 0 || C % 128 != 0) return DG_ERR_SHAPE;
+  if (M / 128 > (int64_t(1) << 23) / (C / 128)) return DG_ERR_SHAPE;
+  if (!aligned(qt, 16) || !aligned(q, 16) || !aligned(st, 4) || !aligned(s, 4) ||
+      !aligned(m_indices, 4))
+    return DG_ERR_ALIGN;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(q), b = reinterpret_cast<uintptr_t>(qt);
+  const uintptr_t n = (uintptr_t)(M * C);
+  if (a < b + n && b < a + n) return DG_ERR_UNSUPPORTED;
+  const dg::TransposeArgs p{qt, st, q, s, m_indices, M, C};
+  return from_hip(dg::launch_transpose_blocks(p, block_rows == 1, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -160,4 +160,101 @@ struct MoeProblem {
 size_t moe_workspace_bytes(int T, int E, int k, int64_t H, int64_t I);
 hipError_t launch_moe_layer(const MoeProblem& p, void* workspace, hipStream_t stream);
 
+// Routing of any number of tokens, and its gradient (logits and dlogits BF16 or
+// FP32, bias null: none).
+enum { ROUTE_SOFTMAX = MOE_SOFTMAX, ROUTE_SIGMOID = MOE_SIGMOID };
+struct RouteArgs {
+  int32_t* ids;
+  float* weights;         // forward only
+  void* dlogits;          // backward only, as dweights
+  const float* dweights;
+  const void* logits;
+  const float* bias;
+  bool bf16, renormalise;
+  int scoring, groups, top_groups, best;
+  float scale;
+  int64_t T, ldl, ldd;
+  int E, k;
+  int lanes;              // of a wave for each group (set by the launch)
+};
+hipError_t launch_route(RouteArgs p, hipStream_t stream);
+hipError_t launch_route_backward(const RouteArgs& p, hipStream_t stream);
+
+// The layout of the grouped products from the experts ids [n] of the pairs
+// (token, slot).
+struct PlanArgs {
+  int32_t* rows;       // [n]
+  int32_t* pairs;      // [M]
+  int32_t* m_indices;  // [M]
+  int64_t* offsets;    // [E + 1]
+  int32_t* counts;     // [E]
+  const int32_t* ids;  // [n]
+  int64_t n, M;
+  int E;
+  int chunks;          // set by the launch, as what follows
+  int64_t chunk;
+  int* chunk_counts;   // [chunks][E] in the workspace
+};
+int64_t plan_rows(int64_t T, int E, int k);
+size_t plan_workspace_bytes(int64_t T, int E, int k);
+hipError_t launch_plan(PlanArgs p, void* workspace, hipStream_t stream);
+
+// Rows of tokens into the layout in E4M3 (x BF16 or FP32 [T][ldx], weights
+// null: as they are).
+struct DispatchArgs {
+  uint8_t* a;
+  float* sa;
+  const void* x;
+  bool bf16;
+  const int32_t* rows;
+  const int32_t* pairs;
+  const float* weights;
+  int64_t T, ldx, M, H;
+  int k;
+  uint32_t token_groups;  // set by the launch
+};
+hipError_t launch_dispatch(DispatchArgs p, hipStream_t stream);
+
+// Rows of the layout back to tokens: y, and the gradient of the weights.
+struct CombineArgs {
+  uint16_t* y;
+  const uint16_t* c;
+  const int32_t* rows;
+  const float* weights;
+  const uint16_t* residual;
+  float* dweights;     // launch_combine_dot
+  const uint16_t* dy;  // launch_combine_dot
+  int64_t T, M, H, lddy;
+  int k;
+};
+hipError_t launch_combine(const CombineArgs& p, hipStream_t stream);
+hipError_t launch_combine_dot(const CombineArgs& p, hipStream_t stream);
+
+// SwiGLU in E4M3 with its checkpoint, and its gradient.
+struct SwigluArgs {
+  uint8_t* h;              // [M][I]
+  float* sh;               // [I / 128][M]
+  uint8_t* kept;           // [M][2 I], read by the backward
+  float* skept;            // [2 I / 128][M]
+  const uint16_t* gu;      // forward only
+  const uint16_t* dh;      // backward only, as dgu and sdgu
+  uint8_t* dgu;
+  float* sdgu;
+  const int32_t* m_indices;
+  int64_t M, I;
+};
+hipError_t launch_swiglu(const SwigluArgs& p, bool backward, hipStream_t stream);
+
+// E4M3 rows [M][C] with 1 x 128 scales -> [C][M] with scales over 128 rows of one
+// column, or of 128.
+struct TransposeArgs {
+  uint8_t* qt;
+  float* st;
+  const uint8_t* q;
+  const float* s;
+  const int32_t* m_indices;
+  int64_t M, C;
+};
+hipError_t launch_transpose_blocks(const TransposeArgs& p, bool column, hipStream_t stream);
+
 }  // namespace dg

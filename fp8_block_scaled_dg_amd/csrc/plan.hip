@@ -1,0 +1,209 @@
+// The layout of the grouped products (experts contiguous along M, each one's
+// rows filled up to a multiple of 128) from the experts of all tokens, gfx950.
+//
+// A stable counting sort of the n = T k pairs (token, slot) by expert: the row
+// of a pair is its expert's offset plus the number of earlier pairs of that
+// expert.  The pairs are cut into chunks, one workgroup each; a workgroup needs
+// each expert's total and its count in the chunks before its own.  Few pairs:
+// every workgroup counts all of them itself (one launch).  Many: a first launch
+// leaves each chunk's counts in the workspace.
+//
+// Nothing depends on the order in which workgroups or waves run: the counters
+// in LDS are sums, and a wave ranks its 64 pairs by which lanes hold the same
+// expert (one ballot a bit of the expert's id).
+#include "dg_device.hpp"
+#include "dg_internal.hpp"
+
+namespace dg {
+namespace {
+
+constexpr int kPlanWaves = 8, kPlanThreads = 64 * kPlanWaves;
+constexpr int kPlanMaxChunks = 256;
+constexpr int64_t kPlanSelfPairs = 4096;  // up to here workgroups count all pairs
+static_assert(2 * kPlanThreads >= kMoeMaxExperts, "two experts a thread");
+
+__device__ __forceinline__ int expert_of(const PlanArgs& p, int64_t i) {
+  const int id = p.ids[i];
+  return (unsigned)id < (unsigned)p.E ? id : -1;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(PlanArgs p) {
+  __shared__ int s_count[kMoeMaxExperts];
+  for (int e = threadIdx.x; e < p.E; e += kPlanThreads) s_count[e] = 0;
+  __syncthreads();
+  const int64_t begin = blockIdx.x * p.chunk, end = begin + p.chunk < p.n ? begin + p.chunk : p.n;
+  for (int64_t i = begin + threadIdx.x; i < end; i += kPlanThreads) {
+    const int e = expert_of(p, i);
+    if (e >= 0) atomicAdd(&s_count[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kPlanThreads)
+    p.chunk_counts[(int64_t)blockIdx.x * p.E + e] = s_count[e];
+}
+
+template <bool SELF>
+__global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanArgs p) {
+  __shared__ int s_next[kPlanWaves][kMoeMaxExperts];  // a wave's next row of each expert
+  __shared__ int s_total[kMoeMaxExperts], s_before[SELF ? kMoeMaxExperts : 1];
+  __shared__ int s_offset[kMoeMaxExperts + 1], s_sum[kPlanWaves];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t begin = blockIdx.x * p.chunk, end = begin + p.chunk < p.n ? begin + p.chunk : p.n;
+  for (int e = tid; e < p.E; e += kPlanThreads) {
+    s_total[e] = 0;
+    if constexpr (SELF) s_before[e] = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) s_next[w][e] = 0;
+  }
+  __syncthreads();
+  // this wave's part of the chunk, a multiple of 64 pairs
+  const int64_t part = (p.chunk + kPlanThreads - 1) / kPlanThreads * 64;
+  const int64_t w0 = begin + wave * part < end ? begin + wave * part : end;
+  const int64_t w1 = w0 + part < end ? w0 + part : end;
+  for (int64_t i = w0 + lane; i < w1; i += 64) {
+    const int e = expert_of(p, i);
+    if (e >= 0) atomicAdd(&s_next[wave][e], 1);
+  }
+  if constexpr (SELF) {
+    for (int64_t i = tid; i < p.n; i += kPlanThreads) {
+      const int e = expert_of(p, i);
+      if (e >= 0) {
+        atomicAdd(&s_total[e], 1);
+        if (i < begin) atomicAdd(&s_before[e], 1);
+      }
+    }
+    __syncthreads();
+  }
+  // experts 2 tid and 2 tid + 1
+  int total[2] = {0, 0}, before[2] = {0, 0}, padded[2], own = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int e = 2 * tid + h;
+    if (e < p.E) {
+      if constexpr (SELF) {
+        total[h] = s_total[e];
+        before[h] = s_before[e];
+      } else {
+        for (int c = 0; c < p.chunks; ++c) {
+          const int n = p.chunk_counts[(int64_t)c * p.E + e];
+          total[h] += n;
+          if (c < (int)blockIdx.x) before[h] += n;
+        }
+        s_total[e] = total[h];
+      }
+    }
+    padded[h] = (total[h] + 127) & ~127;
+    own += padded[h];
+  }
+  int sum = own;  // running sum over the wave, then over the waves
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(sum, d, 64);
+    if (lane >= d) sum += o;
+  }
+  if (lane == 63) s_sum[wave] = sum;
+  __syncthreads();
+  int offset = sum - own;
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w)
+    if (w < wave) offset += s_sum[w];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int e = 2 * tid + h;
+    if (e < p.E) {
+      s_offset[e] = offset;
+      int next = offset + before[h];
+#pragma unroll
+      for (int w = 0; w < kPlanWaves; ++w) {
+        const int n = s_next[w][e];
+        s_next[w][e] = next;
+        next += n;
+      }
+      if (blockIdx.x == 0) {
+        p.offsets[e] = offset;
+        p.counts[e] = total[h];
+      }
+      offset += padded[h];
+      if (e == p.E - 1) {
+        s_offset[p.E] = offset;
+        if (blockIdx.x == 0) p.offsets[p.E] = offset;
+      }
+    }
+  }
+  __syncthreads();
+  const int bits = 32 - __builtin_clz((unsigned)p.E);
+  for (int64_t i0 = w0; i0 < w1; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const int e = i < w1 ? expert_of(p, i) : -1;
+    uint64_t same = __ballot(e >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot(e >> b & 1);
+      same &= e >> b & 1 ? set : ~set;
+    }
+    const int first = __ffsll((unsigned long long)same) - 1;
+    int row = 0;
+    if (e >= 0 && lane == first) row = atomicAdd(&s_next[wave][e], (int)__popcll(same));
+    row = __shfl(row, first < 0 ? 0 : first, 64) + __popcll(same & ((1ull << lane) - 1));
+    if (i < w1) p.rows[i] = e >= 0 ? row : -1;
+    if (e >= 0) {
+      p.pairs[row] = (int)i;
+      p.m_indices[row] = e;
+    }
+  }
+  // rows that no pair has: the ends of the experts' blocks (128 threads an
+  // expert) and what is behind the last expert
+  for (int e = (int)blockIdx.x * (kPlanThreads / 128) + (tid >> 7); e < p.E;
+       e += p.chunks * (kPlanThreads / 128)) {
+    const int r = s_offset[e] + s_total[e] + (tid & 127);
+    if (r < s_offset[e + 1]) {
+      p.pairs[r] = -1;
+      p.m_indices[r] = -1;
+    }
+  }
+  for (int64_t r = s_offset[p.E] + (int64_t)blockIdx.x * kPlanThreads + tid; r < p.M;
+       r += (int64_t)p.chunks * kPlanThreads) {
+    p.pairs[r] = -1;
+    p.m_indices[r] = -1;
+  }
+}
+
+// Chunks of 1024 pairs (128 a wave, two rounds of 64), more where the rows to
+// fill are many next to the pairs, at most 256.
+int plan_chunks(int64_t n, int64_t M) {
+  int64_t c = (n + 1023) / 1024;
+  const int64_t fill = (M + 8191) / 8192;
+  if (c < fill) c = fill;
+  const int64_t most = (n + 63) / 64;  // not more than there is work for
+  if (c > most) c = most;
+  return (int)(c < 1 ? 1 : c > kPlanMaxChunks ? kPlanMaxChunks : c);
+}
+
+}  // namespace
+
+int64_t plan_rows(int64_t T, int E, int k) {
+  const int64_t n = T * k, used = n < E ? n : E;
+  return 128 * (used + (n - used) / 128);
+}
+
+size_t plan_workspace_bytes(int64_t T, int E, int k) {
+  const int64_t n = T * k;
+  return n <= kPlanSelfPairs ? 0 : (size_t)kPlanMaxChunks * E * sizeof(int);
+}
+
+hipError_t launch_plan(PlanArgs p, void* workspace, hipStream_t stream) {
+  p.chunks = plan_chunks(p.n, p.M);
+  p.chunk = (p.n + p.chunks - 1) / p.chunks;
+  p.chunk_counts = static_cast<int*>(workspace);
+  const dim3 grid((unsigned)p.chunks), block(kPlanThreads);
+  if (p.n <= kPlanSelfPairs) {
+    hipLaunchKernelGGL(plan_place_kernel<true>, grid, block, 0, stream, p);
+  } else {
+    hipLaunchKernelGGL(plan_count_kernel, grid, block, 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(plan_place_kernel<false>, grid, block, 0, stream, p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace dg

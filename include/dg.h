@@ -549,6 +549,164 @@ int dg_moe_layer(uint16_t *y, const uint16_t *x, const uint8_t *w13, const uint8
                  const float *logits, int scoring, int T, int E, int k, int64_t H, int64_t I,
                  void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Routing of any number of tokens to experts: the k experts of each token and
+ * their weights (dg_moe_layer does this for up to 64 tokens inside its launch).
+ *   logits : [T][ldl], dtype DG_DTYPE_F32 or DG_DTYPE_BF16, ldl >= E elements
+ *            from token to token, aligned to its element only.
+ *   bias   : FP32 [E] or NULL.
+ *   ids    : out, int32 [T][k]; weights : out, FP32 [T][k].
+ * Scores s = softmax(l) over the token's logits (DG_MOE_SOFTMAX) or
+ * 1 / (1 + e^-l) (DG_MOE_SIGMOID).  Choice values c = s + bias, held in 64 bits;
+ * without a bias the order of the logits themselves.  With top_groups < groups
+ * the E / groups consecutive experts of a group stay only if its value, the
+ * sum of its group_best (1 or 2) largest choice values, is one of the top_groups
+ * largest.  ids are the k largest choice values of what stays, in descending
+ * order; every tie goes to the lowest index.  weights = scale * s, divided by
+ * the sum of the token's chosen s if renormalise is not 0 (the bias has no part
+ * in them).  A logit of -inf or NaN, or a bias of -inf or NaN, is an expert that
+ * is never chosen (a group without any never stays ahead of others); slots left
+ * over get id -1 and weight 0.  With the softmax, +inf makes its token's weights
+ * NaN.
+ * Requirements: T >= 1, T <= 2^25; 1 <= E <= DG_MOE_MAX_EXPERTS; 1 <= k <=
+ * min(E, DG_MOE_MAX_SLOTS); 1 <= groups <= DG_ROUTE_MAX_GROUPS, E a multiple of
+ * it; 1 <= top_groups <= groups; E / groups >= group_best.  Deterministic.
+ */
+#define DG_ROUTE_MAX_GROUPS 64
+int dg_moe_route(int32_t *ids, float *weights, const void *logits, int dtype, int64_t ldl,
+                 const float *bias, int scoring, int groups, int top_groups, int group_best,
+                 int renormalise, float scale, int64_t T, int E, int k, void *stream);
+
+/*
+ * Gradient of dg_moe_route's weights: dlogits [T][ldd] (dtype of logits, all E
+ * columns written, ldd >= E, aligned to its element) from dweights FP32 [T][k],
+ * with the ids, scoring, renormalise and scale of the forward call.  FP32
+ * throughout, rounded once.  A slot with an id outside [0, E), or with a logit
+ * of -inf or NaN, gives nothing; such logits get 0.  The choice, and with it
+ * the bias, has no gradient.
+ */
+int dg_moe_route_backward(void *dlogits, int64_t ldd, const float *dweights, const int32_t *ids,
+                          const void *logits, int dtype, int64_t ldl, int scoring,
+                          int renormalise, float scale, int64_t T, int E, int k, void *stream);
+
+/*
+ * The M-contiguous layout of the grouped products from the experts of all
+ * tokens.  A pair is a (token, slot), number t * k + j; an expert's rows hold
+ * its pairs in ascending number and are filled up to a multiple of 128.
+ *   ids       : int32 [T][k]; outside [0, E): an empty slot, no row.  An expert
+ *               may stand in several slots of a token: each gets its own row.
+ *   rows      : out, int32 [T][k], the row of each pair, -1 for an empty slot.
+ *   pairs     : out, int32 [M], the pair of each row, -1 for a row without.
+ *   m_indices : out, int32 [M], its expert or -1, as the grouped calls take it.
+ *   offsets   : out, int64 [E + 1], 8-byte aligned: first row of each expert
+ *               and the end of the layout, as dg_fp8_grouped_gemm_k takes it.
+ *   counts    : out, int32 [E], pairs of each expert.
+ *   M         : rows of the layout's arrays, a multiple of 128, at least
+ *               dg_moe_plan_rows(T, E, k), which suffices for every ids.
+ *   workspace : dg_moe_plan_workspace_bytes(T, E, k) bytes (0: none needed),
+ *               4-byte aligned, any contents, clobbered; calls that may run at
+ *               the same time need distinct ones.
+ * Requirements: T >= 1, T * k <= 2^27, M <= 2^30, E and k as dg_moe_route.
+ * Deterministic.
+ */
+int64_t dg_moe_plan_rows(int64_t T, int E, int k);
+size_t dg_moe_plan_workspace_bytes(int64_t T, int E, int k);
+int dg_moe_plan(int32_t *rows, int32_t *pairs, int32_t *m_indices, int64_t *offsets,
+                int32_t *counts, const int32_t *ids, int64_t T, int E, int k, int64_t M,
+                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Activations into the layout, quantised on the way: row rows[t][j] of a and sa
+ * gets the codes and 1 x 128 scales that dg_quantize_fp8_block (block_rows 1)
+ * gives for x[t], or with weights (FP32 [T][k], or NULL) for the FP32 products
+ * weights[t][j] * x[t].
+ *   a   : out, E4M3 [M][H]; sa : out, FP32 [H/128][M].
+ *   x   : [T][ldx], dtype DG_DTYPE_F32 or DG_DTYPE_BF16, ldx >= H, aligned to its
+ *         element only.
+ *   rows, pairs : of dg_moe_plan (rows outside [0, M) are left out).
+ * Rows that fill an expert's last 128 rows get codes and scales 0; 128-row
+ * blocks without an expert are not written.  The gradient of x is dg_moe_combine
+ * without weights.
+ * Requirements: T >= 1, 1 <= k <= DG_MOE_MAX_SLOTS, M >= 128, M % 128 == 0,
+ * H >= 128, H % 128 == 0; T * ceil(H/512) <= 2^25, M * ceil(H/512) <= 2^29;
+ * a 16-byte, the rest 4-byte aligned.  Deterministic.
+ */
+int dg_moe_dispatch_fp8(uint8_t *a, float *sa, const void *x, int dtype, int64_t ldx,
+                        const int32_t *rows, const int32_t *pairs, const float *weights,
+                        int64_t T, int k, int64_t M, int64_t H, void *stream);
+
+/*
+ * The experts' rows back to the tokens:
+ *   y[t] = bf16( sum_j weights[t][j] * c[rows[t][j]] + residual[t] )
+ * FP32 sums in slot order, the residual last; rows outside [0, M) are left out,
+ * whatever their weight.
+ *   y, residual : BF16 [T][H]; residual may be NULL or y itself.  c : BF16 [M][H].
+ *   weights     : FP32 [T][k], or NULL (all 1: the gradient of dispatch).
+ * Requirements: T, k, M as dg_moe_dispatch_fp8; H >= 8, H % 8 == 0; y, c and
+ * residual 16-byte aligned.  Deterministic.
+ *
+ * dg_moe_combine_backward: gradients from dy (BF16 [T][lddy], aligned to its
+ * element), either pair of outputs or both:
+ *   dc, sdc  : what dg_moe_dispatch_fp8 writes for dy and weights: the gradient
+ *              of c, quantised for the next grouped product; or NULL.
+ *   dweights : FP32 [T][k], dy[t] . c[rows[t][j]] in FP32, 0 for a slot without
+ *              a row; or NULL (c is not needed then).
+ * Requirements as dg_moe_dispatch_fp8.
+ */
+int dg_moe_combine(uint16_t *y, const uint16_t *c, const int32_t *rows, const float *weights,
+                   const uint16_t *residual, int64_t T, int k, int64_t M, int64_t H,
+                   void *stream);
+int dg_moe_combine_backward(uint8_t *dc, float *sdc, float *dweights, const uint16_t *dy,
+                            int64_t lddy, const uint16_t *c, const int32_t *rows,
+                            const int32_t *pairs, const float *weights, int64_t T, int k,
+                            int64_t M, int64_t H, void *stream);
+
+/*
+ * SwiGLU between two FP8 products, and the activation checkpoint in 8 bits.
+ *   gu   : BF16 [M][2 I], column 2i gate, 2i + 1 up of hidden unit i (a product
+ *          with the weights' rows interleaved as for DG_EPI_SWIGLU).
+ *   h    : out, E4M3 [M][I], sh FP32 [I/128][M]: silu(gate) * up in FP32,
+ *          quantised as dg_quantize_fp8_block does with block_rows 1.
+ *   kept : out, E4M3 [M][2 I], skept FP32 [2 I/128][M]: gu quantised the same
+ *          way, for the backward; or NULL, both.
+ *   m_indices : int32 [M] as the grouped calls take it (M % 128 == 0 then), or
+ *          NULL: every row is real.  Rows of -1 in a 128-row block with an expert
+ *          get codes and scales 0 whatever gu holds there; blocks whose first
+ *          row has -1 are not touched.
+ *
+ * dg_swiglu_fp8_backward: from the checkpoint's values g, u (code * scale) and
+ * dh BF16 [M][I], with sig = 1 / (1 + e^-g), in FP32:
+ *   dg = dh u sig (1 + g (1 - sig)),  du = dh g sig
+ *   dgu  : out, E4M3 [M][2 I] interleaved as gu, sdgu FP32 [2 I/128][M].
+ *   h, sh: out, silu(g) * u again, quantised (the operand of the weight
+ *          gradient, so that the forward's h need not be kept); or NULL, both.
+ * Requirements: M >= 1, I >= 128, I % 128 == 0, M * ceil(I/512) <= 2^25; codes,
+ * gu and dh 16-byte, scales and m_indices 4-byte aligned.  Deterministic.
+ */
+int dg_swiglu_fp8(uint8_t *h, float *sh, uint8_t *kept, float *skept, const uint16_t *gu,
+                  const int32_t *m_indices, int64_t M, int64_t I, void *stream);
+int dg_swiglu_fp8_backward(uint8_t *dgu, float *sdgu, uint8_t *h, float *sh, const uint16_t *dh,
+                           const uint8_t *kept, const float *skept, const int32_t *m_indices,
+                           int64_t M, int64_t I, void *stream);
+
+/*
+ * Codes with 1 x 128 scales (row blocks) turned into the transposed matrix with
+ * scales over 128 rows: the operands of weight gradients (dg_fp8_grouped_gemm_k,
+ * or dg_fp8_gemm_nt over K = M).
+ *   q  : E4M3 [M][C], s FP32 [C/128][M].
+ *   qt : out, E4M3 [C][M]; st : out, FP32 [M/128][C] (block_rows 1: a scale per
+ *        column of q and 128 rows) or [M/128][C/128] (block_rows 128).
+ * Each value code * scale (FP32) is quantised anew as dg_quantize_fp8_block does
+ * with this block_rows on the transposed values.  m_indices: as dg_swiglu_fp8;
+ * 128-row blocks without an expert are not touched (their columns of qt, their
+ * row of st).
+ * Requirements: M, C >= 128 and multiples of it, M/128 * C/128 <= 2^23; q, qt 16-byte,
+ * the rest 4-byte aligned; qt may not overlap q.  Deterministic.
+ */
+int dg_transpose_fp8_blocks(uint8_t *qt, float *st, int block_rows, const uint8_t *q,
+                            const float *s, const int32_t *m_indices, int64_t M, int64_t C,
+                            void *stream);
+
 #ifdef __cplusplus
 }
 #endif
