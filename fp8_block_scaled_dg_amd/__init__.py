@@ -143,12 +143,15 @@ def _load():
     lib.dg_moe_plan.restype = i32
     lib.dg_moe_plan.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, vp, sz, vp]
     lib.dg_moe_dispatch_fp8.restype = i32
-    lib.dg_moe_dispatch_fp8.argtypes = [vp, vp, vp, i32, i64, vp, vp, vp, i64, i32, i64, i64, vp]
+    lib.dg_moe_dispatch_fp8.argtypes = [vp, vp, vp, i32, i64, vp, vp, vp, i64, i32, i64, i64, vp, sz,
+                                        vp]
+    lib.dg_moe_dispatch_fp8_workspace_bytes.restype = sz
+    lib.dg_moe_dispatch_fp8_workspace_bytes.argtypes = [i64, i32, i64, i32]
     lib.dg_moe_combine.restype = i32
     lib.dg_moe_combine.argtypes = [vp, vp, vp, vp, vp, i64, i32, i64, i64, vp]
     lib.dg_moe_combine_backward.restype = i32
     lib.dg_moe_combine_backward.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp, vp, i64, i32, i64,
-                                            i64, vp]
+                                            i64, vp, sz, vp]
     lib.dg_swiglu_fp8.restype = i32
     lib.dg_swiglu_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, vp]
     lib.dg_swiglu_fp8_backward.restype = i32
@@ -779,22 +782,35 @@ def dg_moe_layer(y, x, w13, w2, s13, s2, ids, weights, logits=None, scoring: str
 # Around the grouped products: routing, layout, dispatch, combine, SwiGLU
 # ---------------------------------------------------------------------------
 
-def _shaped(t, dtype, shape, name):
-    _require(t, dtype, name)
-    if t.shape != shape:
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+
+
+def _need(t, dtypes, shape, device, name):
+    """t is a contiguous tensor of one of dtypes, of this shape (None: any)
+    on device number `device`.  One test where it is; the reason where not."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == device >= 0
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(map(str, dtypes)), t.dtype))
+    _require(t, t.dtype, name)
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s is on device %d, other tensors on %d" % (name, t.get_device(), device))
 
 
-def _fp8_pair(q, s, rows, cols, name):
+def _need_fp8(q, s, rows, cols, device, name):
     """Codes [rows, cols] and their 1 x 128 scales."""
-    _codes(q, name)
-    if q.shape != (rows, cols):
-        raise ValueError("%s must be %s, got %s" % (name, (rows, cols), tuple(q.shape)))
-    _shaped(s, torch.float32, (cdiv(cols, 128), rows), "scales of " + name)
+    _need(q, _CODES, (rows, cols), device, name)
+    _need(s, (_F32,), ((cols + 127) // 128, rows), device, "scales of " + name)
 
 
-def _rows_of_any_stride(x, name, dtypes=_DTYPES):
-    """(rows, columns, row stride) of a device matrix with contiguous rows."""
+def _need_rows(x, dtypes, name):
+    """(rows, columns, row stride, device number) of a device matrix with
+    contiguous rows of any stride."""
     if not isinstance(x, torch.Tensor) or x.dtype not in dtypes:
         raise TypeError("%s must be a tensor of %s" % (name, " or ".join(map(str, dtypes))))
     if not x.is_cuda:
@@ -805,16 +821,25 @@ def _rows_of_any_stride(x, name, dtypes=_DTYPES):
     ld, one = x.stride()
     if cols > 1 and one != 1 or rows > 1 and ld < cols:
         raise ValueError("the rows of %s must be contiguous and must not overlap" % name)
-    return rows, cols, ld if rows > 1 else cols
+    return rows, cols, ld if rows > 1 else cols, x.get_device()
 
 
-def _same_device(first, *others):
-    """The launch goes to the current device: its tensors have to be there."""
-    if first.device.index != torch._C._cuda_getDevice():
-        raise ValueError("the tensors are on %s, which is not the current device" % first.device)
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError("tensors on %s and %s" % (first.device, t.device))
+def _launch_stream(stream, device):
+    """The stream of a launch, which goes to the current device: the tensors
+    have to be there."""
+    current = torch._C._cuda_getDevice()
+    if device != current:
+        raise ValueError("the tensors are on device %d, the current one is %d" % (device, current))
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream
+
+
+def _two(t, name):
+    """(rows, columns) of a matrix whose type and place are looked at later."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix" % name)
+    return t.shape
 
 
 def dg_moe_route(ids, weights, logits, bias=None, scoring: str = "softmax", groups: int = 1,
@@ -825,18 +850,16 @@ def dg_moe_route(ids, weights, logits, bias=None, scoring: str = "softmax", grou
     stride).  bias float32 [E] is added to the scores for the choice alone;
     of `groups` groups of experts the top_groups (default: all) with the
     largest sums of their group_best largest choice values stay."""
-    T, E, ld = _rows_of_any_stride(logits, "logits")
-    _require(ids, torch.int32, "ids")
-    _require(weights, torch.float32, "weights")
-    if ids.dim() != 2 or ids.shape[0] != T or weights.shape != ids.shape:
-        raise ValueError("ids and weights must be [T, k]")
+    T, E, ld, dev = _need_rows(logits, _DTYPES, "logits")
+    k = _two(ids, "ids")[1]
+    _need(ids, (_I32,), (T, k), dev, "ids")
+    _need(weights, (_F32,), (T, k), dev, "weights")
     if bias is not None:
-        _shaped(bias, torch.float32, (E,), "bias")
-    _same_device(logits, ids, weights, bias)
-    _check(lib.dg_moe_route(_ptr(ids), _ptr(weights), _ptr(logits), _DTYPES[logits.dtype], ld,
-                            _ptr(bias), MOE_SCORINGS[scoring], groups,
+        _need(bias, (_F32,), (E,), dev, "bias")
+    _check(lib.dg_moe_route(ids.data_ptr(), weights.data_ptr(), logits.data_ptr(),
+                            _DTYPES[logits.dtype], ld, _ptr(bias), MOE_SCORINGS[scoring], groups,
                             groups if top_groups is None else top_groups, group_best,
-                            bool(renormalise), scale, T, E, ids.shape[1], _stream(stream)),
+                            bool(renormalise), scale, T, E, k, _launch_stream(stream, dev)),
            "dg_moe_route")
 
 
@@ -844,19 +867,17 @@ def dg_moe_route_backward(dlogits, dweights, ids, logits, scoring: str = "softma
                           renormalise: bool = True, scale: float = 1.0, stream=None) -> None:
     """dlogits [T, E] (the type of logits, any row stride) from dweights
     float32 [T, k] and the forward call's ids, logits and settings."""
-    T, E, ld = _rows_of_any_stride(logits, "logits")
-    if _rows_of_any_stride(dlogits, "dlogits", (logits.dtype,))[:2] != (T, E):
-        raise ValueError("dlogits must be [T, E]")
-    _require(ids, torch.int32, "ids")
-    if ids.dim() != 2 or ids.shape[0] != T:
-        raise ValueError("ids must be [T, k]")
-    _shaped(dweights, torch.float32, ids.shape, "dweights")
-    _same_device(logits, dlogits, ids, dweights)
-    _check(lib.dg_moe_route_backward(_ptr(dlogits), dlogits.stride(0) if T > 1 else E,
-                                     _ptr(dweights), _ptr(ids), _ptr(logits),
-                                     _DTYPES[logits.dtype], ld, MOE_SCORINGS[scoring],
-                                     bool(renormalise), scale, T, E, ids.shape[1],
-                                     _stream(stream)), "dg_moe_route_backward")
+    T, E, ld, dev = _need_rows(logits, _DTYPES, "logits")
+    rows, cols, ldd, where = _need_rows(dlogits, (logits.dtype,), "dlogits")
+    if (rows, cols, where) != (T, E, dev):
+        raise ValueError("dlogits must be [T, E] on the device of logits")
+    k = _two(ids, "ids")[1]
+    _need(ids, (_I32,), (T, k), dev, "ids")
+    _need(dweights, (_F32,), (T, k), dev, "dweights")
+    _check(lib.dg_moe_route_backward(dlogits.data_ptr(), ldd, dweights.data_ptr(), ids.data_ptr(),
+                                     logits.data_ptr(), _DTYPES[logits.dtype], ld,
+                                     MOE_SCORINGS[scoring], bool(renormalise), scale, T, E, k,
+                                     _launch_stream(stream, dev)), "dg_moe_route_backward")
 
 
 def dg_moe_plan_rows(T: int, E: int, k: int) -> int:
@@ -873,88 +894,98 @@ def dg_moe_plan(rows, pairs, m_indices, offsets, counts, ids, workspace=None, st
     offsets int64 [E + 1], counts int32 [E]; M a multiple of 128, at least
     dg_moe_plan_rows(T, E, k).  workspace: dg_moe_plan_workspace_bytes(T, E, k)
     bytes of any contents."""
-    for t, name in ((ids, "ids"), (pairs, "pairs"), (counts, "counts")):
-        _require(t, torch.int32, name)
-    if ids.dim() != 2 or pairs.dim() != 1 or counts.dim() != 1:
-        raise ValueError("ids must be [T, k], pairs [M] and counts [E]")
-    (T, k), M, E = ids.shape, pairs.numel(), counts.numel()
-    _shaped(rows, torch.int32, ids.shape, "rows")
-    _shaped(m_indices, torch.int32, pairs.shape, "m_indices")
-    _shaped(offsets, torch.int64, (E + 1,), "offsets")
-    _same_device(ids, rows, pairs, m_indices, offsets, counts, workspace)
-    _check(lib.dg_moe_plan(_ptr(rows), _ptr(pairs), _ptr(m_indices), _ptr(offsets), _ptr(counts),
-                           _ptr(ids), T, E, k, M, _ptr(workspace), _workspace_bytes(workspace),
-                           _stream(stream)), "dg_moe_plan")
+    T, k = shape = _two(ids, "ids")
+    dev = ids.get_device()
+    _need(ids, (_I32,), None, dev, "ids")
+    _need(rows, (_I32,), shape, dev, "rows")
+    _need(pairs, (_I32,), None, dev, "pairs")
+    _need(counts, (_I32,), None, dev, "counts")
+    M, E = pairs.numel(), counts.numel()
+    _need(m_indices, (_I32,), (M,), dev, "m_indices")
+    _need(offsets, (_I64,), (E + 1,), dev, "offsets")
+    _check(lib.dg_moe_plan(rows.data_ptr(), pairs.data_ptr(), m_indices.data_ptr(),
+                           offsets.data_ptr(), counts.data_ptr(), ids.data_ptr(), T, E, k, M,
+                           _ptr(workspace), _workspace_bytes(workspace),
+                           _launch_stream(stream, dev)), "dg_moe_plan")
 
 
-def _slots(rows, weights, T):
-    _require(rows, torch.int32, "rows")
-    if rows.dim() != 2 or rows.shape[0] != T:
-        raise ValueError("rows must be [T, k]")
-    if weights is not None:
-        _shaped(weights, torch.float32, rows.shape, "weights")
-    return rows.shape[1]
+def dg_moe_dispatch_fp8_workspace_bytes(T: int, k: int, H: int, weighted: bool = False) -> int:
+    return lib.dg_moe_dispatch_fp8_workspace_bytes(T, k, H, bool(weighted))
 
 
-def dg_moe_dispatch_fp8(a, sa, x, rows, pairs, weights=None, stream=None) -> None:
+def _dispatch_workspace(workspace, stream, T, k, H, weights, device):
+    """The caller's workspace, else one from torch for a call that has use for
+    it; torch's memory belongs to its current stream, so not where the call
+    is sent to another one."""
+    if workspace is not None or stream is not None:
+        return workspace
+    n = lib.dg_moe_dispatch_fp8_workspace_bytes(T, k, H, weights is not None)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def dg_moe_dispatch_fp8(a, sa, x, rows, pairs, weights=None, workspace=None, stream=None) -> None:
     """a (codes [M, H]) and sa float32 [H/128, M] = the rows of x [T, H]
     (float32 or bfloat16, any row stride), times weights float32 [T, k] if
-    given, quantised with 1 x 128 scales, at the rows of a dg_moe_plan."""
-    T, H, ld = _rows_of_any_stride(x, "x")
-    k = _slots(rows, weights, T)
-    _require(pairs, torch.int32, "pairs")
+    given, quantised with 1 x 128 scales, at the rows of a dg_moe_plan.
+    workspace: dg_moe_dispatch_fp8_workspace_bytes(T, k, H, weighted) bytes;
+    without one, and without a stream, a large call takes its own from
+    torch."""
+    T, H, ld, dev = _need_rows(x, _DTYPES, "x")
+    k = _two(rows, "rows")[1]
+    _need(rows, (_I32,), (T, k), dev, "rows")
+    _need(pairs, (_I32,), None, dev, "pairs")
     M = pairs.numel()
-    _fp8_pair(a, sa, M, H, "a")
-    _same_device(x, a, sa, rows, pairs, weights)
-    _check(lib.dg_moe_dispatch_fp8(_ptr(a), _ptr(sa), _ptr(x), _DTYPES[x.dtype], ld, _ptr(rows),
-                                   _ptr(pairs), _ptr(weights), T, k, M, H, _stream(stream)),
-           "dg_moe_dispatch_fp8")
+    if weights is not None:
+        _need(weights, (_F32,), (T, k), dev, "weights")
+    _need_fp8(a, sa, M, H, dev, "a")
+    workspace = _dispatch_workspace(workspace, stream, T, k, H, weights, x.device)
+    _check(lib.dg_moe_dispatch_fp8(a.data_ptr(), sa.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], ld,
+                                   rows.data_ptr(), pairs.data_ptr(), _ptr(weights), T, k, M, H,
+                                   _ptr(workspace), _workspace_bytes(workspace),
+                                   _launch_stream(stream, dev)), "dg_moe_dispatch_fp8")
 
 
 def dg_moe_combine(y, c, rows, weights=None, residual=None, stream=None) -> None:
     """y [T, H] (bf16) = sum over the slots of weights (float32 [T, k], or all
     1) times the rows of c [M, H] (bf16), plus residual [T, H] (bf16)."""
-    _bf16(y, "y")
-    _bf16(c, "c")
-    if y.dim() != 2 or c.dim() != 2 or c.shape[1] != y.shape[1]:
-        raise ValueError("y must be [T, H] and c [M, H]")
-    T, H = y.shape
-    k = _slots(rows, weights, T)
+    T, H = shape = _two(y, "y")
+    M, k, dev = _two(c, "c")[0], _two(rows, "rows")[1], y.get_device()
+    _need(y, _BF16_TYPES, None, dev, "y")
+    _need(c, _BF16_TYPES, (M, H), dev, "c")
+    _need(rows, (_I32,), (T, k), dev, "rows")
+    if weights is not None:
+        _need(weights, (_F32,), (T, k), dev, "weights")
     if residual is not None:
-        _bf16(residual, "residual")
-        if residual.shape != y.shape:
-            raise ValueError("residual must be [T, H]")
-    _same_device(y, c, rows, weights, residual)
-    _check(lib.dg_moe_combine(_ptr(y), _ptr(c), _ptr(rows), _ptr(weights), _ptr(residual), T, k,
-                              c.shape[0], H, _stream(stream)), "dg_moe_combine")
+        _need(residual, _BF16_TYPES, shape, dev, "residual")
+    _check(lib.dg_moe_combine(y.data_ptr(), c.data_ptr(), rows.data_ptr(), _ptr(weights),
+                              _ptr(residual), T, k, M, H, _launch_stream(stream, dev)),
+           "dg_moe_combine")
 
 
-def dg_moe_combine_backward(dc, sdc, dweights, dy, c, rows, pairs, weights=None,
+def dg_moe_combine_backward(dc, sdc, dweights, dy, c, rows, pairs, weights=None, workspace=None,
                             stream=None) -> None:
     """From dy [T, H] (bf16, any row stride): dc (codes [M, H]) and sdc float32
     [H/128, M], the gradient of c quantised as dg_moe_dispatch_fp8 does with
     weights, and dweights float32 [T, k]; dc and sdc, or dweights, may be
-    None."""
-    T, H, ld = _rows_of_any_stride(dy, "dy", (torch.bfloat16,))
-    k = _slots(rows, weights, T)
-    _require(pairs, torch.int32, "pairs")
+    None.  workspace: as for dg_moe_dispatch_fp8."""
+    T, H, ld, dev = _need_rows(dy, (torch.bfloat16,), "dy")
+    k = _two(rows, "rows")[1]
+    _need(rows, (_I32,), (T, k), dev, "rows")
+    _need(pairs, (_I32,), None, dev, "pairs")
     M = pairs.numel()
+    if weights is not None:
+        _need(weights, (_F32,), (T, k), dev, "weights")
     if dc is not None or sdc is not None:
-        _fp8_pair(dc, sdc, M, H, "dc")
+        _need_fp8(dc, sdc, M, H, dev, "dc")
+        workspace = _dispatch_workspace(workspace, stream, T, k, H, weights, dy.device)
     if dweights is not None:
-        _shaped(dweights, torch.float32, rows.shape, "dweights")
-        _bf16(c, "c")
-        if c.shape != (M, H):
-            raise ValueError("c must be [M, H]")
-    _same_device(dy, dc, sdc, dweights, c, rows, pairs, weights)
-    _check(lib.dg_moe_combine_backward(_ptr(dc), _ptr(sdc), _ptr(dweights), _ptr(dy), ld, _ptr(c),
-                                       _ptr(rows), _ptr(pairs), _ptr(weights), T, k, M, H,
-                                       _stream(stream)), "dg_moe_combine_backward")
-
-
-def _layout_rows(m_indices, M):
-    if m_indices is not None:
-        _shaped(m_indices, torch.int32, (M,), "m_indices")
+        _need(dweights, (_F32,), (T, k), dev, "dweights")
+        _need(c, _BF16_TYPES, (M, H), dev, "c")
+    _check(lib.dg_moe_combine_backward(_ptr(dc), _ptr(sdc), _ptr(dweights), dy.data_ptr(), ld,
+                                       None if dweights is None else c.data_ptr(),
+                                       rows.data_ptr(), pairs.data_ptr(), _ptr(weights), T, k, M,
+                                       H, _ptr(workspace), _workspace_bytes(workspace),
+                                       _launch_stream(stream, dev)), "dg_moe_combine_backward")
 
 
 def dg_swiglu_fp8(h, sh, gu, kept=None, skept=None, m_indices=None, stream=None) -> None:
@@ -962,19 +993,19 @@ def dg_swiglu_fp8(h, sh, gu, kept=None, skept=None, m_indices=None, stream=None)
     (bf16, column 2i gate, 2i+1 up), and kept (codes [M, 2I]), skept float32
     [2I/128, M] = gu itself in 8 bits for dg_swiglu_fp8_backward.  m_indices
     int32 [M]: the rows of the grouped layout that are real."""
-    _bf16(gu, "gu")
-    if gu.dim() != 2:
+    M, two = _two(gu, "gu")
+    dev = gu.get_device()
+    _need(gu, _BF16_TYPES, None, dev, "gu")
+    if two % 2:
         raise ValueError("gu must be [M, 2I]")
-    M, I = gu.shape[0], gu.shape[1] // 2
-    _fp8_pair(h, sh, M, I, "h")
-    if gu.shape[1] != 2 * I:
-        raise ValueError("gu must be [M, 2I]")
+    _need_fp8(h, sh, M, two // 2, dev, "h")
     if kept is not None or skept is not None:
-        _fp8_pair(kept, skept, M, 2 * I, "kept")
-    _layout_rows(m_indices, M)
-    _same_device(gu, h, sh, kept, skept, m_indices)
-    _check(lib.dg_swiglu_fp8(_ptr(h), _ptr(sh), _ptr(kept), _ptr(skept), _ptr(gu),
-                             _ptr(m_indices), M, I, _stream(stream)), "dg_swiglu_fp8")
+        _need_fp8(kept, skept, M, two, dev, "kept")
+    if m_indices is not None:
+        _need(m_indices, (_I32,), (M,), dev, "m_indices")
+    _check(lib.dg_swiglu_fp8(h.data_ptr(), sh.data_ptr(), _ptr(kept), _ptr(skept), gu.data_ptr(),
+                             _ptr(m_indices), M, two // 2, _launch_stream(stream, dev)),
+           "dg_swiglu_fp8")
 
 
 def dg_swiglu_fp8_backward(dgu, sdgu, dh, kept, skept, h=None, sh=None, m_indices=None,
@@ -982,19 +1013,19 @@ def dg_swiglu_fp8_backward(dgu, sdgu, dh, kept, skept, h=None, sh=None, m_indice
     """dgu (codes [M, 2I]) and sdgu from dh [M, I] (bf16) and the checkpoint
     kept, skept; with h (codes [M, I]) and sh also silu(gate) * up of the
     checkpoint's values."""
-    _bf16(dh, "dh")
-    if dh.dim() != 2:
-        raise ValueError("dh must be [M, I]")
-    M, I = dh.shape
-    _fp8_pair(dgu, sdgu, M, 2 * I, "dgu")
-    _fp8_pair(kept, skept, M, 2 * I, "kept")
+    M, I = _two(dh, "dh")
+    dev = dh.get_device()
+    _need(dh, _BF16_TYPES, None, dev, "dh")
+    _need_fp8(dgu, sdgu, M, 2 * I, dev, "dgu")
+    _need_fp8(kept, skept, M, 2 * I, dev, "kept")
     if h is not None or sh is not None:
-        _fp8_pair(h, sh, M, I, "h")
-    _layout_rows(m_indices, M)
-    _same_device(dh, dgu, sdgu, kept, skept, h, sh, m_indices)
-    _check(lib.dg_swiglu_fp8_backward(_ptr(dgu), _ptr(sdgu), _ptr(h), _ptr(sh), _ptr(dh),
-                                      _ptr(kept), _ptr(skept), _ptr(m_indices), M, I,
-                                      _stream(stream)), "dg_swiglu_fp8_backward")
+        _need_fp8(h, sh, M, I, dev, "h")
+    if m_indices is not None:
+        _need(m_indices, (_I32,), (M,), dev, "m_indices")
+    _check(lib.dg_swiglu_fp8_backward(dgu.data_ptr(), sdgu.data_ptr(), _ptr(h), _ptr(sh),
+                                      dh.data_ptr(), kept.data_ptr(), skept.data_ptr(),
+                                      _ptr(m_indices), M, I, _launch_stream(stream, dev)),
+           "dg_swiglu_fp8_backward")
 
 
 def dg_transpose_fp8_blocks(qt, st, q, s, block_rows: int = 128, m_indices=None,
@@ -1002,20 +1033,16 @@ def dg_transpose_fp8_blocks(qt, st, q, s, block_rows: int = 128, m_indices=None,
     """qt (codes [C, M]) and st float32 [M/128, C] (block_rows 1) or [M/128,
     C/128] (block_rows 128) = the transpose of q (codes [M, C], 1 x 128 scales
     s float32 [C/128, M]), quantised anew along the rows of q."""
-    _codes(q, "q")
-    if q.dim() != 2:
-        raise ValueError("q must be [M, C]")
-    M, C = q.shape
-    _fp8_pair(q, s, M, C, "q")
-    _codes(qt, "qt")
-    if qt.shape != (C, M):
-        raise ValueError("qt must be [C, M]")
-    _shaped(st, torch.float32, (cdiv(M, 128), cdiv(C, block_rows) if block_rows > 0 else 0), "st")
-    _layout_rows(m_indices, M)
-    _same_device(q, s, qt, st, m_indices)
-    _check(lib.dg_transpose_fp8_blocks(_ptr(qt), _ptr(st), block_rows, _ptr(q), _ptr(s),
-                                       _ptr(m_indices), M, C, _stream(stream)),
-           "dg_transpose_fp8_blocks")
+    M, C = _two(q, "q")
+    dev = q.get_device()
+    _need_fp8(q, s, M, C, dev, "q")
+    _need(qt, _CODES, (C, M), dev, "qt")
+    _need(st, (_F32,), ((M + 127) // 128, C if block_rows == 1 else (C + 127) // 128), dev, "st")
+    if m_indices is not None:
+        _need(m_indices, (_I32,), (M,), dev, "m_indices")
+    _check(lib.dg_transpose_fp8_blocks(qt.data_ptr(), st.data_ptr(), block_rows, q.data_ptr(),
+                                       s.data_ptr(), _ptr(m_indices), M, C,
+                                       _launch_stream(stream, dev)), "dg_transpose_fp8_blocks")
 
 
 # ---------------------------------------------------------------------------
@@ -1188,7 +1215,7 @@ __all__ = [
     "dg_moe_layer_workspace_bytes", "dg_moe_layer", "MOE_SCORINGS",
     "dg_moe_route", "dg_moe_route_backward", "moe_route", "dg_moe_plan_rows",
     "dg_moe_plan_workspace_bytes", "dg_moe_plan", "MoePlan", "moe_plan", "dg_moe_dispatch_fp8",
-    "moe_dispatch_fp8", "dg_moe_combine", "dg_moe_combine_backward", "moe_combine",
+    "dg_moe_dispatch_fp8_workspace_bytes", "moe_dispatch_fp8", "dg_moe_combine", "dg_moe_combine_backward", "moe_combine",
     "dg_swiglu_fp8", "dg_swiglu_fp8_backward", "swiglu_fp8", "dg_transpose_fp8_blocks",
     "transpose_fp8_blocks",
 ]

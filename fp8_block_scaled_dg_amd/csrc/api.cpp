@@ -701,23 +701,42 @@ int dg_moe_plan(int32_t* rows, int32_t* pairs, int32_t* m_indices, int64_t* offs
   const size_t need = dg::plan_workspace_bytes(T, E, k);
   if (need > 0 && (!workspace || workspace_bytes < need)) return DG_ERR_WORKSPACE;
   if (!aligned(rows, 4) || !aligned(pairs, 4) || !aligned(m_indices, 4) || !aligned(offsets, 8) ||
-      !aligned(counts, 4) || !aligned(ids, 4) || !aligned(workspace, 4))
+      !aligned(counts, 4) || !aligned(ids, 4) || !aligned(workspace, 16))
     return DG_ERR_ALIGN;
   dg::PlanArgs p{rows, pairs, m_indices, offsets, counts, ids, T * k, M, E, 0, 0, nullptr};
   return from_hip(dg::launch_plan(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
+namespace {
+
+// A workspace for the scales is optional; one that is given has to hold them.
+int run_dispatch(const dg::DispatchArgs& p, void* workspace, size_t workspace_bytes, void* stream) {
+  const size_t need = dg::dispatch_workspace_bytes(p.T, p.k, p.H, p.weights != nullptr);
+  if (workspace == nullptr || workspace_bytes == 0 || need == 0) workspace = nullptr;
+  else if (workspace_bytes < need) return DG_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return DG_ERR_ALIGN;
+  return from_hip(dg::launch_dispatch(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+size_t dg_moe_dispatch_fp8_workspace_bytes(int64_t T, int k, int64_t H, int weighted) {
+  return layout_ok(T, k, 128, H, 128) ? dg::dispatch_workspace_bytes(T, k, H, weighted != 0) : 0;
+}
+
 int dg_moe_dispatch_fp8(uint8_t* a, float* sa, const void* x, int dtype, int64_t ldx,
                         const int32_t* rows, const int32_t* pairs, const float* weights,
-                        int64_t T, int k, int64_t M, int64_t H, void* stream) {
+                        int64_t T, int k, int64_t M, int64_t H, void* workspace,
+                        size_t workspace_bytes, void* stream) {
   if (!a || !sa || !x || !rows || !pairs) return DG_ERR_NULL;
   if (!dtype_ok(dtype)) return DG_ERR_UNSUPPORTED;
   if (!layout_ok(T, k, M, H, 128) || ldx < H || ldx > INT64_MAX / 4 / T) return DG_ERR_SHAPE;
   if (!aligned(a, 16) || !aligned(sa, 4) || !aligned(x, dtype_size(dtype)) || !aligned(rows, 4) ||
       !aligned(pairs, 4) || !aligned(weights, 4))
     return DG_ERR_ALIGN;
-  dg::DispatchArgs p{a, sa, x, dtype == DG_DTYPE_BF16, rows, pairs, weights, T, ldx, M, H, k, 0};
-  return from_hip(dg::launch_dispatch(p, static_cast<hipStream_t>(stream)));
+  const dg::DispatchArgs p{a, sa, x, dtype == DG_DTYPE_BF16, rows, pairs, weights, T, ldx, M, H, k,
+                           0, nullptr};
+  return run_dispatch(p, workspace, workspace_bytes, stream);
 }
 
 int dg_moe_combine(uint16_t* y, const uint16_t* c, const int32_t* rows, const float* weights,
@@ -735,7 +754,8 @@ int dg_moe_combine(uint16_t* y, const uint16_t* c, const int32_t* rows, const fl
 int dg_moe_combine_backward(uint8_t* dc, float* sdc, float* dweights, const uint16_t* dy,
                             int64_t lddy, const uint16_t* c, const int32_t* rows,
                             const int32_t* pairs, const float* weights, int64_t T, int k,
-                            int64_t M, int64_t H, void* stream) {
+                            int64_t M, int64_t H, void* workspace, size_t workspace_bytes,
+                            void* stream) {
   if (!dy || !rows || (!dc && !dweights) || !dc != !sdc || (dc && !pairs) || (dweights && !c))
     return DG_ERR_NULL;
   if (!layout_ok(T, k, M, H, 128) || lddy < H || lddy > INT64_MAX / 4 / T) return DG_ERR_SHAPE;
@@ -743,8 +763,8 @@ int dg_moe_combine_backward(uint8_t* dc, float* sdc, float* dweights, const uint
       !aligned(dweights, 4) || !aligned(rows, 4) || !aligned(pairs, 4) || !aligned(weights, 4))
     return DG_ERR_ALIGN;
   if (dc) {
-    dg::DispatchArgs p{dc, sdc, dy, true, rows, pairs, weights, T, lddy, M, H, k, 0};
-    const int st = from_hip(dg::launch_dispatch(p, static_cast<hipStream_t>(stream)));
+    const dg::DispatchArgs p{dc, sdc, dy, true, rows, pairs, weights, T, lddy, M, H, k, 0, nullptr};
+    const int st = run_dispatch(p, workspace, workspace_bytes, stream);
     if (st != DG_OK) return st;
   }
   if (!dweights) return DG_OK;
@@ -760,7 +780,7 @@ int dg_swiglu_fp8(uint8_t* h, float* sh, uint8_t* kept, float* skept, const uint
   if (!aligned(h, 16) || !aligned(kept, 16) || !aligned(gu, 16) || !aligned(sh, 4) ||
       !aligned(skept, 4))
     return DG_ERR_ALIGN;
-  const dg::SwigluArgs p{h, sh, kept, skept, gu, nullptr, nullptr, nullptr, m_indices, M, I};
+  const dg::SwigluArgs p{h, sh, kept, skept, gu, nullptr, nullptr, nullptr, m_indices, M, I, 0};
   return from_hip(dg::launch_swiglu(p, false, static_cast<hipStream_t>(stream)));
 }
 
@@ -774,7 +794,7 @@ int dg_swiglu_fp8_backward(uint8_t* dgu, float* sdgu, uint8_t* h, float* sh, con
       !aligned(sdgu, 4) || !aligned(sh, 4) || !aligned(skept, 4))
     return DG_ERR_ALIGN;
   const dg::SwigluArgs p{h, sh, const_cast<uint8_t*>(kept), const_cast<float*>(skept),
-                         nullptr, dh, dgu, sdgu, m_indices, M, I};
+                         nullptr, dh, dgu, sdgu, m_indices, M, I, 0};
   return from_hip(dg::launch_swiglu(p, true, static_cast<hipStream_t>(stream)));
 }
 

@@ -211,9 +211,11 @@ struct DispatchArgs {
   const float* weights;
   int64_t T, ldx, M, H;
   int k;
-  uint32_t token_groups;  // set by the launch
+  uint32_t token_groups;  // set by the launch, as parked
+  float* parked;          // in the workspace (null: the scales go out one by one)
 };
-hipError_t launch_dispatch(DispatchArgs p, hipStream_t stream);
+size_t dispatch_workspace_bytes(int64_t T, int k, int64_t H, bool weighted);
+hipError_t launch_dispatch(DispatchArgs p, void* workspace, hipStream_t stream);
 
 // Rows of the layout back to tokens: y, and the gradient of the weights.
 struct CombineArgs {
@@ -242,8 +244,9 @@ struct SwigluArgs {
   float* sdgu;
   const int32_t* m_indices;
   int64_t M, I;
+  int tile_rows;           // set by the launch
 };
-hipError_t launch_swiglu(const SwigluArgs& p, bool backward, hipStream_t stream);
+hipError_t launch_swiglu(SwigluArgs p, bool backward, hipStream_t stream);
 
 // E4M3 rows [M][C] with 1 x 128 scales -> [C][M] with scales over 128 rows of one
 // column, or of 128.

@@ -14,6 +14,7 @@
 // times.
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
+#include "fp8_rows.hpp"
 
 namespace dg {
 namespace {
@@ -35,81 +36,162 @@ __device__ __forceinline__ void load8(const void* x, bool bf16, int64_t at, floa
   }
 }
 
-// Eight values of a lane's 128-column block (16 lanes): codes and scale.
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], float& scale) {
-  const float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
-  const BlockScale s = block_scale(row16_max(abs_max4(abs_max4(0.0f, a), b)));
-  scale = s.s;
-  return make_uint2(encode4_block(a, s), encode4_block(b, s));
+// The slots of token t, one a lane: row in the layout (-1: none) and weight.
+// Read at once; slot j is then a lane of a register.
+struct Slots {
+  int row;
+  float weight;
+  __device__ __forceinline__ Slots(const int32_t* rows, const float* weights, int64_t t, int k,
+                                   int64_t M, int lane) {
+    const bool ok = lane < k;
+    row = ok ? rows[t * k + lane] : -1;
+    weight = ok && weights ? weights[t * k + lane] : 1.0f;
+    if (row >= M) row = -1;
+  }
+  __device__ __forceinline__ int row_of(int j) const { return __builtin_amdgcn_readlane(row, j); }
+  __device__ __forceinline__ float weight_of(int j) const {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), j));
+  }
+};
+
+// f(IntTag<K>) for the smallest K = 1, 2, 4, 8, 16 that is not below k.
+template <int K = 1, class F>
+__device__ __host__ __forceinline__ void with_slots(int k, F&& f) {
+  if constexpr (K == kMoeMaxSlots) {
+    f(IntTag<K>{});
+  } else {
+    if (k <= K) f(IntTag<K>{});
+    else with_slots<2 * K>(k, f);
+  }
 }
 
-__device__ __forceinline__ int row_of(const int32_t* rows, int64_t at, int64_t M) {
-  const int r = rows[at];
-  return r < M ? r : -1;
+// Fills rows first .. 31 of the 32 from r0 on (the end of an expert's last block)
+// with zero codes, columns c .. c + 15 of this thread.
+__device__ __forceinline__ void fill_rows(const DispatchArgs& p, int64_t r0, int first, int64_t c) {
+  const uint32_t none[4] = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int r = first; r < 32; ++r) store_stream(p.a + (r0 + r) * p.H + c, none);
 }
 
-// Workgroups 0 .. token_groups - 1: a wave a (token, 512 columns); the others: the
-// rows that fill an expert's last block, 2048 columns each, with zeros.
+// A wave a (token, 512 columns).  PARKED: the scales go to the workspace, token by
+// token ([T][H/128], WEIGHTED [T k][H/128]), and dispatch_scales_kernel takes them
+// from there; else each goes to its place, and workgroups from token_groups on fill
+// the ends of the experts' last blocks, 32 rows by 4096 columns each.
+template <bool WEIGHTED, bool PARKED>
 __global__ void __launch_bounds__(256) dispatch_kernel(DispatchArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (blockIdx.x >= p.token_groups) {
-    const uint32_t i = blockIdx.x - p.token_groups, parts = (uint32_t)((p.H + 2047) / 2048);
-    const int64_t r0 = (int64_t)(i / parts) * 128, c = (int64_t)(i % parts) * 2048 + threadIdx.x * 8;
-    if (p.pairs[r0] < 0 || p.pairs[r0 + 127] >= 0 || c >= p.H) return;
-    for (int r = 127; r > 0 && p.pairs[r0 + r] < 0; --r) {
-      *reinterpret_cast<uint2*>(p.a + (r0 + r) * p.H + c) = make_uint2(0, 0);
-      if ((threadIdx.x & 15) == 0) p.sa[c / 128 * p.M + r0 + r] = 0.0f;
-    }
+  if (!PARKED && blockIdx.x >= p.token_groups) {
+    const uint32_t i = blockIdx.x - p.token_groups, parts = (uint32_t)((p.H + 4095) / 4096);
+    const int64_t r0 = (int64_t)(i / parts) * 32, c = (int64_t)(i % parts) * 4096 + threadIdx.x * 16;
+    if (p.pairs[r0 & ~int64_t(127)] < 0) return;
+    const int first = (int)__popcll(__ballot(lane < 32 && p.pairs[r0 + (lane & 31)] >= 0));
+    if (c >= p.H) return;
+    fill_rows(p, r0, first, c);
+    if ((threadIdx.x & 7) == 0)
+      for (int r = first; r < 32; ++r) p.sa[c / 128 * p.M + r0 + r] = 0.0f;
     return;
   }
   const uint32_t unit = blockIdx.x * 4 + wave, units = (uint32_t)((p.H + kCols - 1) / kCols);
   const int64_t t = unit / units, c = (int64_t)(unit % units) * kCols + lane * 8;
-  if (t >= p.T || c >= p.H) return;
+  if (t >= p.T) return;
+  const Slots slots(p.rows, p.weights, t, p.k, p.M, lane);
+  if (c >= p.H) return;  // whole blocks of 16 lanes: the first k, with the slots, stay
   float v[8];
   load8(p.x, p.bf16, t * p.ldx + c, v);
-  float scale;
-  uint2 q = encode8(v, scale);
+  const float top = group_top<16>(top_of(v));
+  const bool leader = (lane & 15) == 0;
+  uint32_t q[2];
+  float scale = 0.0f;
+  if constexpr (!WEIGHTED) {
+    const RowScale b = row_scale(v, top);
+    encode_values(v, b, q);
+    scale = b.scale;
+    if (PARKED && leader) p.parked[t * (p.H / 128) + c / 128] = scale;
+  }
   for (int j = 0; j < p.k; ++j) {
-    const int row = row_of(p.rows, t * p.k + j, p.M);
+    const int row = slots.row_of(j);
     if (row < 0) continue;
-    if (p.weights) {
-      const float w = p.weights[t * p.k + j];
+    if constexpr (WEIGHTED) {
+      const float w = slots.weight_of(j);
       float wv[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) wv[i] = w * v[i];
-      q = encode8(wv, scale);
+      // rounding is monotone: the largest product is that of the largest value
+      const RowScale b = row_scale(wv, fabsf(w) * top);
+      encode_values(wv, b, q);
+      scale = b.scale;
+      if (PARKED && leader) p.parked[(t * p.k + j) * (p.H / 128) + c / 128] = scale;
     }
-    *reinterpret_cast<uint2*>(p.a + (int64_t)row * p.H + c) = q;
-    if ((lane & 15) == 0) p.sa[c / 128 * p.M + row] = scale;
+    store_stream(p.a + (int64_t)row * p.H + c, q);
+    if (!PARKED && leader) p.sa[c / 128 * p.M + row] = scale;
   }
 }
 
+// Parked scales to their places, 32 rows by 64 blocks of columns a workgroup
+// through LDS (runs of 128 bytes both ways), and zeros where a row only fills its
+// block.
+template <bool WEIGHTED>
+__global__ void __launch_bounds__(256) dispatch_scales_kernel(DispatchArgs p) {
+  __shared__ float s_scale[32][65];
+  __shared__ int s_from[32];
+  const int t = threadIdx.x, lane = t & 63;
+  const int64_t kbs = p.H / 128;
+  const uint32_t parts = (uint32_t)((kbs + 63) / 64);
+  const int64_t r0 = (int64_t)(blockIdx.x / parts) * 32, kb0 = (int64_t)(blockIdx.x % parts) * 64;
+  if (p.pairs[r0 & ~int64_t(127)] < 0) return;
+  const int n = (int)(kbs - kb0 < 64 ? kbs - kb0 : 64);
+  const int pair = p.pairs[r0 + (lane & 31)];
+  const int first = (int)__popcll(__ballot(lane < 32 && pair >= 0));
+  if (t < 32) s_from[t] = WEIGHTED ? pair : pair / p.k;  // of no use where pair is -1
+  __syncthreads();
+#pragma unroll
+  for (int r = t >> 6; r < 32; r += 4)
+    s_scale[r][lane] = r < first && lane < n ? p.parked[(int64_t)s_from[r] * kbs + kb0 + lane] : 0.0f;
+  for (int64_t c = kb0 * 128 + t * 16; c < (kb0 + n) * 128; c += 4096) fill_rows(p, r0, first, c);
+  __syncthreads();
+#pragma unroll
+  for (int kb = t >> 5; kb < 64; kb += 8)
+    if (kb < n) p.sa[(kb0 + kb) * p.M + r0 + (t & 31)] = s_scale[t & 31][kb];
+}
+
+// All slots' rows are asked for before the first is added.
+template <int K>
 __global__ void __launch_bounds__(256) combine_kernel(CombineArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t unit = blockIdx.x * 4 + wave, units = (uint32_t)((p.H + kCols - 1) / kCols);
-  const int64_t t = unit / units, c = (int64_t)(unit % units) * kCols + lane * 8;
-  if (t >= p.T || c >= p.H) return;
+  const int64_t t = unit / units, c0 = (int64_t)(unit % units) * kCols + lane * 8;
+  if (t >= p.T) return;
+  // the first k lanes hold the slots, so all stay; past the end they repeat the
+  // last columns, unstored
+  const int64_t c = c0 < p.H ? c0 : p.H - 8;
+  const Slots slots(p.rows, p.weights, t, p.k, p.M, lane);
+  u4 v[K], res = {};
+  if (p.residual) res = *reinterpret_cast<const u4*>(p.residual + t * p.H + c);
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+    if (slots.row_of(j) >= 0)
+      v[j] = __builtin_nontemporal_load(
+          reinterpret_cast<const u4*>(p.c + (int64_t)slots.row_of(j) * p.H + c));
   float y[8] = {};
-  for (int j = 0; j < p.k; ++j) {
-    const int row = row_of(p.rows, t * p.k + j, p.M);
-    if (row < 0) continue;
-    const float w = p.weights ? p.weights[t * p.k + j] : 1.0f;
-    float v[8];
-    load8(p.c, true, (int64_t)row * p.H + c, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(w, v[i], y[i]);
-  }
-  if (p.residual) {
-    float v[8];
-    load8(p.residual, true, t * p.H + c, v);
+  for (int j = 0; j < K; ++j)
+    if (slots.row_of(j) >= 0) {
+      const float w = slots.weight_of(j);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] += v[i];
-  }
-  *reinterpret_cast<uint4*>(p.y + t * p.H + c) =
-      make_uint4(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]),
-                 bf16x2_rne(y[6], y[7]));
+      for (int i = 0; i < 4; ++i) {
+        y[2 * i] = fmaf(w, __uint_as_float(v[j][i] << 16), y[2 * i]);
+        y[2 * i + 1] = fmaf(w, __uint_as_float(v[j][i] & 0xFFFF0000u), y[2 * i + 1]);
+      }
+    }
+  u4 out;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // without a residual the sum keeps the sign of a zero
+    out[i] = p.residual ? bf16x2_rne(y[2 * i] + __uint_as_float(res[i] << 16),
+                                     y[2 * i + 1] + __uint_as_float(res[i] & 0xFFFF0000u))
+                        : bf16x2_rne(y[2 * i], y[2 * i + 1]);
+  if (c0 < p.H) __builtin_nontemporal_store(out, reinterpret_cast<u4*>(p.y + t * p.H + c));
 }
 
 __device__ __forceinline__ float wave_add(float v) {
@@ -119,24 +201,37 @@ __device__ __forceinline__ float wave_add(float v) {
 }
 
 // One workgroup a token: its waves' partial sums meet in LDS, in wave order.
+template <int K>
 __global__ void __launch_bounds__(256) combine_dot_kernel(CombineArgs p) {
   __shared__ float s_sum[4][kMoeMaxSlots];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x;
-  for (int j = 0; j < p.k; ++j) {
-    const int row = row_of(p.rows, t * p.k + j, p.M);
-    float sum = 0.0f;
-    if (row >= 0)
-      for (int64_t c = threadIdx.x * 8; c < p.H; c += 2048) {
-        float a[8], b[8];
-        load8(p.dy, true, t * p.lddy + c, a);
-        load8(p.c, true, (int64_t)row * p.H + c, b);
+  const Slots slots(p.rows, nullptr, t, p.k, p.M, lane);
+  float sum[K] = {};
+  for (int64_t c = threadIdx.x * 8; c < p.H; c += 2048) {
+    u4 v[K];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(a[i], b[i], sum);
+    for (int j = 0; j < K; ++j)
+      if (slots.row_of(j) >= 0)
+        v[j] = __builtin_nontemporal_load(
+            reinterpret_cast<const u4*>(p.c + (int64_t)slots.row_of(j) * p.H + c));
+    float d[8];
+    load8(p.dy, true, t * p.lddy + c, d);
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (slots.row_of(j) >= 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[j] = fmaf(d[2 * i], __uint_as_float(v[j][i] << 16), sum[j]);
+          sum[j] = fmaf(d[2 * i + 1], __uint_as_float(v[j][i] & 0xFFFF0000u), sum[j]);
+        }
       }
-    sum = wave_add(sum);
-    if (lane == 0) s_sum[wave][j] = sum;
+  }
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const float s = wave_add(sum[j]);
+    if (lane == 0) s_sum[wave][j] = s;
   }
   __syncthreads();
   if (threadIdx.x < p.k) {
@@ -147,22 +242,49 @@ __global__ void __launch_bounds__(256) combine_dot_kernel(CombineArgs p) {
 
 }  // namespace
 
-hipError_t launch_dispatch(DispatchArgs p, hipStream_t stream) {
+// A scale stored by itself is one request to the L2, and there are as many of them
+// as of the codes' lines: 8192 x 7168 to 8 of 256 (3.7 million scales) 193 us with
+// them, 148 us parked (111 + 37).  The second launch is worth it from about a million scales:
+// 4001 x 2048 to 4 of 60 (256 thousand) 15.3 against 18.1 us.
+size_t dispatch_workspace_bytes(int64_t T, int k, int64_t H, bool weighted) {
+  if (T * k < (int64_t(1) << 20) / (H / 128)) return 0;
+  return (size_t)(weighted ? T * k : T) * (H / 128) * sizeof(float);
+}
+
+hipError_t launch_dispatch(DispatchArgs p, void* workspace, hipStream_t stream) {
   const int64_t units = (p.H + kCols - 1) / kCols;
   p.token_groups = (uint32_t)((p.T * units + 3) / 4);
-  const int64_t fill = p.M / 128 * ((p.H + 2047) / 2048);
-  hipLaunchKernelGGL(dispatch_kernel, dim3((unsigned)(p.token_groups + fill)), dim3(256), 0, stream, p);
+  p.parked = static_cast<float*>(workspace);
+  const int64_t fill = workspace ? 0 : p.M / 32 * ((p.H + 4095) / 4096);
+  const dim3 grid((unsigned)(p.token_groups + fill)), block(256);
+  if (!workspace) {
+    if (p.weights) hipLaunchKernelGGL((dispatch_kernel<true, false>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((dispatch_kernel<false, false>), grid, block, 0, stream, p);
+    return hipGetLastError();
+  }
+  const dim3 rows((unsigned)(p.M / 32 * ((p.H / 128 + 63) / 64)));
+  if (p.weights) hipLaunchKernelGGL((dispatch_kernel<true, true>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((dispatch_kernel<false, true>), grid, block, 0, stream, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (p.weights) hipLaunchKernelGGL(dispatch_scales_kernel<true>, rows, block, 0, stream, p);
+  else hipLaunchKernelGGL(dispatch_scales_kernel<false>, rows, block, 0, stream, p);
   return hipGetLastError();
 }
 
 hipError_t launch_combine(const CombineArgs& p, hipStream_t stream) {
   const int64_t units = (p.H + kCols - 1) / kCols;
-  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((p.T * units + 3) / 4)), dim3(256), 0, stream, p);
+  const dim3 grid((unsigned)((p.T * units + 3) / 4));
+  with_slots(p.k, [&](auto K) {
+    hipLaunchKernelGGL(combine_kernel<decltype(K)::value>, grid, dim3(256), 0, stream, p);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_combine_dot(const CombineArgs& p, hipStream_t stream) {
-  hipLaunchKernelGGL(combine_dot_kernel, dim3((unsigned)p.T), dim3(256), 0, stream, p);
+  with_slots(p.k, [&](auto K) {
+    hipLaunchKernelGGL(combine_dot_kernel<decltype(K)::value>, dim3((unsigned)p.T), dim3(256), 0, stream, p);
+  });
   return hipGetLastError();
 }
 

@@ -37,21 +37,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(PlanArgs p) {
     if (e >= 0) atomicAdd(&s_count[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kPlanThreads)
-    p.chunk_counts[(int64_t)blockIdx.x * p.E + e] = s_count[e];
+  const int pitch = (p.E + 3) & ~3;
+  for (int e = threadIdx.x; e < pitch; e += kPlanThreads)
+    p.chunk_counts[(int64_t)blockIdx.x * pitch + e] = e < p.E ? s_count[e] : 0;
 }
 
 template <bool SELF>
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanArgs p) {
   __shared__ int s_next[kPlanWaves][kMoeMaxExperts];  // a wave's next row of each expert
-  __shared__ int s_total[kMoeMaxExperts], s_before[SELF ? kMoeMaxExperts : 1];
+  __shared__ int s_total[kMoeMaxExperts], s_before[kMoeMaxExperts];
   __shared__ int s_offset[kMoeMaxExperts + 1], s_sum[kPlanWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t begin = blockIdx.x * p.chunk, end = begin + p.chunk < p.n ? begin + p.chunk : p.n;
   for (int e = tid; e < p.E; e += kPlanThreads) {
     s_total[e] = 0;
-    if constexpr (SELF) s_before[e] = 0;
+    s_before[e] = 0;
 #pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) s_next[w][e] = 0;
   }
@@ -72,25 +73,37 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanArgs p) {
         if (i < begin) atomicAdd(&s_before[e], 1);
       }
     }
-    __syncthreads();
+  } else {
+    // four experts a thread, the chunks shared out over the threads that have
+    // the same four
+    const int quads = (p.E + 3) / 4, q = tid % quads, first = tid / quads, step = kPlanThreads / quads;
+    const int4* counts = reinterpret_cast<const int4*>(p.chunk_counts);
+    if (first < step) {
+      int4 t = make_int4(0, 0, 0, 0), b = t;
+#pragma unroll 8
+      for (int c = first; c < p.chunks; c += step) {
+        const int4 n = counts[(int64_t)c * quads + q];
+        t.x += n.x; t.y += n.y; t.z += n.z; t.w += n.w;
+        if (c < (int)blockIdx.x) { b.x += n.x; b.y += n.y; b.z += n.z; b.w += n.w; }
+      }
+      const int tt[4] = {t.x, t.y, t.z, t.w}, bb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * q + i < p.E) {
+          atomicAdd(&s_total[4 * q + i], tt[i]);
+          atomicAdd(&s_before[4 * q + i], bb[i]);
+        }
+    }
   }
+  __syncthreads();
   // experts 2 tid and 2 tid + 1
   int total[2] = {0, 0}, before[2] = {0, 0}, padded[2], own = 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int e = 2 * tid + h;
     if (e < p.E) {
-      if constexpr (SELF) {
-        total[h] = s_total[e];
-        before[h] = s_before[e];
-      } else {
-        for (int c = 0; c < p.chunks; ++c) {
-          const int n = p.chunk_counts[(int64_t)c * p.E + e];
-          total[h] += n;
-          if (c < (int)blockIdx.x) before[h] += n;
-        }
-        s_total[e] = total[h];
-      }
+      total[h] = s_total[e];
+      before[h] = s_before[e];
     }
     padded[h] = (total[h] + 127) & ~127;
     own += padded[h];
@@ -187,7 +200,7 @@ int64_t plan_rows(int64_t T, int E, int k) {
 
 size_t plan_workspace_bytes(int64_t T, int E, int k) {
   const int64_t n = T * k;
-  return n <= kPlanSelfPairs ? 0 : (size_t)kPlanMaxChunks * E * sizeof(int);
+  return n <= kPlanSelfPairs ? 0 : (size_t)kPlanMaxChunks * ((E + 3) / 4) * sizeof(int4);
 }
 
 hipError_t launch_plan(PlanArgs p, void* workspace, hipStream_t stream) {

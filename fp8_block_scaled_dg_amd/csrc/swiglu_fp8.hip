@@ -14,6 +14,7 @@
 // not touched.  All are bound by HBM.
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
+#include "fp8_rows.hpp"
 
 namespace dg {
 namespace {
@@ -25,108 +26,120 @@ __device__ __forceinline__ float2 decode2(uint32_t codes, bool high) {
                     : __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
   return make_float2(v.x, v.y);
 }
-__device__ __forceinline__ float4 decode4(uint32_t codes) {
-  const float2 a = decode2(codes, false), b = decode2(codes, true);
-  return make_float4(a.x, a.y, b.x, b.y);
+// 1 / (1 + e^-g) with the hardware's exp2 and reciprocal (one ulp each): off by
+// at most (|g| + 2) 2^-23 relative, against 2^-4 of the E4M3 codes that follow.
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
-// 1 real row, 0 a row that fills its block, -1 a row of a block without expert
-__device__ __forceinline__ int kind_of(const int32_t* m_indices, int64_t r) {
-  if (!m_indices || m_indices[r] >= 0) return 1;
-  return m_indices[r & ~int64_t(127)] >= 0 ? 0 : -1;
+// A workgroup takes p.tile_rows rows by 512 hidden units, a wave a row at a time,
+// eight units a lane: a block of h is 16 lanes, one of gate/up 8.  The scales of
+// the tile are put together in LDS and leave in runs along the rows.
+constexpr int kUnits = 512, kTileRows = 32;
+struct ScaleTile {
+  float h[kUnits / 128][kTileRows], g[kUnits / 64][kTileRows];
+};
+
+template <int KB>
+__device__ __forceinline__ void store_scales(const float (&s)[KB][kTileRows], float* out, int64_t M,
+                                             int64_t kbs, int64_t kb0, int64_t r0, int tile_rows) {
+  for (int i = threadIdx.x; i < KB * tile_rows; i += 256) {
+    const int kb = i / tile_rows, r = i % tile_rows;
+    if (kb0 + kb < kbs && r0 + r < M) out[(kb0 + kb) * M + r0 + r] = s[kb][r];
+  }
 }
 
-__device__ __forceinline__ float max4(float m, const float* v) {
-  return abs_max4(m, make_float4(v[0], v[1], v[2], v[3]));
-}
-
-// N values (a multiple of 4) of a block with scale s
-template <int N>
-__device__ __forceinline__ void encode(const float* v, const BlockScale& s, uint8_t* out) {
-  uint32_t w[N / 4];
-#pragma unroll
-  for (int i = 0; i < N / 4; ++i)
-    w[i] = encode4_block(make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]), s);
-  __builtin_memcpy(__builtin_assume_aligned(out, N), w, N);
-}
-template <int N>
-__device__ __forceinline__ float top_of(const float* v) {
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < N; i += 4) m = max4(m, v + i);
-  return m;
-}
-
-// A wave takes 512 hidden units of a row, eight a lane: a block of h is 16
-// lanes, one of gate/up 8.  Four rows a workgroup.
-__global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs p) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t parts = (uint32_t)((p.I + 511) / 512);
-  const int64_t r = (int64_t)(blockIdx.x / parts) * 4 + wave;
-  const int64_t c = (int64_t)(blockIdx.x % parts) * 512 + lane * 8;
-  if (r >= p.M || c >= p.I) return;
-  const int kind = kind_of(p.m_indices, r);
-  if (kind < 0) return;
-  float gu[16] = {}, h[8] = {};
-  if (kind > 0) {
-    const uint4* s = reinterpret_cast<const uint4*>(p.gu + r * 2 * p.I + 2 * c);
-    const uint4 a = s[0], b = s[1];
-    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      gu[2 * i] = __uint_as_float(u[i] << 16);
-      gu[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-      h[i] = silu_f(gu[2 * i]) * gu[2 * i + 1];
+// What a lane reads of a row: 16 BF16 gate/up values, or 16 codes with their
+// scale and 8 BF16 values of dh.
+template <bool FORWARD>
+struct RowInput {
+  u4 a, b;
+  float s;
+  __device__ __forceinline__ void load(const SwigluArgs& p, int64_t r, int64_t c) {
+    if constexpr (FORWARD) {
+      const u4* x = reinterpret_cast<const u4*>(p.gu + r * 2 * p.I + 2 * c);
+      a = __builtin_nontemporal_load(x);
+      b = __builtin_nontemporal_load(x + 1);
+    } else {
+      a = __builtin_nontemporal_load(reinterpret_cast<const u4*>(p.kept + r * 2 * p.I + 2 * c));
+      b = __builtin_nontemporal_load(reinterpret_cast<const u4*>(p.dh + r * p.I + c));
+      s = p.skept[2 * c / 128 * p.M + r];
     }
   }
-  const BlockScale s = block_scale(lane_group_max<16>(top_of<8>(h)));
-  encode<8>(h, s, p.h + r * p.I + c);
-  if ((lane & 15) == 0) p.sh[c / 128 * p.M + r] = s.s;
-  if (p.kept) {
-    const BlockScale g = block_scale(lane_group_max<8>(top_of<16>(gu)));
-    encode<16>(gu, g, p.kept + r * 2 * p.I + 2 * c);
-    if ((lane & 7) == 0) p.skept[2 * c / 128 * p.M + r] = g.s;
-  }
-}
-
-__global__ void __launch_bounds__(256) swiglu_backward_kernel(SwigluArgs p) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t parts = (uint32_t)((p.I + 511) / 512);
-  const int64_t r = (int64_t)(blockIdx.x / parts) * 4 + wave;
-  const int64_t c = (int64_t)(blockIdx.x % parts) * 512 + lane * 8;
-  if (r >= p.M || c >= p.I) return;
-  const int kind = kind_of(p.m_indices, r);
-  if (kind < 0) return;
-  float d[16] = {}, h[8] = {};
-  if (kind > 0) {
-    const uint4 codes = *reinterpret_cast<const uint4*>(p.kept + r * 2 * p.I + 2 * c);
-    const float s = p.skept[2 * c / 128 * p.M + r];
-    const uint4 b = *reinterpret_cast<const uint4*>(p.dh + r * p.I + c);
-    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w}, u[4] = {b.x, b.y, b.z, b.w};
+  // g: gate/up or their gradients, h: silu(gate) * up
+  __device__ __forceinline__ void compute(float (&g)[16], float (&h)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = decode4(w[i]);
-      const float dh[2] = {__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u)};
-      const float gate[2] = {v.x * s, v.z * s}, up[2] = {v.y * s, v.w * s};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float sig = 1.0f / (1.0f + expf(-gate[j])), a = gate[j] * sig;
-        d[4 * i + 2 * j] = dh[j] * up[j] * (sig + a * (1.0f - sig));
-        d[4 * i + 2 * j + 1] = dh[j] * a;
-        h[2 * i + j] = a * up[j];
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (FORWARD) {
+        const uint32_t u = j < 4 ? a[j & 3] : b[j & 3];
+        g[2 * j] = __uint_as_float(u << 16);
+        g[2 * j + 1] = __uint_as_float(u & 0xFFFF0000u);
+        h[j] = g[2 * j] * sigmoid(g[2 * j]) * g[2 * j + 1];
+      } else {
+        const float2 v = decode2(a[j >> 1], j & 1);
+        const float dh = __uint_as_float(j & 1 ? b[j >> 1] & 0xFFFF0000u : b[j >> 1] << 16);
+        const float gate = v.x * s, up = v.y * s, sig = sigmoid(gate), x = gate * sig;
+        g[2 * j] = dh * up * __builtin_fmaf(x, 1.0f - sig, sig);
+        g[2 * j + 1] = dh * x;
+        h[j] = x * up;
       }
     }
   }
-  const BlockScale g = block_scale(lane_group_max<8>(top_of<16>(d)));
-  encode<16>(d, g, p.dgu + r * 2 * p.I + 2 * c);
-  if ((lane & 7) == 0) p.sdgu[2 * c / 128 * p.M + r] = g.s;
-  if (p.h) {
-    const BlockScale s = block_scale(lane_group_max<16>(top_of<8>(h)));
-    encode<8>(h, s, p.h + r * p.I + c);
-    if ((lane & 15) == 0) p.sh[c / 128 * p.M + r] = s.s;
+};
+
+// FORWARD: h (and KEEP: the checkpoint) from gu; else dgu (and KEEP: h) from dh
+// and the checkpoint.  A wave has the next row's values on their way while it
+// works on a row.
+template <bool FORWARD, bool KEEP>
+__global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs p) {
+  constexpr bool H = FORWARD || KEEP, G = !FORWARD || KEEP;
+  __shared__ ScaleTile tile;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t parts = (uint32_t)((p.I + kUnits - 1) / kUnits), part = blockIdx.x % parts;
+  const int64_t r0 = (int64_t)(blockIdx.x / parts) * p.tile_rows, c0 = (int64_t)part * kUnits + lane * 8;
+  if (p.m_indices && p.m_indices[r0 & ~int64_t(127)] < 0) return;
+  // lanes past the last column (whole blocks of 16) repeat a lane's work, unstored
+  const bool inside = c0 < p.I;
+  const int64_t c = inside ? c0 : p.I - 8;
+  // this wave's rows are wave, wave + 4, ..; bit i: row r0 + i is real
+  const int rows = (int)(p.M - r0 < p.tile_rows ? p.M - r0 : p.tile_rows);
+  const uint64_t real = __ballot(lane < rows && (!p.m_indices || p.m_indices[r0 + lane] >= 0));
+  uint8_t* const codes = FORWARD ? p.kept : p.dgu;
+  RowInput<FORWARD> next;
+  if (real >> wave & 1) next.load(p, r0 + wave, c);
+  for (int i = wave; i < rows; i += 4) {
+    const int64_t r = r0 + i;
+    const RowInput<FORWARD> in = next;
+    if (i + 4 < rows && (real >> (i + 4) & 1)) next.load(p, r + 4, c);
+    uint32_t wh[2] = {0, 0}, wg[4] = {0, 0, 0, 0};
+    float sh = 0.0f, sg = 0.0f;
+    if (real >> i & 1) {  // the same in every lane
+      float g[16], h[8];
+      in.compute(g, h);
+      if constexpr (H) {
+        const RowScale b = row_scale(h, group_top<16>(top_of(h)));
+        encode_values(h, b, wh);
+        sh = b.scale;
+      }
+      if constexpr (G) {
+        const RowScale b = row_scale(g, group_top<8>(top_of(g)));
+        encode_values(g, b, wg);
+        sg = b.scale;
+      }
+    }
+    if constexpr (H) {
+      if (inside) store_stream(p.h + r * p.I + c, wh);
+      if ((lane & 15) == 0) tile.h[lane >> 4][i] = sh;
+    }
+    if constexpr (G) {
+      if (inside) store_stream(codes + r * 2 * p.I + 2 * c, wg);
+      if ((lane & 7) == 0) tile.g[lane >> 3][i] = sg;
+    }
   }
+  __syncthreads();
+  if constexpr (H) store_scales(tile.h, p.sh, p.M, p.I / 128, part * 4, r0, p.tile_rows);
+  if constexpr (G) store_scales(tile.g, FORWARD ? p.skept : p.sdgu, p.M, p.I / 64, part * 8, r0, p.tile_rows);
 }
 
 // A tile of 128 rows by 128 columns; thread: 4 columns by 16 rows, the eight
@@ -140,53 +153,53 @@ __global__ void __launch_bounds__(256) transpose_blocks_kernel(TransposeArgs p) 
   const int64_t r0 = (int64_t)rb * 128, c0 = (int64_t)cb * 128;
   if (p.m_indices && p.m_indices[r0] < 0) return;
   const float* scales = p.s + cb * p.M + r0 + 16 * rg;
-  float4 v[16];
-  float4 top = make_float4(0.f, 0.f, 0.f, 0.f);
+  float v[4][16], top[4];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(p.q + (r0 + 16 * rg + i) * p.C + c0 + 4 * cg);
     const float s = scales[i];
-    v[i] = decode4(w);
-    v[i].x *= s; v[i].y *= s; v[i].z *= s; v[i].w *= s;
-    top.x = fmaxf(top.x, fabsf(v[i].x));
-    top.y = fmaxf(top.y, fabsf(v[i].y));
-    top.z = fmaxf(top.z, fabsf(v[i].z));
-    top.w = fmaxf(top.w, fabsf(v[i].w));
+    const float2 a = decode2(w, false), b = decode2(w, true);
+    v[0][i] = a.x * s;
+    v[1][i] = a.y * s;
+    v[2][i] = b.x * s;
+    v[3][i] = b.y * s;
   }
-  if constexpr (COLUMN) {
-    top.x = lane_group_max<8>(top.x);
-    top.y = lane_group_max<8>(top.y);
-    top.z = lane_group_max<8>(top.z);
-    top.w = lane_group_max<8>(top.w);
-  } else {
-    float m = wave_max(abs_max4(0.0f, top));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) top[j] = group_top<8>(top_of(v[j]));
+  if constexpr (!COLUMN) {
+    float m = wave_max(join_top(join_top(top[0], top[1]), join_top(top[2], top[3])));
     if ((t & 63) == 0) s_top[t >> 6] = m;
     __syncthreads();
     m = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
-    top = make_float4(m, m, m, m);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top[j] = m;
   }
-  const float tops[4] = {top.x, top.y, top.z, top.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const BlockScale s = block_scale(tops[j]);
-    float col[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) col[i] = j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w;
-    encode<16>(col, s, p.qt + (c0 + 4 * cg + j) * p.M + r0 + 16 * rg);
+    const RowScale b = row_scale(v[j], top[j]);
+    uint32_t w[4];
+    encode_values(v[j], b, w);
+    store_stream(p.qt + (c0 + 4 * cg + j) * p.M + r0 + 16 * rg, w);
     if constexpr (COLUMN) {
-      if (rg == 0) p.st[rb * p.C + c0 + 4 * cg + j] = s.s;
+      if (rg == 0) p.st[rb * p.C + c0 + 4 * cg + j] = b.scale;
     } else if (t == 0 && j == 0) {
-      p.st[(int64_t)rb * across + cb] = s.s;
+      p.st[(int64_t)rb * across + cb] = b.scale;
     }
   }
 }
 
 }  // namespace
 
-hipError_t launch_swiglu(const SwigluArgs& p, bool backward, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.I + 511) / 512 * ((p.M + 3) / 4)));
-  if (backward) hipLaunchKernelGGL(swiglu_backward_kernel, grid, dim3(256), 0, stream, p);
-  else hipLaunchKernelGGL(swiglu_kernel, grid, dim3(256), 0, stream, p);
+hipError_t launch_swiglu(SwigluArgs p, bool backward, hipStream_t stream) {
+  const int64_t parts = (p.I + kUnits - 1) / kUnits;
+  // long runs of scales, but at least four workgroups a CU
+  p.tile_rows = kTileRows;
+  while (p.tile_rows > 4 && (p.M + p.tile_rows - 1) / p.tile_rows * parts < 1024) p.tile_rows /= 2;
+  const dim3 grid((unsigned)((p.M + p.tile_rows - 1) / p.tile_rows * parts)), block(256);
+  if (!backward && !p.kept) hipLaunchKernelGGL((swiglu_kernel<true, false>), grid, block, 0, stream, p);
+  else if (!backward) hipLaunchKernelGGL((swiglu_kernel<true, true>), grid, block, 0, stream, p);
+  else if (!p.h) hipLaunchKernelGGL((swiglu_kernel<false, false>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((swiglu_kernel<false, true>), grid, block, 0, stream, p);
   return hipGetLastError();
 }
 

@@ -604,7 +604,7 @@ int dg_moe_route_backward(void *dlogits, int64_t ldd, const float *dweights, con
  *   M         : rows of the layout's arrays, a multiple of 128, at least
  *               dg_moe_plan_rows(T, E, k), which suffices for every ids.
  *   workspace : dg_moe_plan_workspace_bytes(T, E, k) bytes (0: none needed),
- *               4-byte aligned, any contents, clobbered; calls that may run at
+ *               16-byte aligned, any contents, clobbered; calls that may run at
  *               the same time need distinct ones.
  * Requirements: T >= 1, T * k <= 2^27, M <= 2^30, E and k as dg_moe_route.
  * Deterministic.
@@ -627,13 +627,21 @@ int dg_moe_plan(int32_t *rows, int32_t *pairs, int32_t *m_indices, int64_t *offs
  * Rows that fill an expert's last 128 rows get codes and scales 0; 128-row
  * blocks without an expert are not written.  The gradient of x is dg_moe_combine
  * without weights.
+ *   workspace : optional (NULL or 0 bytes: none; the results are the same), of
+ *         dg_moe_dispatch_fp8_workspace_bytes(T, k, H, weights given) bytes,
+ *         16-byte aligned, any contents, clobbered: the scales meet there on
+ *         their way to sa, which saves a large call a fifth to a quarter of its time.  The
+ *         query returns 0 for calls that have no use for one.  Calls that may
+ *         run at the same time need distinct ones.
  * Requirements: T >= 1, 1 <= k <= DG_MOE_MAX_SLOTS, M >= 128, M % 128 == 0,
  * H >= 128, H % 128 == 0; T * ceil(H/512) <= 2^25, M * ceil(H/512) <= 2^29;
  * a 16-byte, the rest 4-byte aligned.  Deterministic.
  */
+size_t dg_moe_dispatch_fp8_workspace_bytes(int64_t T, int k, int64_t H, int weighted);
 int dg_moe_dispatch_fp8(uint8_t *a, float *sa, const void *x, int dtype, int64_t ldx,
                         const int32_t *rows, const int32_t *pairs, const float *weights,
-                        int64_t T, int k, int64_t M, int64_t H, void *stream);
+                        int64_t T, int k, int64_t M, int64_t H, void *workspace,
+                        size_t workspace_bytes, void *stream);
 
 /*
  * The experts' rows back to the tokens:
@@ -651,6 +659,7 @@ int dg_moe_dispatch_fp8(uint8_t *a, float *sa, const void *x, int dtype, int64_t
  *              of c, quantised for the next grouped product; or NULL.
  *   dweights : FP32 [T][k], dy[t] . c[rows[t][j]] in FP32, 0 for a slot without
  *              a row; or NULL (c is not needed then).
+ *   workspace : as for dg_moe_dispatch_fp8.
  * Requirements as dg_moe_dispatch_fp8.
  */
 int dg_moe_combine(uint16_t *y, const uint16_t *c, const int32_t *rows, const float *weights,
@@ -659,7 +668,8 @@ int dg_moe_combine(uint16_t *y, const uint16_t *c, const int32_t *rows, const fl
 int dg_moe_combine_backward(uint8_t *dc, float *sdc, float *dweights, const uint16_t *dy,
                             int64_t lddy, const uint16_t *c, const int32_t *rows,
                             const int32_t *pairs, const float *weights, int64_t T, int k,
-                            int64_t M, int64_t H, void *stream);
+                            int64_t M, int64_t H, void *workspace, size_t workspace_bytes,
+                            void *stream);
 
 /*
  * SwiGLU between two FP8 products, and the activation checkpoint in 8 bits.
