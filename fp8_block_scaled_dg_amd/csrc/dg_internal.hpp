@@ -175,7 +175,7 @@ struct RouteArgs {
   float scale;
   int64_t T, ldl, ldd;
   int E, k;
-  int lanes;              // of a wave for each group (set by the launch)
+  int lanes, wide_lanes;  // for each group: of 16, of a wave (set by the launch)
 };
 hipError_t launch_route(RouteArgs p, hipStream_t stream);
 hipError_t launch_route_backward(const RouteArgs& p, hipStream_t stream);

@@ -18,7 +18,10 @@
 //                     sigmoid dl_j = scale g_j s_j (1 - s_j)
 // The choice itself, and so the bias, has no gradient.
 //
-// One wave per token, PER consecutive experts a lane.
+// Up to 256 experts: 16 lanes per token, four tokens a wave, all in FP32 with
+// bounds on its errors; a token whose choice these bounds leave open is done
+// again by the whole wave in 64 bits (route_exact).  More experts: one wave per
+// token in 64 bits.
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
 
@@ -30,6 +33,10 @@ constexpr int kRouteWaves = 4;
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
 }
 template <int CTRL>
 __device__ __forceinline__ double dpp(double v) {
@@ -67,35 +74,34 @@ __device__ __forceinline__ T wave_sum(T v) {
   return wave_join(v, [](T a, T b) { return a + b; });
 }
 
-// Experts lane * PER .. + PER - 1 of a token's logits as FP32, -inf where there
-// is none; a row starts at any element.
+// PER logits from element `at` on as FP32, -inf from the count-th on (count may be
+// negative); they start at any element.
 template <int PER>
-__device__ __forceinline__ void load_logits(const void* logits, bool bf16, int64_t at, int E,
-                                            int lane, float (&v)[PER]) {
-  const int e0 = lane * PER;
+__device__ __forceinline__ void load_logits(const void* logits, bool bf16, int64_t at, int count,
+                                            float (&v)[PER]) {
 #pragma unroll
   for (int q = 0; q < PER; ++q) v[q] = -INFINITY;
-  if (e0 >= E) return;
+  if (count <= 0) return;
   if (bf16) {
-    const uint16_t* s = static_cast<const uint16_t*>(logits) + at + e0;
+    const uint16_t* s = static_cast<const uint16_t*>(logits) + at;
     uint16_t u[PER];
-    if (e0 + PER <= E) {
+    if (count >= PER) {
       __builtin_memcpy(u, __builtin_assume_aligned(s, 2), sizeof u);
 #pragma unroll
       for (int q = 0; q < PER; ++q) v[q] = bf16_bits_to_f32(u[q]);
     } else {
 #pragma unroll
       for (int q = 0; q < PER; ++q)
-        if (e0 + q < E) v[q] = bf16_bits_to_f32(s[q]);
+        if (q < count) v[q] = bf16_bits_to_f32(s[q]);
     }
   } else {
-    const float* s = static_cast<const float*>(logits) + at + e0;
-    if (e0 + PER <= E) {
+    const float* s = static_cast<const float*>(logits) + at;
+    if (count >= PER) {
       __builtin_memcpy(v, __builtin_assume_aligned(s, 4), sizeof v);
     } else {
 #pragma unroll
       for (int q = 0; q < PER; ++q)
-        if (e0 + q < E) v[q] = s[q];
+        if (q < count) v[q] = s[q];
     }
   }
 }
@@ -137,16 +143,13 @@ __device__ __forceinline__ void wide_scores(const float (&v)[PER], float m, int 
   }
 }
 
+// One wave, token t, PER consecutive experts a lane; value: room for 64 * PER
+// numbers of this wave (GROUPED).
 template <int PER, bool BIASED, bool GROUPED>
-__global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
+__device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t, int lane, double* value) {
   using Key = std::conditional_t<BIASED, double, float>;
-  __shared__ double s_value[GROUPED ? kRouteWaves : 1][GROUPED ? 64 * PER : 1];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (t >= p.T) return;
   float v[PER];
-  load_logits<PER>(p.logits, p.bf16, t * p.ldl, p.E, lane, v);
+  load_logits<PER>(p.logits, p.bf16, t * p.ldl + lane * PER, p.E - lane * PER, v);
   float m = -INFINITY;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
@@ -170,18 +173,17 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
     }
   }
   if constexpr (GROUPED) {
-    double* value = s_value[wave];
 #pragma unroll
     for (int q = 0; q < PER; ++q)
       value[lane * PER + q] = BIASED || p.best == 1 || key[q] == (Key)-INFINITY ? (double)key[q] : c[q];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    // p.lanes (a power of two) lanes a group
-    const int per = p.E / p.groups, g = lane / p.lanes;
+    // p.wide_lanes (a power of two) lanes a group
+    const int lanes = p.wide_lanes, per = p.E / p.groups, g = lane / lanes;
     double a = -INFINITY, b = -INFINITY;  // the two largest, a >= b
     if (g < p.groups)
-      for (int i = lane % p.lanes; i < per; i += p.lanes) {
+      for (int i = lane % lanes; i < per; i += lanes) {
         const double x = value[g * per + i];
         if (x > a) {
           b = a;
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
           b = x;
         }
       }
-    for (int d = 1; d < p.lanes; d *= 2) {
+    for (int d = 1; d < lanes; d *= 2) {
       const double oa = __shfl_xor(a, d, 64), ob = __shfl_xor(b, d, 64);
       const double lo = oa > a ? a : oa;  // of the two largest the smaller
       a = oa > a ? oa : a;
@@ -201,14 +203,14 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
     // groups ahead of this one: larger, or equal and before it
     int ahead = 0;
     for (int i = 0; i < p.groups; ++i) {
-      const double o = lane_of(a, i * p.lanes);
+      const double o = lane_of(a, i * lanes);
       ahead += o > a || (o == a && i < g);
     }
     const uint64_t stays = __ballot(g < p.groups && ahead < p.top_groups);
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int e = lane * PER + q;
-      if (e < p.E && !(stays >> (e / per * p.lanes) & 1)) key[q] = (Key)-INFINITY;
+      if (e < p.E && !(stays >> (e / per * lanes) & 1)) key[q] = (Key)-INFINITY;
     }
   }
   int my_id = -1;
@@ -252,64 +254,307 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
   }
 }
 
-template <int PER>
-__global__ void __launch_bounds__(64 * kRouteWaves) route_backward_kernel(RouteArgs p) {
-  const int lane = threadIdx.x & 63;
+template <int PER, bool BIASED, bool GROUPED>
+__global__ void __launch_bounds__(64 * kRouteWaves) route_wide_kernel(RouteArgs p) {
+  __shared__ double s_value[GROUPED ? kRouteWaves : 1][GROUPED ? 64 * PER : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (t >= p.T) return;
-  float v[PER];
-  load_logits<PER>(p.logits, p.bf16, t * p.ldl, p.E, lane, v);
+  if (t < p.T) route_exact<PER, BIASED, GROUPED>(p, t, threadIdx.x & 63, s_value[GROUPED ? wave : 0]);
+}
+
+// ---- 16 lanes per token ----
+
+// f over 16 neighbouring lanes, in each of them; like every move across lanes,
+// outside of branches that lanes of a row take differently.
+template <class T, class F>
+__device__ __forceinline__ T row_join(T v, F&& f) {
+  v = f(v, dpp<0xB1>(v));
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  v = f(v, dpp<0x140>(v));
+  return v;
+}
+__device__ __forceinline__ float larger(float a, float b) {  // no NaN; one instruction
+  return __builtin_amdgcn_fmed3f(a, b, __builtin_inff());
+}
+__device__ __forceinline__ float row_top(float v) { return row_join(v, larger); }
+__device__ __forceinline__ float row_low(float v) { return -row_top(-v); }
+__device__ __forceinline__ float row_sum(float v) {
+  return row_join(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ uint32_t row_top(uint32_t v) {
+  return row_join(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+
+// FP32 as an unsigned number of the same order, and back (no NaN, no -0).
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u >> 31 ? u ^ 0x80000000u : ~u);
+}
+
+// A token's choice by unsigned keys, value above index, so that one maximum
+// gives both and equal values go to the lowest index.  Value 0: cannot be chosen.
+//   BF16 logits without a bias: the 16 bits of the logit in their order, exact.
+//   else: 24 bits, the place of the choice value c on a grid of kSteps steps over
+//   the kWindow below the largest c (what is further below gets 0 as well).
+// The value is off from c's place by at most eps kSteps + 3 steps for an error eps
+// of c: the difference to the window's end is rounded by a step, its product with the
+// step by one, and the fraction is cut.  eps of the sigmoid, from v_exp_f32, v_rcp_f32 (one ulp
+// each) and the roundings of the argument, of 1 + e and of the product, is below
+// 2^-21 (s (1 - s) |l| <= 0.23 times 1.5 2^-22, s (1 - s) / 4 of 2^-23, s of 3 2^-24).  Of
+// the softmax: s times 2^-18 (|l - m| 2^-22 in the numerator, at most ln E <= 6 of
+// it weighted in the sum, 20 additions), s at most 1 / sum.  The sum with the bias
+// adds |c| 2^-24.  Two keys whose values differ by more than twice that are in c's
+// order; closer ones, and tokens that have to look below the window, are left to
+// route_exact, unless logit and bias are equal.  With 256 sigmoid scores and a
+// bias that is one token in two thousand.
+template <bool BIASED>
+struct Grid {
+  static constexpr float window = BIASED ? 2.0f : 16.0f, steps = 16000000.0f / window;
+};
+constexpr uint32_t kIndexBits = 8;
+
+template <int PER, bool BIASED, bool GROUPED>
+__global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
+  __shared__ double s_value[GROUPED ? kRouteWaves : 1][GROUPED ? 256 : 1];
+  const int lane = threadIdx.x & 63, lane16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * 4;
+  if (t0 >= p.T) return;
+  const int64_t t = t0 + (lane >> 4) < p.T ? t0 + (lane >> 4) : p.T - 1;
+  // p.lanes lanes a group (16: no groups), PER consecutive experts of it each
+  const int per = GROUPED ? p.E / p.groups : p.E, group = GROUPED ? lane16 / p.lanes : 0;
+  const int sub = (GROUPED ? lane16 % p.lanes : lane16) * PER, base = group * per + sub;
+  const int count = GROUPED && group >= p.groups ? 0 : per - sub;
+  float v[PER], c[PER];
+  load_logits<PER>(p.logits, p.bf16, t * p.ldl + base, count, v);
+  if constexpr (BIASED) load_logits<PER>(p.bias, false, base, count, c);
+  const bool pairs = GROUPED && p.best == 2;
+  const bool exact = !BIASED && p.bf16, softmax = p.scoring == ROUTE_SOFTMAX;
+  float m = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < PER; ++q)
-    if (v[q] != v[q]) v[q] = -INFINITY;
+  for (int q = 0; q < PER; ++q) {
+    if (softmax && v[q] != v[q]) v[q] = -INFINITY;
+    m = larger(m, v[q]);  // with a NaN: m
+  }
+  m = row_top(m);
+  bool open = m == INFINITY;  // left to route_exact
+  if (m == -INFINITY) m = 0.0f;
+  // scores (what cannot be chosen: NaN), also where the weights need their sum
+  float inverse = 1.0f, eps = 0x1p-21f;
+  if (BIASED || pairs || (!p.renormalise && softmax)) {
+    float e[PER];
+    if (softmax) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        e[q] = __builtin_amdgcn_exp2f((v[q] - m) * 1.44269504f);
+        sum += e[q];
+      }
+      inverse = 1.0f / row_sum(sum);
+      eps = inverse * 0x1p-18f;
+#pragma unroll
+      for (int q = 0; q < PER; ++q) e[q] *= inverse;
+    } else {
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        e[q] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v[q] * -1.44269504f));
+    }
+#pragma unroll
+    for (int q = 0; q < PER; ++q)  // v 0 is NaN for a v of -inf
+      c[q] = BIASED ? __builtin_fmaf(v[q], 0.0f, e[q] + c[q]) : __builtin_fmaf(v[q], 0.0f, e[q]);
+  }
+  uint32_t key[PER], near = 0;  // values within `near` of each other are not told apart
+  if (exact) {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const uint32_t u = ordered(v[q] + 0.0f) & 0xFFFF0000u;  // -0 is 0
+      key[q] = v[q] > -INFINITY ? u | (uint32_t)(0xFFFF - base - q) : 0;
+    }
+  } else {
+    using G = Grid<BIASED>;
+    float hi = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) hi = larger(hi, BIASED ? c[q] : v[q]);  // NaN: the other
+    hi = row_top(hi);
+    const float lo = hi - G::window;
+    open = open || (hi > -INFINITY && !(fabsf(hi) < 65536.0f));
+    near = 8 + (BIASED ? (uint32_t)(2.0f * G::steps * (fminf(eps, 1.0f) + (fminf(fabsf(hi), 65536.0f) + 2.0f) * 0x1p-24f)) : 0);
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const float x = BIASED ? c[q] : v[q];
+      const uint32_t value = (uint32_t)__builtin_amdgcn_fmed3f((x - lo) * G::steps, 0.0f, 16777215.0f);
+      key[q] = (value << kIndexBits) + (uint32_t)(255 - base - q);
+    }
+  }
+  const uint32_t shift = exact ? 16 : kIndexBits;
+  if constexpr (GROUPED) {
+    // a group's value, as an unsigned number: the largest key, or the sum of the
+    // two largest scores in FP32 (off by the two errors and one rounding)
+    uint32_t value = 0;
+    float off = 0.0f;
+    if (pairs) {
+      float a = -INFINITY, b = -INFINITY;  // a >= b
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        b = __builtin_amdgcn_fmed3f(a, b, c[q]);  // with a NaN the least of the others: b
+        a = larger(a, c[q]);
+      }
+      const auto meet = [&](float oa, float ob) {
+        b = larger(__builtin_amdgcn_fmed3f(a, b, oa), ob);  // the second of the two firsts, or a second
+        a = larger(a, oa);
+      };
+      if (p.lanes >= 2) meet(dpp<0xB1>(a), dpp<0xB1>(b));
+      if (p.lanes >= 4) meet(dpp<0x4E>(a), dpp<0x4E>(b));
+      if (p.lanes >= 8) meet(dpp<0x141>(a), dpp<0x141>(b));
+      if (!(b > -INFINITY)) b = 0.0f;
+      if (a > -INFINITY) value = ordered(a + b + 0.0f);
+      // two sums of two scores with their bias, each sum rounded
+      const float size = row_top(a > -INFINITY ? larger(fabsf(a), fabsf(b)) : 0.0f);
+      off = 4.0f * eps + size * (BIASED ? 8 * 0x1p-24f : 4 * 0x1p-24f);
+    } else {
+#pragma unroll
+      for (int q = 0; q < PER; ++q) value = max(value, key[q]);
+      if (p.lanes >= 2) value = max(value, dpp<0xB1>(value));
+      if (p.lanes >= 4) value = max(value, dpp<0x4E>(value));
+      if (p.lanes >= 8) value = max(value, dpp<0x141>(value));
+    }
+    int ahead = 0;  // of the other groups, by rotating the 16 lanes
+    static_for<15>([&](auto R) {
+      constexpr int r = decltype(R)::value + 1;
+      if ((r & (p.lanes - 1)) == 0) ahead += dpp<0x120 + r>(value) > value;
+    });
+    const bool stays = ahead < p.top_groups;
+    // the smallest that stays against the largest that does not
+    const uint32_t in = ~row_top(stays ? ~value : 0u), out = row_top(stays ? 0u : value);
+    if (out > 0) {
+      if (pairs) {
+        open = open || !(from_ordered(in) - from_ordered(out) > off);
+      } else {
+        open = open || (!exact && (in >> shift) - (out >> shift) <= near);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < PER; ++q) key[q] = stays ? key[q] : 0;
+  }
+  // k rounds of the largest key below the last one: key - last wraps round to
+  // the top of the range for these and stays below them for keys taken before
+  uint32_t mine = 0, after = 0, last = 0;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) last = max(last, key[q]);
+  last = row_top(last);
+  for (int j = 0; j < p.k; ++j) {
+    if (lane16 == j) mine = last;
+    uint32_t d = 0u - last;  // no key: 0
+#pragma unroll
+    for (int q = 0; q < PER; ++q) d = max(d, key[q] - last);
+    const uint32_t next = last + row_top(d);
+    last = last > 0 ? next : 0;
+    if (lane16 == j) after = last;
+  }
+  const int id = mine >> shift == 0 ? -1 : (int)((exact ? 0xFFFFu : 255u) - (mine & ((1u << shift) - 1)));
+  const float l = id >= 0 ? load_logit(p, t * p.ldl + id) : -INFINITY;
+  if (!exact) {
+    // equal logits and biases are in order, but not at the end of the choice,
+    // where others may be near as well
+    const float b = BIASED && id >= 0 ? p.bias[id] : 0.0f;
+    const float l1 = dpp<0x101>(l), b1 = dpp<0x101>(b);  // the next slot's
+    const bool same = lane16 + 1 < p.k && l1 == l && b1 == b;
+    open = open || (lane16 < p.k && (id < 0 || ((mine >> shift) - (after >> shift) <= near && !same)));
+  }
+  const uint64_t left = __ballot(open && t0 + (lane >> 4) < p.T);
+  float w = 0.0f;
+  if (p.renormalise) {
+    const float top = row_top(l);
+    const float r = id >= 0 ? relative_score(l, top, p.scoring) : 0.0f;
+    w = p.scale * r / row_sum(r);
+  } else if (p.scoring == ROUTE_SOFTMAX) {
+    w = p.scale * expf(l - m) * inverse;
+  } else {
+    w = p.scale * sigmoid(l);
+  }
+  if (lane16 < p.k && t0 + (lane >> 4) < p.T && !(left >> (lane & 48) & 0xFFFF)) {
+    p.ids[t * p.k + lane16] = id;
+    p.weights[t * p.k + lane16] = id >= 0 ? w : 0.0f;
+  }
+  if (left == 0) return;
+  for (int r = 0; r < 4; ++r)
+    if (left >> (16 * r) & 0xFFFF)
+      route_exact<4, BIASED, GROUPED>(p, t0 + r, lane, s_value[GROUPED ? wave : 0]);
+}
+
+// The gradient: LANES lanes a token (16 or 64), PER consecutive experts each.
+template <int LANES, int PER>
+__global__ void __launch_bounds__(64 * kRouteWaves) route_backward_kernel(RouteArgs p) {
+  constexpr int TOKENS = 64 / LANES;
+  const int lane = threadIdx.x & 63, at = lane & (LANES - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * TOKENS;
+  if (t0 >= p.T) return;
+  const bool real = t0 + lane / LANES < p.T;
+  const int64_t t = real ? t0 + lane / LANES : p.T - 1;
+  const auto top_of = [](float x) { return LANES == 16 ? row_top(x) : wave_top(x); };
+  const auto sum_of = [](float x) { return LANES == 16 ? row_sum(x) : wave_sum(x); };
   // lane j has slot j; a slot without an expert, or one of an expert that
   // cannot be chosen, gives and gets nothing
-  int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
+  int id = at < p.k ? p.ids[t * p.k + at] : -1;
   if (id >= p.E) id = -1;
   float l = id >= 0 ? load_logit(p, t * p.ldl + id) : -INFINITY;
   if (!(l > -INFINITY)) id = -1, l = -INFINITY;
-  const float g = id >= 0 ? p.scale * p.dweights[t * p.k + lane] : 0.0f;
-  // slot: what is added to the logit of the slot's expert; all: what is
-  // subtracted from every logit, times its score
-  float slot = 0.0f, all = 0.0f, m = 0.0f, inverse = 0.0f;
+  const float g = id >= 0 ? p.scale * p.dweights[t * p.k + at] : 0.0f;
+  // slot: what is added to the logit of the slot's expert
+  float slot = 0.0f, d[PER];
+#pragma unroll
+  for (int q = 0; q < PER; ++q) d[q] = 0.0f;
   if (p.renormalise) {
-    const float top = wave_top(l);
+    const float top = top_of(l);
     const float r = id >= 0 ? relative_score(l, top, p.scoring) : 0.0f;
-    const float sum = wave_sum(r);
+    const float sum = sum_of(r);
     const float q = sum > 0.0f ? r / sum : 0.0f;
-    slot = q * (g - wave_sum(g * q));
+    slot = q * (g - sum_of(g * q));
     if (p.scoring == ROUTE_SIGMOID) slot *= sigmoid(-l);
   } else if (p.scoring == ROUTE_SOFTMAX) {
-    m = -INFINITY;
+    // every logit: minus the sum of the slots' parts times its score
+    float v[PER], m = -INFINITY, sum = 0.0f;
+    load_logits<PER>(p.logits, p.bf16, t * p.ldl + at * PER, p.E - at * PER, v);
 #pragma unroll
-    for (int q = 0; q < PER; ++q) m = fmaxf(m, v[q]);
-    m = wave_top(m);
-    float sum = 0.0f;
-    if (m > -INFINITY) {
-#pragma unroll
-      for (int q = 0; q < PER; ++q) sum += expf(v[q] - m);
+    for (int q = 0; q < PER; ++q) {
+      if (v[q] != v[q]) v[q] = -INFINITY;
+      m = larger(m, v[q]);
     }
-    sum = wave_sum(sum);
-    inverse = sum > 0.0f ? 1.0f / sum : 0.0f;
-    slot = id >= 0 ? g * expf(l - m) * inverse : 0.0f;
-    all = wave_sum(slot);
+    m = top_of(m);
+    if (!(m > -INFINITY)) m = 0.0f;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      d[q] = __builtin_amdgcn_exp2f((v[q] - m) * 1.44269504f);
+      sum += d[q];
+    }
+    sum = sum_of(sum);
+    const float inverse = sum > 0.0f ? 1.0f / sum : 0.0f;
+    slot = id >= 0 ? g * (expf(l - m) * inverse) : 0.0f;
+    const float all = -sum_of(slot) * inverse;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) d[q] *= all;
   } else {
     slot = g * sigmoid(l) * sigmoid(-l);
   }
   if (id < 0) slot = 0.0f;
-  float d[PER];
+  const int e0 = at * PER;
+  const auto add = [&](int e, float s) {
 #pragma unroll
-  for (int q = 0; q < PER; ++q) d[q] = all != 0.0f && v[q] > -INFINITY ? -all * (expf(v[q] - m) * inverse) : 0.0f;
-  for (int j = 0; j < p.k; ++j) {
-    const int e = __builtin_amdgcn_readlane(id, j);
-    const float s = lane_of(slot, j);
-#pragma unroll
-    for (int q = 0; q < PER; ++q)
-      if (e == lane * PER + q) d[q] += s;
-  }
-  const int e0 = lane * PER;
-  if (e0 >= p.E) return;
+    for (int q = 0; q < PER; ++q) d[q] += e - e0 == q ? s : 0.0f;
+  };
+  static_while<kMoeMaxSlots>([&](auto J) {
+    constexpr int j = decltype(J)::value;
+    if (j >= p.k) return false;
+    if constexpr (LANES == 16) add((int)dpp<0x150 + j>((uint32_t)id), dpp<0x150 + j>(slot));
+    else add(__builtin_amdgcn_readlane(id, j), lane_of(slot, j));
+    return true;
+  });
+  if (!real || e0 >= p.E) return;
   if (p.bf16) {
     uint16_t* o = static_cast<uint16_t*>(p.dlogits) + t * p.ldd + e0;
     uint16_t u[PER];
@@ -334,39 +579,60 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_backward_kernel(RouteA
   }
 }
 
-template <int PER>
-void launch_per(const RouteArgs& p, bool backward, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
-  if (backward) {
-    hipLaunchKernelGGL(route_backward_kernel<PER>, grid, block, 0, stream, p);
-  } else if (p.top_groups < p.groups) {
-    if (p.bias) hipLaunchKernelGGL((route_kernel<PER, true, true>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((route_kernel<PER, false, true>), grid, block, 0, stream, p);
-  } else {
-    if (p.bias) hipLaunchKernelGGL((route_kernel<PER, true, false>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((route_kernel<PER, false, false>), grid, block, 0, stream, p);
-  }
+template <int PER, bool WIDE>
+void launch_forward(const RouteArgs& p, hipStream_t stream) {
+  const int64_t tokens = kRouteWaves * (WIDE ? 1 : 4);  // a workgroup
+  const dim3 grid((unsigned)((p.T + tokens - 1) / tokens)), block(64 * kRouteWaves);
+  const auto go = [&](auto biased, auto grouped) {
+    constexpr bool B = decltype(biased)::value, G = decltype(grouped)::value;
+    if constexpr (WIDE) hipLaunchKernelGGL((route_wide_kernel<PER, B, G>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((route_kernel<PER, B, G>), grid, block, 0, stream, p);
+  };
+  if (p.top_groups < p.groups) p.bias ? go(IntTag<1>{}, IntTag<1>{}) : go(IntTag<0>{}, IntTag<1>{});
+  else p.bias ? go(IntTag<1>{}, IntTag<0>{}) : go(IntTag<0>{}, IntTag<0>{});
 }
 
-hipError_t launch_any(const RouteArgs& p, bool backward, hipStream_t stream) {
-  if (p.E <= 64) launch_per<1>(p, backward, stream);
-  else if (p.E <= 128) launch_per<2>(p, backward, stream);
-  else if (p.E <= 256) launch_per<4>(p, backward, stream);
-  else if (p.E <= 512) launch_per<8>(p, backward, stream);
-  else launch_per<16>(p, backward, stream);
-  return hipGetLastError();
+template <int LANES, int PER>
+void launch_backward(const RouteArgs& p, hipStream_t stream) {
+  constexpr int64_t tokens = kRouteWaves * 64 / LANES;
+  hipLaunchKernelGGL((route_backward_kernel<LANES, PER>), dim3((unsigned)((p.T + tokens - 1) / tokens)),
+                     dim3(64 * kRouteWaves), 0, stream, p);
 }
 
 }  // namespace
 
 hipError_t launch_route(RouteArgs p, hipStream_t stream) {
-  p.lanes = 1;
-  while (2 * p.lanes * p.groups <= 64) p.lanes *= 2;
-  return launch_any(p, false, stream);
+  const bool grouped = p.top_groups < p.groups;
+  const auto lanes_of = [&](int lanes) {  // the power of two that gives every group as many
+    int n = 1;
+    while (2 * n * p.groups <= lanes) n *= 2;
+    return n;
+  };
+  p.wide_lanes = lanes_of(64);
+  p.lanes = grouped ? lanes_of(16) : 16;
+  // experts a lane, where 16 lanes take a token
+  const int per = grouped ? (p.E / p.groups + p.lanes - 1) / p.lanes : (p.E + 15) / 16;
+  if (p.E > 256 || per > 16 || (grouped && p.groups > 16)) {
+    if (p.E <= 256) launch_forward<4, true>(p, stream);
+    else if (p.E <= 512) launch_forward<8, true>(p, stream);
+    else launch_forward<16, true>(p, stream);
+  } else if (per <= 4) {
+    launch_forward<4, false>(p, stream);
+  } else if (per <= 8) {
+    launch_forward<8, false>(p, stream);
+  } else {
+    launch_forward<16, false>(p, stream);
+  }
+  return hipGetLastError();
 }
 
 hipError_t launch_route_backward(const RouteArgs& p, hipStream_t stream) {
-  return launch_any(p, true, stream);
+  if (p.E <= 64) launch_backward<16, 4>(p, stream);
+  else if (p.E <= 128) launch_backward<16, 8>(p, stream);
+  else if (p.E <= 256) launch_backward<16, 16>(p, stream);
+  else if (p.E <= 512) launch_backward<64, 8>(p, stream);
+  else launch_backward<64, 16>(p, stream);
+  return hipGetLastError();
 }
 
 }  // namespace dg
