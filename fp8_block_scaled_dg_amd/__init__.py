@@ -782,16 +782,19 @@ def dg_moe_layer(y, x, w13, w2, s13, s2, ids, weights, logits=None, scoring: str
 # Around the grouped products: routing, layout, dispatch, combine, SwiGLU
 # ---------------------------------------------------------------------------
 
+# A launch takes less time than the checks of its tensors one by one, so each
+# call first looks at all of them in one expression; only where that fails do
+# the _refuse_ functions look again, for the reason to raise.
+
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_device_now = torch._C._cuda_getDevice
+_stream_now = torch._C._cuda_getCurrentRawStream
 
 
 def _need(t, dtypes, shape, device, name):
-    """t is a contiguous tensor of one of dtypes, of this shape (None: any)
-    on device number `device`.  One test where it is; the reason where not."""
-    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == device >= 0
-            and (shape is None or t.shape == shape) and t.is_contiguous()):
-        return
+    """t is a contiguous tensor of one of dtypes, of this shape (None: any),
+    on device number `device`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype not in dtypes:
@@ -799,7 +802,8 @@ def _need(t, dtypes, shape, device, name):
     _require(t, t.dtype, name)
     if shape is not None and t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    raise ValueError("%s is on device %d, other tensors on %d" % (name, t.get_device(), device))
+    if t.get_device() != device:
+        raise ValueError("%s is on device %d, other tensors on %d" % (name, t.get_device(), device))
 
 
 def _need_fp8(q, s, rows, cols, device, name):
@@ -808,38 +812,50 @@ def _need_fp8(q, s, rows, cols, device, name):
     _need(s, (_F32,), ((cols + 127) // 128, rows), device, "scales of " + name)
 
 
+def _is_fp8(q, s, rows, cols, device):
+    return (q.dtype in _CODES and q.shape == (rows, cols) and q.get_device() == device
+            and q.is_contiguous() and s.dtype is _F32 and s.shape == ((cols + 127) // 128, rows)
+            and s.get_device() == device and s.is_contiguous())
+
+
 def _need_rows(x, dtypes, name):
     """(rows, columns, row stride, device number) of a device matrix with
     contiguous rows of any stride."""
     if not isinstance(x, torch.Tensor) or x.dtype not in dtypes:
         raise TypeError("%s must be a tensor of %s" % (name, " or ".join(map(str, dtypes))))
-    if not x.is_cuda:
-        raise ValueError("%s must be a device tensor" % name)
     if x.dim() != 2:
         raise ValueError("%s must be a matrix" % name)
-    rows, cols = x.shape
-    ld, one = x.stride()
+    if not x.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    (rows, cols), (ld, one) = x.shape, x.stride()
     if cols > 1 and one != 1 or rows > 1 and ld < cols:
         raise ValueError("the rows of %s must be contiguous and must not overlap" % name)
     return rows, cols, ld if rows > 1 else cols, x.get_device()
 
 
-def _launch_stream(stream, device):
-    """The stream of a launch, which goes to the current device: the tensors
-    have to be there."""
-    current = torch._C._cuda_getDevice()
-    if device != current:
-        raise ValueError("the tensors are on device %d, the current one is %d" % (device, current))
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream
-
-
-def _two(t, name):
-    """(rows, columns) of a matrix whose type and place are looked at later."""
+def _need_matrix(t, name):
+    """The shape of a matrix whose type and place are looked at elsewhere."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dim() != 2:
         raise ValueError("%s must be a matrix" % name)
     return t.shape
+
+
+def _launch_stream(stream, device):
+    """The stream of a launch, which goes to the current device: the tensors
+    have to be there."""
+    if device != _device_now():
+        raise ValueError("the tensors are on device %d, the current one is %d"
+                         % (device, _device_now()))
+    return _stream_now(device) if stream is None else stream
+
+
+def _refuse_slots(ids, weights, T, dev, name):
+    k = _need_matrix(ids, name)[1]
+    _need(ids, (_I32,), (T, k), dev, name)
+    if weights is not None:
+        _need(weights, (_F32,), (T, k), dev, "weights")
 
 
 def dg_moe_route(ids, weights, logits, bias=None, scoring: str = "softmax", groups: int = 1,
@@ -851,16 +867,27 @@ def dg_moe_route(ids, weights, logits, bias=None, scoring: str = "softmax", grou
     of `groups` groups of experts the top_groups (default: all) with the
     largest sums of their group_best largest choice values stay."""
     T, E, ld, dev = _need_rows(logits, _DTYPES, "logits")
-    k = _two(ids, "ids")[1]
-    _need(ids, (_I32,), (T, k), dev, "ids")
-    _need(weights, (_F32,), (T, k), dev, "weights")
-    if bias is not None:
+    try:
+        shape = ids.shape
+        k = shape[1]
+        ok = (shape[0] == T and weights.shape == shape and ids.dtype is _I32
+              and weights.dtype is _F32 and ids.get_device() == dev == weights.get_device()
+              and len(shape) == 2 and ids.is_contiguous() and weights.is_contiguous()
+              and (bias is None or bias.dtype is _F32 and bias.shape == (E,)
+                   and bias.get_device() == dev and bias.is_contiguous()))
+    except (AttributeError, IndexError):
+        ok = False
+    if not ok:
+        _refuse_slots(ids, None, T, dev, "ids")
+        _need(weights, (_F32,), ids.shape, dev, "weights")
         _need(bias, (_F32,), (E,), dev, "bias")
-    _check(lib.dg_moe_route(ids.data_ptr(), weights.data_ptr(), logits.data_ptr(),
-                            _DTYPES[logits.dtype], ld, _ptr(bias), MOE_SCORINGS[scoring], groups,
-                            groups if top_groups is None else top_groups, group_best,
-                            bool(renormalise), scale, T, E, k, _launch_stream(stream, dev)),
-           "dg_moe_route")
+    rc = lib.dg_moe_route(ids.data_ptr(), weights.data_ptr(), logits.data_ptr(),
+                          _DTYPES[logits.dtype], ld, None if bias is None else bias.data_ptr(),
+                          MOE_SCORINGS[scoring], groups,
+                          groups if top_groups is None else top_groups, group_best,
+                          bool(renormalise), scale, T, E, k, _launch_stream(stream, dev))
+    if rc:
+        raise DGError(rc, "dg_moe_route")
 
 
 def dg_moe_route_backward(dlogits, dweights, ids, logits, scoring: str = "softmax",
@@ -871,13 +898,23 @@ def dg_moe_route_backward(dlogits, dweights, ids, logits, scoring: str = "softma
     rows, cols, ldd, where = _need_rows(dlogits, (logits.dtype,), "dlogits")
     if (rows, cols, where) != (T, E, dev):
         raise ValueError("dlogits must be [T, E] on the device of logits")
-    k = _two(ids, "ids")[1]
-    _need(ids, (_I32,), (T, k), dev, "ids")
-    _need(dweights, (_F32,), (T, k), dev, "dweights")
-    _check(lib.dg_moe_route_backward(dlogits.data_ptr(), ldd, dweights.data_ptr(), ids.data_ptr(),
-                                     logits.data_ptr(), _DTYPES[logits.dtype], ld,
-                                     MOE_SCORINGS[scoring], bool(renormalise), scale, T, E, k,
-                                     _launch_stream(stream, dev)), "dg_moe_route_backward")
+    try:
+        shape = ids.shape
+        k = shape[1]
+        ok = (shape[0] == T and dweights.shape == shape and ids.dtype is _I32
+              and dweights.dtype is _F32 and ids.get_device() == dev == dweights.get_device()
+              and len(shape) == 2 and ids.is_contiguous() and dweights.is_contiguous())
+    except (AttributeError, IndexError):
+        ok = False
+    if not ok:
+        _refuse_slots(ids, None, T, dev, "ids")
+        _need(dweights, (_F32,), ids.shape, dev, "dweights")
+    rc = lib.dg_moe_route_backward(dlogits.data_ptr(), ldd, dweights.data_ptr(), ids.data_ptr(),
+                                   logits.data_ptr(), _DTYPES[logits.dtype], ld,
+                                   MOE_SCORINGS[scoring], bool(renormalise), scale, T, E, k,
+                                   _launch_stream(stream, dev))
+    if rc:
+        raise DGError(rc, "dg_moe_route_backward")
 
 
 def dg_moe_plan_rows(T: int, E: int, k: int) -> int:
@@ -894,19 +931,33 @@ def dg_moe_plan(rows, pairs, m_indices, offsets, counts, ids, workspace=None, st
     offsets int64 [E + 1], counts int32 [E]; M a multiple of 128, at least
     dg_moe_plan_rows(T, E, k).  workspace: dg_moe_plan_workspace_bytes(T, E, k)
     bytes of any contents."""
-    T, k = shape = _two(ids, "ids")
-    dev = ids.get_device()
-    _need(ids, (_I32,), None, dev, "ids")
-    _need(rows, (_I32,), shape, dev, "rows")
-    _need(pairs, (_I32,), None, dev, "pairs")
-    _need(counts, (_I32,), None, dev, "counts")
-    M, E = pairs.numel(), counts.numel()
-    _need(m_indices, (_I32,), (M,), dev, "m_indices")
-    _need(offsets, (_I64,), (E + 1,), dev, "offsets")
-    _check(lib.dg_moe_plan(rows.data_ptr(), pairs.data_ptr(), m_indices.data_ptr(),
-                           offsets.data_ptr(), counts.data_ptr(), ids.data_ptr(), T, E, k, M,
-                           _ptr(workspace), _workspace_bytes(workspace),
-                           _launch_stream(stream, dev)), "dg_moe_plan")
+    try:
+        T, k = shape = ids.shape
+        dev, M, E = ids.get_device(), pairs.numel(), counts.numel()
+        ok = (ids.dtype is rows.dtype is pairs.dtype is m_indices.dtype is counts.dtype is _I32
+              and offsets.dtype is _I64 and rows.shape == shape and pairs.dim() == 1
+              and counts.dim() == 1 and m_indices.shape == (M,) and offsets.shape == (E + 1,)
+              and rows.get_device() == pairs.get_device() == m_indices.get_device()
+              == offsets.get_device() == counts.get_device() == dev >= 0
+              and ids.is_contiguous() and rows.is_contiguous() and pairs.is_contiguous()
+              and m_indices.is_contiguous() and offsets.is_contiguous() and counts.is_contiguous())
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        shape = _need_matrix(ids, "ids")
+        dev = ids.get_device()
+        for t, n in ((ids, "ids"), (pairs, "pairs"), (counts, "counts")):
+            _need(t, (_I32,), None, dev, n)
+        _need(rows, (_I32,), shape, dev, "rows")
+        _need(m_indices, (_I32,), (pairs.numel(),), dev, "m_indices")
+        _need(offsets, (_I64,), (counts.numel() + 1,), dev, "offsets")
+        raise ValueError("pairs and counts must have one dimension")
+    rc = lib.dg_moe_plan(rows.data_ptr(), pairs.data_ptr(), m_indices.data_ptr(),
+                         offsets.data_ptr(), counts.data_ptr(), ids.data_ptr(), T, E, k, M,
+                         None if workspace is None else workspace.data_ptr(),
+                         _workspace_bytes(workspace), _launch_stream(stream, dev))
+    if rc:
+        raise DGError(rc, "dg_moe_plan")
 
 
 def dg_moe_dispatch_fp8_workspace_bytes(T: int, k: int, H: int, weighted: bool = False) -> int:
@@ -917,10 +968,17 @@ def _dispatch_workspace(workspace, stream, T, k, H, weights, device):
     """The caller's workspace, else one from torch for a call that has use for
     it; torch's memory belongs to its current stream, so not where the call
     is sent to another one."""
-    if workspace is not None or stream is not None:
+    if workspace is not None or stream is not None or T * k * H < 1 << 26:  # as the library says
         return workspace
     n = lib.dg_moe_dispatch_fp8_workspace_bytes(T, k, H, weights is not None)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _are_slots(rows, weights, T, device):
+    return (rows.dtype is _I32 and len(rows.shape) == 2 and rows.shape[0] == T
+            and rows.get_device() == device and rows.is_contiguous()
+            and (weights is None or weights.dtype is _F32 and weights.shape == rows.shape
+                 and weights.get_device() == device and weights.is_contiguous()))
 
 
 def dg_moe_dispatch_fp8(a, sa, x, rows, pairs, weights=None, workspace=None, stream=None) -> None:
@@ -931,35 +989,53 @@ def dg_moe_dispatch_fp8(a, sa, x, rows, pairs, weights=None, workspace=None, str
     without one, and without a stream, a large call takes its own from
     torch."""
     T, H, ld, dev = _need_rows(x, _DTYPES, "x")
-    k = _two(rows, "rows")[1]
-    _need(rows, (_I32,), (T, k), dev, "rows")
-    _need(pairs, (_I32,), None, dev, "pairs")
-    M = pairs.numel()
-    if weights is not None:
-        _need(weights, (_F32,), (T, k), dev, "weights")
-    _need_fp8(a, sa, M, H, dev, "a")
+    try:
+        M = pairs.numel()
+        ok = (pairs.dtype is _I32 and pairs.get_device() == dev and pairs.is_contiguous()
+              and _are_slots(rows, weights, T, dev) and _is_fp8(a, sa, M, H, dev))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse_slots(rows, weights, T, dev, "rows")
+        _need(pairs, (_I32,), None, dev, "pairs")
+        _need_fp8(a, sa, pairs.numel(), H, dev, "a")
+    k = rows.shape[1]
     workspace = _dispatch_workspace(workspace, stream, T, k, H, weights, x.device)
-    _check(lib.dg_moe_dispatch_fp8(a.data_ptr(), sa.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], ld,
-                                   rows.data_ptr(), pairs.data_ptr(), _ptr(weights), T, k, M, H,
-                                   _ptr(workspace), _workspace_bytes(workspace),
-                                   _launch_stream(stream, dev)), "dg_moe_dispatch_fp8")
+    rc = lib.dg_moe_dispatch_fp8(a.data_ptr(), sa.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], ld,
+                                 rows.data_ptr(), pairs.data_ptr(),
+                                 None if weights is None else weights.data_ptr(), T, k, M, H,
+                                 None if workspace is None else workspace.data_ptr(),
+                                 _workspace_bytes(workspace), _launch_stream(stream, dev))
+    if rc:
+        raise DGError(rc, "dg_moe_dispatch_fp8")
 
 
 def dg_moe_combine(y, c, rows, weights=None, residual=None, stream=None) -> None:
     """y [T, H] (bf16) = sum over the slots of weights (float32 [T, k], or all
     1) times the rows of c [M, H] (bf16), plus residual [T, H] (bf16)."""
-    T, H = shape = _two(y, "y")
-    M, k, dev = _two(c, "c")[0], _two(rows, "rows")[1], y.get_device()
-    _need(y, _BF16_TYPES, None, dev, "y")
-    _need(c, _BF16_TYPES, (M, H), dev, "c")
-    _need(rows, (_I32,), (T, k), dev, "rows")
-    if weights is not None:
-        _need(weights, (_F32,), (T, k), dev, "weights")
-    if residual is not None:
+    try:
+        T, H = shape = y.shape
+        M, dev = c.shape[0], y.get_device()
+        ok = (y.dtype in _BF16_TYPES and c.dtype in _BF16_TYPES and c.shape == (M, H)
+              and c.get_device() == dev >= 0 and y.is_contiguous() and c.is_contiguous()
+              and _are_slots(rows, weights, T, dev)
+              and (residual is None or residual.dtype in _BF16_TYPES and residual.shape == shape
+                   and residual.get_device() == dev and residual.is_contiguous()))
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        shape, (M, _) = _need_matrix(y, "y"), _need_matrix(c, "c")
+        dev = y.get_device()
+        _need(y, _BF16_TYPES, None, dev, "y")
+        _need(c, _BF16_TYPES, (M, shape[1]), dev, "c")
+        _refuse_slots(rows, weights, shape[0], dev, "rows")
         _need(residual, _BF16_TYPES, shape, dev, "residual")
-    _check(lib.dg_moe_combine(y.data_ptr(), c.data_ptr(), rows.data_ptr(), _ptr(weights),
-                              _ptr(residual), T, k, M, H, _launch_stream(stream, dev)),
-           "dg_moe_combine")
+    rc = lib.dg_moe_combine(y.data_ptr(), c.data_ptr(), rows.data_ptr(),
+                            None if weights is None else weights.data_ptr(),
+                            None if residual is None else residual.data_ptr(), T, rows.shape[1], M,
+                            H, _launch_stream(stream, dev))
+    if rc:
+        raise DGError(rc, "dg_moe_combine")
 
 
 def dg_moe_combine_backward(dc, sdc, dweights, dy, c, rows, pairs, weights=None, workspace=None,
@@ -969,23 +1045,43 @@ def dg_moe_combine_backward(dc, sdc, dweights, dy, c, rows, pairs, weights=None,
     weights, and dweights float32 [T, k]; dc and sdc, or dweights, may be
     None.  workspace: as for dg_moe_dispatch_fp8."""
     T, H, ld, dev = _need_rows(dy, (torch.bfloat16,), "dy")
-    k = _two(rows, "rows")[1]
-    _need(rows, (_I32,), (T, k), dev, "rows")
-    _need(pairs, (_I32,), None, dev, "pairs")
-    M = pairs.numel()
-    if weights is not None:
-        _need(weights, (_F32,), (T, k), dev, "weights")
-    if dc is not None or sdc is not None:
-        _need_fp8(dc, sdc, M, H, dev, "dc")
-        workspace = _dispatch_workspace(workspace, stream, T, k, H, weights, dy.device)
-    if dweights is not None:
-        _need(dweights, (_F32,), (T, k), dev, "dweights")
+    try:
+        M = pairs.numel()
+        ok = (pairs.dtype is _I32 and pairs.get_device() == dev and pairs.is_contiguous()
+              and _are_slots(rows, weights, T, dev)
+              and (dc is None and sdc is None or _is_fp8(dc, sdc, M, H, dev))
+              and (dweights is None or _are_slots(rows, dweights, T, dev)
+                   and c.dtype in _BF16_TYPES and c.shape == (M, H) and c.get_device() == dev
+                   and c.is_contiguous()))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse_slots(rows, weights, T, dev, "rows")
+        _need(pairs, (_I32,), None, dev, "pairs")
+        M = pairs.numel()
+        if dc is not None or sdc is not None:
+            _need_fp8(dc, sdc, M, H, dev, "dc")
+        _need(dweights, (_F32,), rows.shape, dev, "dweights")
         _need(c, _BF16_TYPES, (M, H), dev, "c")
-    _check(lib.dg_moe_combine_backward(_ptr(dc), _ptr(sdc), _ptr(dweights), dy.data_ptr(), ld,
-                                       None if dweights is None else c.data_ptr(),
-                                       rows.data_ptr(), pairs.data_ptr(), _ptr(weights), T, k, M,
-                                       H, _ptr(workspace), _workspace_bytes(workspace),
-                                       _launch_stream(stream, dev)), "dg_moe_combine_backward")
+    k = rows.shape[1]
+    if dc is not None:
+        workspace = _dispatch_workspace(workspace, stream, T, k, H, weights, dy.device)
+    rc = lib.dg_moe_combine_backward(None if dc is None else dc.data_ptr(),
+                                     None if dc is None else sdc.data_ptr(),
+                                     None if dweights is None else dweights.data_ptr(),
+                                     dy.data_ptr(), ld, None if dweights is None else c.data_ptr(),
+                                     rows.data_ptr(), pairs.data_ptr(),
+                                     None if weights is None else weights.data_ptr(), T, k, M, H,
+                                     None if workspace is None else workspace.data_ptr(),
+                                     _workspace_bytes(workspace), _launch_stream(stream, dev))
+    if rc:
+        raise DGError(rc, "dg_moe_combine_backward")
+
+
+def _are_layout_rows(m_indices, M, device):
+    return m_indices is None or (m_indices.dtype is _I32 and m_indices.shape == (M,)
+                                 and m_indices.get_device() == device
+                                 and m_indices.is_contiguous())
 
 
 def dg_swiglu_fp8(h, sh, gu, kept=None, skept=None, m_indices=None, stream=None) -> None:
@@ -993,19 +1089,28 @@ def dg_swiglu_fp8(h, sh, gu, kept=None, skept=None, m_indices=None, stream=None)
     (bf16, column 2i gate, 2i+1 up), and kept (codes [M, 2I]), skept float32
     [2I/128, M] = gu itself in 8 bits for dg_swiglu_fp8_backward.  m_indices
     int32 [M]: the rows of the grouped layout that are real."""
-    M, two = _two(gu, "gu")
+    M, two = _need_matrix(gu, "gu")
     dev = gu.get_device()
-    _need(gu, _BF16_TYPES, None, dev, "gu")
-    if two % 2:
-        raise ValueError("gu must be [M, 2I]")
-    _need_fp8(h, sh, M, two // 2, dev, "h")
-    if kept is not None or skept is not None:
-        _need_fp8(kept, skept, M, two, dev, "kept")
-    if m_indices is not None:
+    try:
+        ok = (two % 2 == 0 and gu.dtype in _BF16_TYPES and dev >= 0 and gu.is_contiguous()
+              and _is_fp8(h, sh, M, two // 2, dev) and _are_layout_rows(m_indices, M, dev)
+              and (kept is None and skept is None or _is_fp8(kept, skept, M, two, dev)))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _need(gu, _BF16_TYPES, None, dev, "gu")
+        if two % 2:
+            raise ValueError("gu must be [M, 2I]")
+        _need_fp8(h, sh, M, two // 2, dev, "h")
+        if kept is not None or skept is not None:
+            _need_fp8(kept, skept, M, two, dev, "kept")
         _need(m_indices, (_I32,), (M,), dev, "m_indices")
-    _check(lib.dg_swiglu_fp8(h.data_ptr(), sh.data_ptr(), _ptr(kept), _ptr(skept), gu.data_ptr(),
-                             _ptr(m_indices), M, two // 2, _launch_stream(stream, dev)),
-           "dg_swiglu_fp8")
+    rc = lib.dg_swiglu_fp8(h.data_ptr(), sh.data_ptr(), None if kept is None else kept.data_ptr(),
+                           None if kept is None else skept.data_ptr(), gu.data_ptr(),
+                           None if m_indices is None else m_indices.data_ptr(), M, two // 2,
+                           _launch_stream(stream, dev))
+    if rc:
+        raise DGError(rc, "dg_swiglu_fp8")
 
 
 def dg_swiglu_fp8_backward(dgu, sdgu, dh, kept, skept, h=None, sh=None, m_indices=None,
@@ -1013,19 +1118,30 @@ def dg_swiglu_fp8_backward(dgu, sdgu, dh, kept, skept, h=None, sh=None, m_indice
     """dgu (codes [M, 2I]) and sdgu from dh [M, I] (bf16) and the checkpoint
     kept, skept; with h (codes [M, I]) and sh also silu(gate) * up of the
     checkpoint's values."""
-    M, I = _two(dh, "dh")
+    M, I = _need_matrix(dh, "dh")
     dev = dh.get_device()
-    _need(dh, _BF16_TYPES, None, dev, "dh")
-    _need_fp8(dgu, sdgu, M, 2 * I, dev, "dgu")
-    _need_fp8(kept, skept, M, 2 * I, dev, "kept")
-    if h is not None or sh is not None:
-        _need_fp8(h, sh, M, I, dev, "h")
-    if m_indices is not None:
+    try:
+        ok = (dh.dtype in _BF16_TYPES and dev >= 0 and dh.is_contiguous()
+              and _is_fp8(dgu, sdgu, M, 2 * I, dev) and _is_fp8(kept, skept, M, 2 * I, dev)
+              and (h is None and sh is None or _is_fp8(h, sh, M, I, dev))
+              and _are_layout_rows(m_indices, M, dev))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _need(dh, _BF16_TYPES, None, dev, "dh")
+        _need_fp8(dgu, sdgu, M, 2 * I, dev, "dgu")
+        _need_fp8(kept, skept, M, 2 * I, dev, "kept")
+        if h is not None or sh is not None:
+            _need_fp8(h, sh, M, I, dev, "h")
         _need(m_indices, (_I32,), (M,), dev, "m_indices")
-    _check(lib.dg_swiglu_fp8_backward(dgu.data_ptr(), sdgu.data_ptr(), _ptr(h), _ptr(sh),
-                                      dh.data_ptr(), kept.data_ptr(), skept.data_ptr(),
-                                      _ptr(m_indices), M, I, _launch_stream(stream, dev)),
-           "dg_swiglu_fp8_backward")
+    rc = lib.dg_swiglu_fp8_backward(dgu.data_ptr(), sdgu.data_ptr(),
+                                    None if h is None else h.data_ptr(),
+                                    None if h is None else sh.data_ptr(), dh.data_ptr(),
+                                    kept.data_ptr(), skept.data_ptr(),
+                                    None if m_indices is None else m_indices.data_ptr(), M, I,
+                                    _launch_stream(stream, dev))
+    if rc:
+        raise DGError(rc, "dg_swiglu_fp8_backward")
 
 
 def dg_transpose_fp8_blocks(qt, st, q, s, block_rows: int = 128, m_indices=None,
@@ -1033,16 +1149,26 @@ def dg_transpose_fp8_blocks(qt, st, q, s, block_rows: int = 128, m_indices=None,
     """qt (codes [C, M]) and st float32 [M/128, C] (block_rows 1) or [M/128,
     C/128] (block_rows 128) = the transpose of q (codes [M, C], 1 x 128 scales
     s float32 [C/128, M]), quantised anew along the rows of q."""
-    M, C = _two(q, "q")
-    dev = q.get_device()
-    _need_fp8(q, s, M, C, dev, "q")
-    _need(qt, _CODES, (C, M), dev, "qt")
-    _need(st, (_F32,), ((M + 127) // 128, C if block_rows == 1 else (C + 127) // 128), dev, "st")
-    if m_indices is not None:
+    M, C = _need_matrix(q, "q")
+    dev, blocks = q.get_device(), ((M + 127) // 128, C if block_rows == 1 else (C + 127) // 128)
+    try:
+        ok = (dev >= 0 and _is_fp8(q, s, M, C, dev) and qt.dtype in _CODES and qt.shape == (C, M)
+              and qt.get_device() == dev and qt.is_contiguous() and st.dtype is _F32
+              and st.shape == blocks and st.get_device() == dev and st.is_contiguous()
+              and _are_layout_rows(m_indices, M, dev))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _need_fp8(q, s, M, C, dev, "q")
+        _need(qt, _CODES, (C, M), dev, "qt")
+        _need(st, (_F32,), blocks, dev, "st")
         _need(m_indices, (_I32,), (M,), dev, "m_indices")
-    _check(lib.dg_transpose_fp8_blocks(qt.data_ptr(), st.data_ptr(), block_rows, q.data_ptr(),
-                                       s.data_ptr(), _ptr(m_indices), M, C,
-                                       _launch_stream(stream, dev)), "dg_transpose_fp8_blocks")
+    rc = lib.dg_transpose_fp8_blocks(qt.data_ptr(), st.data_ptr(), block_rows, q.data_ptr(),
+                                     s.data_ptr(),
+                                     None if m_indices is None else m_indices.data_ptr(), M, C,
+                                     _launch_stream(stream, dev))
+    if rc:
+        raise DGError(rc, "dg_transpose_fp8_blocks")
 
 
 # ---------------------------------------------------------------------------

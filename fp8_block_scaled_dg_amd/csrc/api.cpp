@@ -710,12 +710,11 @@ int dg_moe_plan(int32_t* rows, int32_t* pairs, int32_t* m_indices, int64_t* offs
 namespace {
 
 // A workspace for the scales is optional; one that is given has to hold them.
-int run_dispatch(const dg::DispatchArgs& p, void* workspace, size_t workspace_bytes, void* stream) {
+int check_scales(const dg::DispatchArgs& p, void** workspace, size_t workspace_bytes) {
   const size_t need = dg::dispatch_workspace_bytes(p.T, p.k, p.H, p.weights != nullptr);
-  if (workspace == nullptr || workspace_bytes == 0 || need == 0) workspace = nullptr;
+  if (*workspace == nullptr || workspace_bytes == 0 || need == 0) *workspace = nullptr;
   else if (workspace_bytes < need) return DG_ERR_WORKSPACE;
-  if (!aligned(workspace, 16)) return DG_ERR_ALIGN;
-  return from_hip(dg::launch_dispatch(p, workspace, static_cast<hipStream_t>(stream)));
+  return aligned(*workspace, 16) ? DG_OK : DG_ERR_ALIGN;
 }
 
 }  // namespace
@@ -736,7 +735,8 @@ int dg_moe_dispatch_fp8(uint8_t* a, float* sa, const void* x, int dtype, int64_t
     return DG_ERR_ALIGN;
   const dg::DispatchArgs p{a, sa, x, dtype == DG_DTYPE_BF16, rows, pairs, weights, T, ldx, M, H, k,
                            0, nullptr};
-  return run_dispatch(p, workspace, workspace_bytes, stream);
+  const int st = check_scales(p, &workspace, workspace_bytes);
+  return st != DG_OK ? st : from_hip(dg::launch_dispatch(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 int dg_moe_combine(uint16_t* y, const uint16_t* c, const int32_t* rows, const float* weights,
@@ -762,14 +762,15 @@ int dg_moe_combine_backward(uint8_t* dc, float* sdc, float* dweights, const uint
   if (!aligned(dc, 16) || !aligned(c, 16) || !aligned(dy, 2) || !aligned(sdc, 4) ||
       !aligned(dweights, 4) || !aligned(rows, 4) || !aligned(pairs, 4) || !aligned(weights, 4))
     return DG_ERR_ALIGN;
+  hipStream_t q = static_cast<hipStream_t>(stream);
+  const dg::DispatchArgs d{dc, sdc, dy, true, rows, pairs, weights, T, lddy, M, H, k, 0, nullptr};
   if (dc) {
-    const dg::DispatchArgs p{dc, sdc, dy, true, rows, pairs, weights, T, lddy, M, H, k, 0, nullptr};
-    const int st = run_dispatch(p, workspace, workspace_bytes, stream);
+    const int st = check_scales(d, &workspace, workspace_bytes);
     if (st != DG_OK) return st;
+    if (!dweights) return from_hip(dg::launch_dispatch(d, workspace, q));
   }
-  if (!dweights) return DG_OK;
   const dg::CombineArgs p{nullptr, c, rows, weights, nullptr, dweights, dy, T, M, H, lddy, k};
-  return from_hip(dg::launch_combine_dot(p, static_cast<hipStream_t>(stream)));
+  return from_hip(dg::launch_combine_backward(p, d, workspace, q));
 }
 
 int dg_swiglu_fp8(uint8_t* h, float* sh, uint8_t* kept, float* skept, const uint16_t* gu,

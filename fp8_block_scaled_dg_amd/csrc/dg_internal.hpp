@@ -224,13 +224,15 @@ struct CombineArgs {
   const int32_t* rows;
   const float* weights;
   const uint16_t* residual;
-  float* dweights;     // launch_combine_dot
-  const uint16_t* dy;  // launch_combine_dot
+  float* dweights;     // backward only, as dy and lddy
+  const uint16_t* dy;
   int64_t T, M, H, lddy;
   int k;
 };
 hipError_t launch_combine(const CombineArgs& p, hipStream_t stream);
-hipError_t launch_combine_dot(const CombineArgs& p, hipStream_t stream);
+// dweights, and with d.a also the dispatch of w dy.
+hipError_t launch_combine_backward(const CombineArgs& p, DispatchArgs d, void* workspace,
+                                   hipStream_t stream);
 
 // SwiGLU in E4M3 with its checkpoint, and its gradient.
 struct SwigluArgs {

@@ -73,23 +73,47 @@ __device__ __forceinline__ void fill_rows(const DispatchArgs& p, int64_t r0, int
   for (int r = first; r < 32; ++r) store_stream(p.a + (r0 + r) * p.H + c, none);
 }
 
+// Part i of the fill: 32 rows by 4096 columns, with their scales.
+__device__ __forceinline__ void fill_block(const DispatchArgs& p, uint32_t i) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t parts = (uint32_t)((p.H + 4095) / 4096);
+  const int64_t r0 = (int64_t)(i / parts) * 32, c = (int64_t)(i % parts) * 4096 + threadIdx.x * 16;
+  if (p.pairs[r0 & ~int64_t(127)] < 0) return;
+  const int first = (int)__popcll(__ballot(lane < 32 && p.pairs[r0 + (lane & 31)] >= 0));
+  if (c >= p.H) return;
+  fill_rows(p, r0, first, c);
+  if ((threadIdx.x & 7) == 0)
+    for (int r = first; r < 32; ++r) p.sa[c / 128 * p.M + r0 + r] = 0.0f;
+}
+
+// One slot of a token whose values go out with its weight: columns c .. c + 7 to row
+// `row`, a parked scale to place `pair`; top: the largest magnitude of the block of v.
+template <bool PARKED>
+__device__ __forceinline__ void put_weighted(const DispatchArgs& p, const float (&v)[8], float top,
+                                             float w, int64_t pair, int64_t row, int64_t c, int lane) {
+  float wv[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) wv[i] = w * v[i];
+  // rounding is monotone: the largest product is that of the largest value
+  const RowScale b = row_scale(wv, fabsf(w) * top);
+  uint32_t q[2];
+  encode_values(wv, b, q);
+  store_stream(p.a + row * p.H + c, q);
+  if ((lane & 15) != 0) return;
+  if (PARKED) p.parked[pair * (p.H / 128) + c / 128] = b.scale;
+  else p.sa[c / 128 * p.M + row] = b.scale;
+}
+
 // A wave a (token, 512 columns).  PARKED: the scales go to the workspace, token by
 // token ([T][H/128], WEIGHTED [T k][H/128]), and dispatch_scales_kernel takes them
 // from there; else each goes to its place, and workgroups from token_groups on fill
-// the ends of the experts' last blocks, 32 rows by 4096 columns each.
+// the ends of the experts' last blocks.
 template <bool WEIGHTED, bool PARKED>
 __global__ void __launch_bounds__(256) dispatch_kernel(DispatchArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (!PARKED && blockIdx.x >= p.token_groups) {
-    const uint32_t i = blockIdx.x - p.token_groups, parts = (uint32_t)((p.H + 4095) / 4096);
-    const int64_t r0 = (int64_t)(i / parts) * 32, c = (int64_t)(i % parts) * 4096 + threadIdx.x * 16;
-    if (p.pairs[r0 & ~int64_t(127)] < 0) return;
-    const int first = (int)__popcll(__ballot(lane < 32 && p.pairs[r0 + (lane & 31)] >= 0));
-    if (c >= p.H) return;
-    fill_rows(p, r0, first, c);
-    if ((threadIdx.x & 7) == 0)
-      for (int r = first; r < 32; ++r) p.sa[c / 128 * p.M + r0 + r] = 0.0f;
+    fill_block(p, blockIdx.x - p.token_groups);
     return;
   }
   const uint32_t unit = blockIdx.x * 4 + wave, units = (uint32_t)((p.H + kCols - 1) / kCols);
@@ -100,31 +124,22 @@ __global__ void __launch_bounds__(256) dispatch_kernel(DispatchArgs p) {
   float v[8];
   load8(p.x, p.bf16, t * p.ldx + c, v);
   const float top = group_top<16>(top_of(v));
-  const bool leader = (lane & 15) == 0;
-  uint32_t q[2];
-  float scale = 0.0f;
-  if constexpr (!WEIGHTED) {
+  if constexpr (WEIGHTED) {
+    for (int j = 0; j < p.k; ++j)
+      if (slots.row_of(j) >= 0)
+        put_weighted<PARKED>(p, v, top, slots.weight_of(j), t * p.k + j, slots.row_of(j), c, lane);
+  } else {
     const RowScale b = row_scale(v, top);
+    uint32_t q[2];
     encode_values(v, b, q);
-    scale = b.scale;
-    if (PARKED && leader) p.parked[t * (p.H / 128) + c / 128] = scale;
-  }
-  for (int j = 0; j < p.k; ++j) {
-    const int row = slots.row_of(j);
-    if (row < 0) continue;
-    if constexpr (WEIGHTED) {
-      const float w = slots.weight_of(j);
-      float wv[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) wv[i] = w * v[i];
-      // rounding is monotone: the largest product is that of the largest value
-      const RowScale b = row_scale(wv, fabsf(w) * top);
-      encode_values(wv, b, q);
-      scale = b.scale;
-      if (PARKED && leader) p.parked[(t * p.k + j) * (p.H / 128) + c / 128] = scale;
+    const bool leader = (lane & 15) == 0;
+    if (PARKED && leader) p.parked[t * (p.H / 128) + c / 128] = b.scale;
+    for (int j = 0; j < p.k; ++j) {
+      const int row = slots.row_of(j);
+      if (row < 0) continue;
+      store_stream(p.a + (int64_t)row * p.H + c, q);
+      if (!PARKED && leader) p.sa[c / 128 * p.M + row] = b.scale;
     }
-    store_stream(p.a + (int64_t)row * p.H + c, q);
-    if (!PARKED && leader) p.sa[c / 128 * p.M + row] = scale;
   }
 }
 
@@ -200,32 +215,43 @@ __device__ __forceinline__ float wave_add(float v) {
   return v;
 }
 
-// One workgroup a token: its waves' partial sums meet in LDS, in wave order.
-template <int K>
-__global__ void __launch_bounds__(256) combine_dot_kernel(CombineArgs p) {
+// Gradient of the weights, one workgroup a token: its waves' partial sums meet in
+// LDS, in wave order.  DC other than none: with each row of c read, the row's
+// gradient (the dispatch of w dy) written, so that dy is read once for both.
+enum { DC_NONE, DC_DIRECT, DC_PARKED };
+template <int K, int DC>
+__global__ void __launch_bounds__(256) combine_backward_kernel(CombineArgs p, DispatchArgs d) {
   __shared__ float s_sum[4][kMoeMaxSlots];
+  if (DC == DC_DIRECT && blockIdx.x >= p.T) {
+    fill_block(d, blockIdx.x - (uint32_t)p.T);
+    return;
+  }
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x;
-  const Slots slots(p.rows, nullptr, t, p.k, p.M, lane);
+  const Slots slots(p.rows, d.weights, t, p.k, p.M, lane);
   float sum[K] = {};
-  for (int64_t c = threadIdx.x * 8; c < p.H; c += 2048) {
+  for (int64_t c = threadIdx.x * 8; c < p.H; c += 2048) {  // lanes leave by blocks of 16
     u4 v[K];
 #pragma unroll
     for (int j = 0; j < K; ++j)
       if (slots.row_of(j) >= 0)
         v[j] = __builtin_nontemporal_load(
             reinterpret_cast<const u4*>(p.c + (int64_t)slots.row_of(j) * p.H + c));
-    float d[8];
-    load8(p.dy, true, t * p.lddy + c, d);
+    float dy[8];
+    load8(p.dy, true, t * p.lddy + c, dy);
+    const float top = DC != DC_NONE ? group_top<16>(top_of(dy)) : 0.0f;
 #pragma unroll
     for (int j = 0; j < K; ++j)
       if (slots.row_of(j) >= 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          sum[j] = fmaf(d[2 * i], __uint_as_float(v[j][i] << 16), sum[j]);
-          sum[j] = fmaf(d[2 * i + 1], __uint_as_float(v[j][i] & 0xFFFF0000u), sum[j]);
+          sum[j] = fmaf(dy[2 * i], __uint_as_float(v[j][i] << 16), sum[j]);
+          sum[j] = fmaf(dy[2 * i + 1], __uint_as_float(v[j][i] & 0xFFFF0000u), sum[j]);
         }
+        if constexpr (DC != DC_NONE)
+          put_weighted<DC == DC_PARKED>(d, dy, top, slots.weight_of(j), d.weights ? t * p.k + j : t,
+                                       slots.row_of(j), c, lane);
       }
   }
 #pragma unroll
@@ -251,25 +277,33 @@ size_t dispatch_workspace_bytes(int64_t T, int k, int64_t H, bool weighted) {
   return (size_t)(weighted ? T * k : T) * (H / 128) * sizeof(float);
 }
 
+namespace {
+
+int64_t fill_blocks(const DispatchArgs& p) { return p.M / 32 * ((p.H + 4095) / 4096); }
+
+hipError_t launch_scales(const DispatchArgs& p, hipStream_t stream) {
+  const dim3 rows((unsigned)(p.M / 32 * ((p.H / 128 + 63) / 64)));
+  if (p.weights) hipLaunchKernelGGL(dispatch_scales_kernel<true>, rows, dim3(256), 0, stream, p);
+  else hipLaunchKernelGGL(dispatch_scales_kernel<false>, rows, dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_dispatch(DispatchArgs p, void* workspace, hipStream_t stream) {
   const int64_t units = (p.H + kCols - 1) / kCols;
   p.token_groups = (uint32_t)((p.T * units + 3) / 4);
   p.parked = static_cast<float*>(workspace);
-  const int64_t fill = workspace ? 0 : p.M / 32 * ((p.H + 4095) / 4096);
-  const dim3 grid((unsigned)(p.token_groups + fill)), block(256);
+  const dim3 grid((unsigned)(p.token_groups + (workspace ? 0 : fill_blocks(p)))), block(256);
   if (!workspace) {
     if (p.weights) hipLaunchKernelGGL((dispatch_kernel<true, false>), grid, block, 0, stream, p);
     else hipLaunchKernelGGL((dispatch_kernel<false, false>), grid, block, 0, stream, p);
     return hipGetLastError();
   }
-  const dim3 rows((unsigned)(p.M / 32 * ((p.H / 128 + 63) / 64)));
   if (p.weights) hipLaunchKernelGGL((dispatch_kernel<true, true>), grid, block, 0, stream, p);
   else hipLaunchKernelGGL((dispatch_kernel<false, true>), grid, block, 0, stream, p);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (p.weights) hipLaunchKernelGGL(dispatch_scales_kernel<true>, rows, block, 0, stream, p);
-  else hipLaunchKernelGGL(dispatch_scales_kernel<false>, rows, block, 0, stream, p);
-  return hipGetLastError();
+  return e == hipSuccess ? launch_scales(p, stream) : e;
 }
 
 hipError_t launch_combine(const CombineArgs& p, hipStream_t stream) {
@@ -281,11 +315,19 @@ hipError_t launch_combine(const CombineArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_combine_dot(const CombineArgs& p, hipStream_t stream) {
+hipError_t launch_combine_backward(const CombineArgs& p, DispatchArgs d, void* workspace,
+                                   hipStream_t stream) {
+  d.parked = static_cast<float*>(workspace);
+  const int mode = !d.a ? DC_NONE : workspace ? DC_PARKED : DC_DIRECT;
+  const dim3 grid((unsigned)(p.T + (mode == DC_DIRECT ? fill_blocks(d) : 0))), block(256);
   with_slots(p.k, [&](auto K) {
-    hipLaunchKernelGGL(combine_dot_kernel<decltype(K)::value>, dim3((unsigned)p.T), dim3(256), 0, stream, p);
+    constexpr int k = decltype(K)::value;
+    if (mode == DC_NONE) hipLaunchKernelGGL((combine_backward_kernel<k, DC_NONE>), grid, block, 0, stream, p, d);
+    else if (mode == DC_DIRECT) hipLaunchKernelGGL((combine_backward_kernel<k, DC_DIRECT>), grid, block, 0, stream, p, d);
+    else hipLaunchKernelGGL((combine_backward_kernel<k, DC_PARKED>), grid, block, 0, stream, p, d);
   });
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess && mode == DC_PARKED ? launch_scales(d, stream) : e;
 }
 
 }  // namespace dg

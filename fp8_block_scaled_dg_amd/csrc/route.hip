@@ -585,7 +585,8 @@ void launch_forward(const RouteArgs& p, hipStream_t stream) {
   const dim3 grid((unsigned)((p.T + tokens - 1) / tokens)), block(64 * kRouteWaves);
   const auto go = [&](auto biased, auto grouped) {
     constexpr bool B = decltype(biased)::value, G = decltype(grouped)::value;
-    if constexpr (WIDE) hipLaunchKernelGGL((route_wide_kernel<PER, B, G>), grid, block, 0, stream, p);
+    if constexpr (WIDE && PER == 4 && !G) return;  // 16 lanes always do
+    else if constexpr (WIDE) hipLaunchKernelGGL((route_wide_kernel<PER, B, G>), grid, block, 0, stream, p);
     else hipLaunchKernelGGL((route_kernel<PER, B, G>), grid, block, 0, stream, p);
   };
   if (p.top_groups < p.groups) p.bias ? go(IntTag<1>{}, IntTag<1>{}) : go(IntTag<0>{}, IntTag<1>{});

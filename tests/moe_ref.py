@@ -143,7 +143,8 @@ def e4m3(codes):
 
 def values(q, s):
     """codes [R][C], scales [C/128][R] -> the FP32 numbers they stand for, float64"""
-    return (e4m3(q) * np.repeat(s.astype(np.float64).T, 128, axis=1)).astype(np.float32).astype(np.float64)
+    with np.errstate(over="ignore", invalid="ignore"):  # rows that nothing wrote hold anything
+        return (e4m3(q) * np.repeat(s.astype(np.float64).T, 128, axis=1)).astype(np.float32).astype(np.float64)
 
 
 def sigmoid(x):

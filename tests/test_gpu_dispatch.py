@@ -41,7 +41,7 @@ def layout(dg, ids, E, extra=0):
     return dg.MoePlan(*out)
 
 
-# T, E, k: one launch up to 4096 pairs, then chunks with their counts in the workspace
+# T, E, k: one launch up to 16384 pairs, then chunks with their counts in the workspace
 PLANS = [(1, 1, 1), (1, 8, 2), (1, 1024, 16), (3, 1000, 3), (64, 8, 2), (127, 3, 1), (128, 1, 1), (129, 2, 2), (300, 60, 4),
          (512, 256, 8), (1365, 7, 3), (4097, 5, 1), (2001, 60, 4), (700, 1023, 7), (9001, 256, 8), (40000, 3, 2)]
 
@@ -140,6 +140,37 @@ def test_dispatch_through_the_workspace(dg, orc, weighted):
     assert np.array_equal(a[rows].cpu().numpy(), want) and np.array_equal(sa[:, rows].cpu().numpy(), ws)
     fill = torch.from_numpy(ref.blocks_used(p.m_indices.cpu().numpy())).cuda() & (p.pairs < 0)
     assert not a[fill].any() and not sa[:, fill].any()
+    # the gradient of combine writes the same rows, with and without the weights' gradient
+    c = torch.empty(p.pairs.numel(), H, dtype=torch.bfloat16, device="cuda")
+    for dw in (None, torch.empty(T, k, device="cuda")):
+        for stream in (None, torch.cuda.current_stream().cuda_stream):
+            b, sb = spoiled(p.pairs.numel(), H)
+            dg.dg_moe_combine_backward(b, sb, dw, x, c, p.rows, p.pairs, w, stream=stream)
+            assert torch.equal(a, b) and torch.equal(sa, sb)
+
+
+# T, E, k, H
+PARKED = [(8300, 3, 1, 16512), (4200, 5, 2, 16512), (1100, 16, 8, 16512), (600, 20, 16, 16512)]
+
+
+@pytest.mark.parametrize("T,E,k,H", PARKED)
+def test_combine_backward_through_the_workspace(dg, T, E, k, H):
+    """The same bits as without a workspace, with and without weights."""
+    g = torch.Generator(device="cuda").manual_seed(k)
+    rng = np.random.default_rng(k)
+    p = layout(dg, choice(rng, T, E, k, "holes"), E)
+    M = p.pairs.numel()
+    dy, c = (torch.randn(n, H, device="cuda", generator=g).to(torch.bfloat16) for n in (T, M))
+    stream = torch.cuda.current_stream().cuda_stream  # no workspace from torch
+    for w in (torch.rand(T, k, device="cuda", generator=g), None):
+        assert dg.dg_moe_dispatch_fp8_workspace_bytes(T, k, H, w is not None) > 0
+        outs = []
+        for s in (stream, None):
+            a, sa = spoiled(M, H)
+            dw = torch.full((T, k), float("nan"), device="cuda")
+            dg.dg_moe_combine_backward(a, sa, dw, dy, c, p.rows, p.pairs, w, stream=s)
+            outs.append((a, sa, dw))
+        assert all(torch.equal(x, y) for x, y in zip(*outs))
 
 
 def test_dispatch_of_tiny_and_huge_values(dg, orc):

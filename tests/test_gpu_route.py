@@ -43,7 +43,7 @@ def check(ids, w, l, k, **kw):
 CASES = [(1, 1, 1, 1, 1, 1), (1, 256, 8, 8, 4, 2), (3, 2, 2, 2, 1, 1), (5, 8, 2, 1, 1, 1), (7, 60, 4, 4, 2, 2),
          (4, 64, 8, 8, 3, 1), (9, 65, 6, 5, 2, 2), (33, 96, 16, 3, 2, 2), (16, 128, 8, 16, 5, 2), (6, 129, 3, 1, 1, 1),
          (17, 250, 8, 10, 4, 2), (8, 256, 8, 64, 20, 1), (5, 257, 8, 1, 1, 1), (3, 384, 8, 12, 4, 2),
-         (10, 513, 16, 27, 9, 2), (4, 1000, 8, 8, 4, 2), (5, 1024, 16, 64, 7, 2), (70, 16, 3, 8, 2, 1)]
+         (10, 513, 16, 27, 9, 2), (6, 100, 4, 1, 1, 1), (5, 300, 4, 10, 3, 1), (4, 700, 9, 1, 1, 1), (4, 1000, 8, 8, 4, 2), (5, 1024, 16, 64, 7, 2), (70, 16, 3, 8, 2, 1)]
 
 
 @pytest.mark.parametrize("bias", [False, True])
