@@ -18,10 +18,18 @@
 //                     sigmoid dl_j = scale g_j s_j (1 - s_j)
 // The choice itself, and so the bias, has no gradient.
 //
-// Up to 256 experts: 16 lanes per token, four tokens a wave, all in FP32 with
-// bounds on its errors; a token whose choice these bounds leave open is done
-// again by the whole wave in 64 bits (route_exact).  More experts: one wave per
-// token in 64 bits.
+// Up to 512 experts (in up to 16 groups): 16 lanes per token, four tokens a wave,
+// all in FP32 with bounds on its errors; a token whose choice these bounds leave
+// open is done again by the whole wave in 64 bits (route_exact).  More of either:
+// one wave per token in 64 bits.
+//
+// What bounds it is the chain of k rounds of a maximum over 16 lanes (45
+// instructions a round for 256 experts), not the logits' bytes.  MI355X, 16384 tokens,
+// k = 8, in a graph: 256 experts without a bias 8.0 us (FP32; 16.8 MB, 3.4 us at 5.0
+// TB/s), with a bias 12.5, and 8 groups by their best two 15.7 (of it some 5 for the
+// one token in two thousand that is done again: the last wave waits for it; a wave
+// per token in 64 bits for all took 37); 512 experts 24; 60 experts, k = 4, 30001
+// tokens 5.1, the gradient 5.0 (14 and 13 with a wave per token).
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
 
@@ -122,29 +130,37 @@ __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-
 
 // Scores in 64 bits: the softmax of the lanes' logits v (largest m) or their
 // sigmoid; 0 for v = -inf.
+__device__ __forceinline__ double wide_score(float v, float m, int scoring) {
+  if (scoring == ROUTE_SIGMOID) return 1.0 / (1.0 + exp(-(double)v));
+  return v == m ? 1.0 : v == -INFINITY ? 0.0 : exp((double)v - (double)m);
+}
 template <int PER>
-__device__ __forceinline__ void wide_scores(const float (&v)[PER], float m, int scoring,
-                                            double (&c)[PER]) {
+__device__ __forceinline__ void wide_scores(const float (&v)[PER], float m, int scoring, double (&c)[PER],
+                                            double* value, int lane) {
   double sum = 0.0;
+  if constexpr (PER <= 4) {
 #pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    if (scoring == ROUTE_SOFTMAX) {
-      c[q] = v[q] == m ? 1.0 : exp((double)v[q] - (double)m);
-      if (v[q] == -INFINITY) c[q] = 0.0;
-      sum += c[q];
-    } else {
-      c[q] = 1.0 / (1.0 + exp(-(double)v[q]));
-    }
+    for (int q = 0; q < PER; ++q) sum += c[q] = wide_score(v[q], m, scoring);
+  } else {
+    // one exponential in the code, not PER: unrolled they take every register
+    // there is (16384 tokens of 1024 experts with a bias 175 us, so 114)
+#pragma unroll
+    for (int q = 0; q < PER; ++q) value[lane * PER + q] = v[q];
+#pragma unroll 1
+    for (int q = 0; q < PER; ++q)
+      sum += value[lane * PER + q] = wide_score((float)value[lane * PER + q], m, scoring);
+#pragma unroll
+    for (int q = 0; q < PER; ++q) c[q] = value[lane * PER + q];
   }
   if (scoring == ROUTE_SOFTMAX) {
-    sum = wave_sum(sum);
+    const double inverse = 1.0 / wave_sum(sum);
 #pragma unroll
-    for (int q = 0; q < PER; ++q) c[q] /= sum;
+    for (int q = 0; q < PER; ++q) c[q] *= inverse;
   }
 }
 
 // One wave, token t, PER consecutive experts a lane; value: room for 64 * PER
-// numbers of this wave (GROUPED).
+// numbers of this wave (GROUPED, or PER above 4).
 template <int PER, bool BIASED, bool GROUPED>
 __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t, int lane, double* value) {
   using Key = std::conditional_t<BIASED, double, float>;
@@ -159,7 +175,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t, int l
   m = wave_top(m);
   Key key[PER];
   double c[PER];
-  if (BIASED || (GROUPED && p.best == 2)) wide_scores<PER>(v, m, p.scoring, c);
+  if (BIASED || (GROUPED && p.best == 2)) wide_scores<PER>(v, m, p.scoring, c, value, lane);
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int e = lane * PER + q;
@@ -256,10 +272,11 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t, int l
 
 template <int PER, bool BIASED, bool GROUPED>
 __global__ void __launch_bounds__(64 * kRouteWaves) route_wide_kernel(RouteArgs p) {
-  __shared__ double s_value[GROUPED ? kRouteWaves : 1][GROUPED ? 64 * PER : 1];
+  constexpr bool ROOM = GROUPED || BIASED;
+  __shared__ double s_value[ROOM ? kRouteWaves : 1][ROOM ? 64 * PER : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (t < p.T) route_exact<PER, BIASED, GROUPED>(p, t, threadIdx.x & 63, s_value[GROUPED ? wave : 0]);
+  if (t < p.T) route_exact<PER, BIASED, GROUPED>(p, t, threadIdx.x & 63, s_value[ROOM ? wave : 0]);
 }
 
 // ---- 16 lanes per token ----
@@ -305,21 +322,26 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
 // step by one, and the fraction is cut.  eps of the sigmoid, from v_exp_f32, v_rcp_f32 (one ulp
 // each) and the roundings of the argument, of 1 + e and of the product, is below
 // 2^-21 (s (1 - s) |l| <= 0.23 times 1.5 2^-22, s (1 - s) / 4 of 2^-23, s of 3 2^-24).  Of
-// the softmax: s times 2^-18 (|l - m| 2^-22 in the numerator, at most ln E <= 6 of
-// it weighted in the sum, 20 additions), s at most 1 / sum.  The sum with the bias
-// adds |c| 2^-24.  Two keys whose values differ by more than twice that are in c's
+// the softmax, with d = m - l: (2.25 d + 2) 2^-24 of the numerator, s d <= 0.37 / sum;
+// of the sum the same with d's mean, at most ln E <= 6.3, and 35 additions; two more
+// roundings: less than 64 2^-24 / sum.  The sum with the bias adds |c| 2^-24.  Two keys whose values differ by more than twice that are in c's
 // order; closer ones, and tokens that have to look below the window, are left to
 // route_exact, unless logit and bias are equal.  With 256 sigmoid scores and a
 // bias that is one token in two thousand.
-template <bool BIASED>
+// With more than 256 experts the index takes 9 bits and the value 23.
+template <bool BIASED, int PER>
 struct Grid {
-  static constexpr float window = BIASED ? 2.0f : 16.0f, steps = 16000000.0f / window;
+  static constexpr uint32_t index_bits = PER > 16 ? 9 : 8, most = (1u << index_bits) - 1;
+  static constexpr float top = (float)((1u << (32 - index_bits)) - 1);
+  static constexpr float window = BIASED ? 2.0f : 16.0f, steps = 0.95f * top / window;
 };
-constexpr uint32_t kIndexBits = 8;
 
 template <int PER, bool BIASED, bool GROUPED>
 __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
-  __shared__ double s_value[GROUPED ? kRouteWaves : 1][GROUPED ? 256 : 1];
+  using G = Grid<BIASED, PER>;
+  constexpr int EXACT = PER > 16 ? 8 : 4;  // experts a lane in route_exact
+  constexpr bool ROOM = GROUPED || (BIASED && EXACT > 4);
+  __shared__ double s_value[ROOM ? kRouteWaves : 1][ROOM ? 64 * EXACT : 1];
   const int lane = threadIdx.x & 63, lane16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * 4;
@@ -375,7 +397,6 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
       key[q] = v[q] > -INFINITY ? u | (uint32_t)(0xFFFF - base - q) : 0;
     }
   } else {
-    using G = Grid<BIASED>;
     float hi = -INFINITY;
 #pragma unroll
     for (int q = 0; q < PER; ++q) hi = larger(hi, BIASED ? c[q] : v[q]);  // NaN: the other
@@ -386,11 +407,11 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const float x = BIASED ? c[q] : v[q];
-      const uint32_t value = (uint32_t)__builtin_amdgcn_fmed3f((x - lo) * G::steps, 0.0f, 16777215.0f);
-      key[q] = (value << kIndexBits) + (uint32_t)(255 - base - q);
+      const uint32_t value = (uint32_t)__builtin_amdgcn_fmed3f((x - lo) * G::steps, 0.0f, G::top);
+      key[q] = (value << G::index_bits) + (G::most - (uint32_t)(base + q));
     }
   }
-  const uint32_t shift = exact ? 16 : kIndexBits;
+  const uint32_t shift = exact ? 16 : G::index_bits;
   if constexpr (GROUPED) {
     // a group's value, as an unsigned number: the largest key, or the sum of the
     // two largest scores in FP32 (off by the two errors and one rounding)
@@ -455,7 +476,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
     last = last > 0 ? next : 0;
     if (lane16 == j) after = last;
   }
-  const int id = mine >> shift == 0 ? -1 : (int)((exact ? 0xFFFFu : 255u) - (mine & ((1u << shift) - 1)));
+  const int id = mine >> shift == 0 ? -1 : (int)((exact ? 0xFFFFu : G::most) - (mine & ((1u << shift) - 1)));
   const float l = id >= 0 ? load_logit(p, t * p.ldl + id) : -INFINITY;
   if (!exact) {
     // equal logits and biases are in order, but not at the end of the choice,
@@ -483,7 +504,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
   if (left == 0) return;
   for (int r = 0; r < 4; ++r)
     if (left >> (16 * r) & 0xFFFF)
-      route_exact<4, BIASED, GROUPED>(p, t0 + r, lane, s_value[GROUPED ? wave : 0]);
+      route_exact<EXACT, BIASED, GROUPED>(p, t0 + r, lane, s_value[ROOM ? wave : 0]);
 }
 
 // The gradient: LANES lanes a token (16 or 64), PER consecutive experts each.
@@ -585,7 +606,7 @@ void launch_forward(const RouteArgs& p, hipStream_t stream) {
   const dim3 grid((unsigned)((p.T + tokens - 1) / tokens)), block(64 * kRouteWaves);
   const auto go = [&](auto biased, auto grouped) {
     constexpr bool B = decltype(biased)::value, G = decltype(grouped)::value;
-    if constexpr (WIDE && PER == 4 && !G) return;  // 16 lanes always do
+    if constexpr (WIDE && PER <= 8 && !G) return;  // 16 lanes always do
     else if constexpr (WIDE) hipLaunchKernelGGL((route_wide_kernel<PER, B, G>), grid, block, 0, stream, p);
     else hipLaunchKernelGGL((route_kernel<PER, B, G>), grid, block, 0, stream, p);
   };
@@ -613,7 +634,7 @@ hipError_t launch_route(RouteArgs p, hipStream_t stream) {
   p.lanes = grouped ? lanes_of(16) : 16;
   // experts a lane, where 16 lanes take a token
   const int per = grouped ? (p.E / p.groups + p.lanes - 1) / p.lanes : (p.E + 15) / 16;
-  if (p.E > 256 || per > 16 || (grouped && p.groups > 16)) {
+  if (p.E > 512 || per > 32 || (grouped && p.groups > 16)) {
     if (p.E <= 256) launch_forward<4, true>(p, stream);
     else if (p.E <= 512) launch_forward<8, true>(p, stream);
     else launch_forward<16, true>(p, stream);
@@ -621,8 +642,10 @@ hipError_t launch_route(RouteArgs p, hipStream_t stream) {
     launch_forward<4, false>(p, stream);
   } else if (per <= 8) {
     launch_forward<8, false>(p, stream);
-  } else {
+  } else if (per <= 16) {
     launch_forward<16, false>(p, stream);
+  } else {
+    launch_forward<32, false>(p, stream);
   }
   return hipGetLastError();
 }

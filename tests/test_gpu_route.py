@@ -43,7 +43,7 @@ def check(ids, w, l, k, **kw):
 CASES = [(1, 1, 1, 1, 1, 1), (1, 256, 8, 8, 4, 2), (3, 2, 2, 2, 1, 1), (5, 8, 2, 1, 1, 1), (7, 60, 4, 4, 2, 2),
          (4, 64, 8, 8, 3, 1), (9, 65, 6, 5, 2, 2), (33, 96, 16, 3, 2, 2), (16, 128, 8, 16, 5, 2), (6, 129, 3, 1, 1, 1),
          (17, 250, 8, 10, 4, 2), (8, 256, 8, 64, 20, 1), (5, 257, 8, 1, 1, 1), (3, 384, 8, 12, 4, 2),
-         (10, 513, 16, 27, 9, 2), (6, 100, 4, 1, 1, 1), (5, 300, 4, 10, 3, 1), (4, 700, 9, 1, 1, 1), (4, 1000, 8, 8, 4, 2), (5, 1024, 16, 64, 7, 2), (70, 16, 3, 8, 2, 1)]
+         (10, 513, 16, 27, 9, 2), (6, 100, 4, 1, 1, 1), (5, 300, 4, 10, 3, 1), (4, 700, 9, 1, 1, 1), (6, 384, 8, 24, 6, 2), (9, 512, 8, 16, 4, 2), (5, 480, 8, 3, 1, 1), (4, 1000, 8, 8, 4, 2), (5, 1024, 16, 64, 7, 2), (70, 16, 3, 8, 2, 1)]
 
 
 @pytest.mark.parametrize("bias", [False, True])
@@ -159,11 +159,13 @@ def test_infinite_logit(dg):
         assert ids.tolist() == [[5, 0], [0, 1]] and w[0].tolist() == [1.0, 0.5]
 
 
-def test_many_tokens(dg):
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [64, 256, 512])
+def test_many_tokens(dg, E, scoring):
     rng = np.random.default_rng(7)
-    logits, l = logits_of(rng, 3001, 256, torch.float32)
-    b = (rng.standard_normal(256) * 0.1).astype(np.float32)
-    kw = dict(scoring="sigmoid", groups=8, top_groups=4, group_best=2, scale=2.5)
+    logits, l = logits_of(rng, 2001, E, torch.float32)
+    b = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    kw = dict(scoring=scoring, groups=8, top_groups=4, group_best=2, scale=2.5)
     ids, w = run(dg, logits, 8, bias=torch.from_numpy(b).cuda(), **kw)
     check(ids, w, l, 8, bias=b, **kw)
 
