@@ -851,6 +851,17 @@ def _launch_stream(stream, device):
     return _stream_now(device) if stream is None else stream
 
 
+def _scratch(workspace, device):
+    """(address, bytes) of a workspace or of none."""
+    if workspace is None:
+        return None, 0
+    n = _workspace_bytes(workspace)
+    if workspace.get_device() != device:
+        raise ValueError("the workspace is on device %d, other tensors on %d"
+                         % (workspace.get_device(), device))
+    return workspace.data_ptr(), n
+
+
 def _refuse_slots(ids, weights, T, dev, name):
     k = _need_matrix(ids, name)[1]
     _need(ids, (_I32,), (T, k), dev, name)
@@ -954,8 +965,7 @@ def dg_moe_plan(rows, pairs, m_indices, offsets, counts, ids, workspace=None, st
         raise ValueError("pairs and counts must have one dimension")
     rc = lib.dg_moe_plan(rows.data_ptr(), pairs.data_ptr(), m_indices.data_ptr(),
                          offsets.data_ptr(), counts.data_ptr(), ids.data_ptr(), T, E, k, M,
-                         None if workspace is None else workspace.data_ptr(),
-                         _workspace_bytes(workspace), _launch_stream(stream, dev))
+                         *_scratch(workspace, dev), _launch_stream(stream, dev))
     if rc:
         raise DGError(rc, "dg_moe_plan")
 
@@ -1004,8 +1014,7 @@ def dg_moe_dispatch_fp8(a, sa, x, rows, pairs, weights=None, workspace=None, str
     rc = lib.dg_moe_dispatch_fp8(a.data_ptr(), sa.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], ld,
                                  rows.data_ptr(), pairs.data_ptr(),
                                  None if weights is None else weights.data_ptr(), T, k, M, H,
-                                 None if workspace is None else workspace.data_ptr(),
-                                 _workspace_bytes(workspace), _launch_stream(stream, dev))
+                                 *_scratch(workspace, dev), _launch_stream(stream, dev))
     if rc:
         raise DGError(rc, "dg_moe_dispatch_fp8")
 
@@ -1072,8 +1081,7 @@ def dg_moe_combine_backward(dc, sdc, dweights, dy, c, rows, pairs, weights=None,
                                      dy.data_ptr(), ld, None if dweights is None else c.data_ptr(),
                                      rows.data_ptr(), pairs.data_ptr(),
                                      None if weights is None else weights.data_ptr(), T, k, M, H,
-                                     None if workspace is None else workspace.data_ptr(),
-                                     _workspace_bytes(workspace), _launch_stream(stream, dev))
+                                     *_scratch(workspace, dev), _launch_stream(stream, dev))
     if rc:
         raise DGError(rc, "dg_moe_combine_backward")
 

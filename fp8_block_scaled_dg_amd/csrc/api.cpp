@@ -618,7 +618,8 @@ bool layout_ok(int64_t T, int k, int64_t M, int64_t cols, int64_t step) {
       cols % step != 0 || cols > (int64_t(1) << 34))
     return false;
   const int64_t parts = (cols + 511) / 512;
-  return T <= (int64_t(1) << 25) / parts && M <= (int64_t(1) << 29) / parts;
+  // launches of 256 threads have fewer than 2^24 workgroups
+  return T <= (int64_t(1) << 23) && T <= (int64_t(1) << 25) / parts && M <= (int64_t(1) << 27) / parts;
 }
 
 int check_swiglu(const int32_t* m_indices, int64_t M, int64_t I) {

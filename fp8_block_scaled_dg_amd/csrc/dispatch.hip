@@ -65,25 +65,29 @@ __device__ __host__ __forceinline__ void with_slots(int k, F&& f) {
   }
 }
 
-// Fills rows first .. 31 of the 32 from r0 on (the end of an expert's last block)
-// with zero codes, columns c .. c + 15 of this thread.
-__device__ __forceinline__ void fill_rows(const DispatchArgs& p, int64_t r0, int first, int64_t c) {
+// The rows of the 32 from r0 on that no pair has, one bit each; 0 in a 128-row
+// block without an expert.
+__device__ __forceinline__ uint32_t rows_to_fill(const DispatchArgs& p, int64_t r0) {
+  const int lane = threadIdx.x & 63;
+  if (p.pairs[r0 & ~int64_t(127)] < 0) return 0;
+  return (uint32_t)__ballot(lane < 32 && p.pairs[r0 + (lane & 31)] < 0);
+}
+
+// Zero codes for these rows, columns c .. c + 15 of this thread.
+__device__ __forceinline__ void fill_rows(const DispatchArgs& p, int64_t r0, uint32_t fill, int64_t c) {
   const uint32_t none[4] = {0, 0, 0, 0};
-#pragma unroll 4
-  for (int r = first; r < 32; ++r) store_stream(p.a + (r0 + r) * p.H + c, none);
+  for (; fill; fill &= fill - 1) store_stream(p.a + (r0 + __builtin_ctz(fill)) * p.H + c, none);
 }
 
 // Part i of the fill: 32 rows by 4096 columns, with their scales.
 __device__ __forceinline__ void fill_block(const DispatchArgs& p, uint32_t i) {
-  const int lane = threadIdx.x & 63;
   const uint32_t parts = (uint32_t)((p.H + 4095) / 4096);
   const int64_t r0 = (int64_t)(i / parts) * 32, c = (int64_t)(i % parts) * 4096 + threadIdx.x * 16;
-  if (p.pairs[r0 & ~int64_t(127)] < 0) return;
-  const int first = (int)__popcll(__ballot(lane < 32 && p.pairs[r0 + (lane & 31)] >= 0));
+  uint32_t fill = rows_to_fill(p, r0);
   if (c >= p.H) return;
-  fill_rows(p, r0, first, c);
+  fill_rows(p, r0, fill, c);
   if ((threadIdx.x & 7) == 0)
-    for (int r = first; r < 32; ++r) p.sa[c / 128 * p.M + r0 + r] = 0.0f;
+    for (; fill; fill &= fill - 1) p.sa[c / 128 * p.M + r0 + __builtin_ctz(fill)] = 0.0f;
 }
 
 // One slot of a token whose values go out with its weight: columns c .. c + 7 to row
@@ -156,14 +160,16 @@ __global__ void __launch_bounds__(256) dispatch_scales_kernel(DispatchArgs p) {
   const int64_t r0 = (int64_t)(blockIdx.x / parts) * 32, kb0 = (int64_t)(blockIdx.x % parts) * 64;
   if (p.pairs[r0 & ~int64_t(127)] < 0) return;
   const int n = (int)(kbs - kb0 < 64 ? kbs - kb0 : 64);
-  const int pair = p.pairs[r0 + (lane & 31)];
-  const int first = (int)__popcll(__ballot(lane < 32 && pair >= 0));
-  if (t < 32) s_from[t] = WEIGHTED ? pair : pair / p.k;  // of no use where pair is -1
+  const uint32_t fill = rows_to_fill(p, r0);
+  if (t < 32) {
+    const int pair = p.pairs[r0 + t];
+    s_from[t] = pair < 0 || pair >= p.T * p.k ? -1 : WEIGHTED ? pair : pair / p.k;
+  }
   __syncthreads();
 #pragma unroll
   for (int r = t >> 6; r < 32; r += 4)
-    s_scale[r][lane] = r < first && lane < n ? p.parked[(int64_t)s_from[r] * kbs + kb0 + lane] : 0.0f;
-  for (int64_t c = kb0 * 128 + t * 16; c < (kb0 + n) * 128; c += 4096) fill_rows(p, r0, first, c);
+    s_scale[r][lane] = s_from[r] >= 0 && lane < n ? p.parked[(int64_t)s_from[r] * kbs + kb0 + lane] : 0.0f;
+  for (int64_t c = kb0 * 128 + t * 16; c < (kb0 + n) * 128; c += 4096) fill_rows(p, r0, fill, c);
   __syncthreads();
 #pragma unroll
   for (int kb = t >> 5; kb < 64; kb += 8)

@@ -634,7 +634,7 @@ int dg_moe_plan(int32_t *rows, int32_t *pairs, int32_t *m_indices, int64_t *offs
  *         query returns 0 for calls that have no use for one.  Calls that may
  *         run at the same time need distinct ones.
  * Requirements: T >= 1, 1 <= k <= DG_MOE_MAX_SLOTS, M >= 128, M % 128 == 0,
- * H >= 128, H % 128 == 0; T * ceil(H/512) <= 2^25, M * ceil(H/512) <= 2^29;
+ * H >= 128, H % 128 == 0; T <= 2^23, T * ceil(H/512) <= 2^25, M * ceil(H/512) <= 2^27;
  * a 16-byte, the rest 4-byte aligned.  Deterministic.
  */
 size_t dg_moe_dispatch_fp8_workspace_bytes(int64_t T, int k, int64_t H, int weighted);
@@ -688,6 +688,7 @@ int dg_moe_combine_backward(uint8_t *dc, float *sdc, float *dweights, const uint
  * dh BF16 [M][I], with sig = 1 / (1 + e^-g), in FP32:
  *   dg = dh u sig (1 + g (1 - sig)),  du = dh g sig
  *   dgu  : out, E4M3 [M][2 I] interleaved as gu, sdgu FP32 [2 I/128][M].
+ *          dgu may be kept and sdgu skept: the gradient in its place.
  *   h, sh: out, silu(g) * u again, quantised (the operand of the weight
  *          gradient, so that the forward's h need not be kept); or NULL, both.
  * Requirements: M >= 1, I >= 128, I % 128 == 0, M * ceil(I/512) <= 2^25; codes,

@@ -280,6 +280,30 @@ def test_rows_past_32_bits(dg, orc):
     assert torch.equal(y, torch.stack((c[M - 128].float() + c[0].float(), c[M - 127].float())).to(torch.bfloat16))
 
 
+def test_layout_with_holes(dg, orc):
+    """A layout that no plan wrote, with rows to fill between those with pairs."""
+    for H in (256, 131072):              # the latter through the workspace
+        T, k, M = 64, 16, 2048
+        rng = np.random.default_rng(H)
+        rows = rng.permutation(M)[:T * k].reshape(T, k)
+        rows[0] = np.arange(0, M, 128)   # each block's first row has a pair
+        pairs, n = np.full(M, -1), np.arange(T * k).reshape(T, k)
+        _, first = np.unique(rows[::-1].reshape(-1), return_index=True)
+        keep = np.zeros(T * k, bool)
+        keep[first] = True
+        rows = np.where(keep.reshape(T, k)[::-1], rows, -1)
+        pairs[rows[rows >= 0]] = n[rows >= 0]
+        x = dev(rng.standard_normal((T, H)).astype(np.float32))
+        a, sa = spoiled(M, H)
+        assert (dg.dg_moe_dispatch_fp8_workspace_bytes(T, k, H) > 0) == (H > 256)
+        dg.dg_moe_dispatch_fp8(a, sa, x, dev(rows.astype(np.int32)), dev(pairs.astype(np.int32)))
+        at = np.concatenate([np.nonzero(pairs >= 0)[0][:200], np.nonzero(pairs < 0)[0][:200]])
+        q, s = orc.quantize(x.cpu().numpy(), 1)
+        want = np.where((pairs[at] >= 0)[:, None], q[pairs[at] // k], 0)
+        assert np.array_equal(a[dev(at)].cpu().numpy(), want)
+        assert np.array_equal(sa[:, dev(at)].cpu().numpy(), np.where(pairs[at] >= 0, s[:, pairs[at] // k], 0))
+
+
 def test_foreign_rows_are_left_out(dg):
     """Rows outside [0, M) in a layout that no plan wrote."""
     rows = torch.tensor([[0, 128], [-9, 2 ** 31 - 1]], dtype=torch.int32, device="cuda")

@@ -81,6 +81,9 @@ def test_forward_and_backward(dg, orc, M, I, grouped):
     h2, sh2 = spoiled(M, I)
     dg.dg_swiglu_fp8_backward(d1, sd1, dh, kept, skept, h2, sh2, m_indices=mi)
     assert torch.equal(d, d1) and torch.equal(sd, sd1)
+    k1, sk1 = kept.clone(), skept.clone()         # in the checkpoint's place
+    dg.dg_swiglu_fp8_backward(k1, sk1, dh, k1, sk1, m_indices=mi)
+    assert torch.equal(d, k1) and torch.equal(sd, sk1)
     v = ref.values(qk, sk)                        # the checkpoint's values
     y = dh.double().cpu().numpy()[real]
     a, b, ea, eb = ref.swiglu_gradient(v[:, 0::2], v[:, 1::2], y)

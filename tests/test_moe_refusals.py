@@ -63,7 +63,7 @@ def test_dispatch(dg):
         assert f(**{name: None}) == 1, name
     assert f(dt=2) == 3
     assert f(T=0) == f(k=0) == f(k=17) == f(M=0) == f(M=200) == f(H=0) == f(H=192) == f(ldx=255) == 2
-    assert f(T=1 << 26) == f(M=1 << 30) == f(T=1 << 25, H=1024, ldx=1024) == f(ldx=1 << 61) == 2
+    assert f(T=(1 << 23) + 1) == f(M=(1 << 27) + 128) == f(T=1 << 23, H=4096, ldx=4096) == f(ldx=1 << 61) == 2
     assert f(a=P4) == f(sa=P1) == f(x=P1) == f(x=P2, dt=0) == f(w=P2) == f(pairs=P1) == 4
     need = dg.dg_moe_dispatch_fp8_workspace_bytes(8192, 8, 7168)
     assert need == 8192 * 56 * 4 and dg.dg_moe_dispatch_fp8_workspace_bytes(8192, 8, 7168, True) == 8 * need
