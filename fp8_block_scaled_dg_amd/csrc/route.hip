@@ -25,11 +25,12 @@
 //
 // What bounds it is the chain of k rounds of a maximum over 16 lanes (45
 // instructions a round for 256 experts), not the logits' bytes.  MI355X, 16384 tokens,
-// k = 8, in a graph: 256 experts without a bias 8.0 us (FP32; 16.8 MB, 3.4 us at 5.0
-// TB/s), with a bias 12.5, and 8 groups by their best two 15.7 (of it some 5 for the
-// one token in two thousand that is done again: the last wave waits for it; a wave
-// per token in 64 bits for all took 37); 512 experts 24; 60 experts, k = 4, 30001
-// tokens 5.1, the gradient 5.0 (14 and 13 with a wave per token).
+// k = 8, in a graph: 256 experts without a bias 7.3 us (FP32; 16.8 MB, 3.4 us at 5.0
+// TB/s), with a bias 10.6, and 8 groups by their best two 12.2 (of it about 2 for the
+// tokens that are looked at again, since the last wave waits for them; 15.7 with
+// route_exact for all of these, 37 with a wave per token in 64 bits); 512 experts 21,
+// 1024 with a bias 84; 60 experts, k = 4, 30001 tokens 5.2, the gradient 5.0 (14 and
+// 13 with a wave per token).
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
 
@@ -137,21 +138,16 @@ __device__ __forceinline__ double wide_score(float v, float m, int scoring) {
 template <int PER>
 __device__ __forceinline__ void wide_scores(const float (&v)[PER], float m, int scoring, double (&c)[PER],
                                             double* value, int lane) {
+  // one exponential in the code, not PER: unrolled they take every register there
+  // is (16384 tokens of 1024 experts with a bias 175 us, so 84)
   double sum = 0.0;
-  if constexpr (PER <= 4) {
 #pragma unroll
-    for (int q = 0; q < PER; ++q) sum += c[q] = wide_score(v[q], m, scoring);
-  } else {
-    // one exponential in the code, not PER: unrolled they take every register
-    // there is (16384 tokens of 1024 experts with a bias 175 us, so 114)
-#pragma unroll
-    for (int q = 0; q < PER; ++q) value[lane * PER + q] = v[q];
+  for (int q = 0; q < PER; ++q) value[lane * PER + q] = v[q];
 #pragma unroll 1
-    for (int q = 0; q < PER; ++q)
-      sum += value[lane * PER + q] = wide_score((float)value[lane * PER + q], m, scoring);
+  for (int q = 0; q < PER; ++q)
+    sum += value[lane * PER + q] = wide_score((float)value[lane * PER + q], m, scoring);
 #pragma unroll
-    for (int q = 0; q < PER; ++q) c[q] = value[lane * PER + q];
-  }
+  for (int q = 0; q < PER; ++q) c[q] = value[lane * PER + q];
   if (scoring == ROUTE_SOFTMAX) {
     const double inverse = 1.0 / wave_sum(sum);
 #pragma unroll
@@ -160,7 +156,7 @@ __device__ __forceinline__ void wide_scores(const float (&v)[PER], float m, int 
 }
 
 // One wave, token t, PER consecutive experts a lane; value: room for 64 * PER
-// numbers of this wave (GROUPED, or PER above 4).
+// numbers of this wave (GROUPED or BIASED).
 template <int PER, bool BIASED, bool GROUPED>
 __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t, int lane, double* value) {
   using Key = std::conditional_t<BIASED, double, float>;
@@ -317,17 +313,21 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
 //   BF16 logits without a bias: the 16 bits of the logit in their order, exact.
 //   else: 24 bits, the place of the choice value c on a grid of kSteps steps over
 //   the kWindow below the largest c (what is further below gets 0 as well).
-// The value is off from c's place by at most eps kSteps + 3 steps for an error eps
-// of c: the difference to the window's end is rounded by a step, its product with the
-// step by one, and the fraction is cut.  eps of the sigmoid, from v_exp_f32, v_rcp_f32 (one ulp
-// each) and the roundings of the argument, of 1 + e and of the product, is below
-// 2^-21 (s (1 - s) |l| <= 0.23 times 1.5 2^-22, s (1 - s) / 4 of 2^-23, s of 3 2^-24).  Of
-// the softmax, with d = m - l: (2.25 d + 2) 2^-24 of the numerator, s d <= 0.37 / sum;
-// of the sum the same with d's mean, at most ln E <= 6.3, and 35 additions; two more
-// roundings: less than 64 2^-24 / sum.  The sum with the bias adds |c| 2^-24.  Two keys whose values differ by more than twice that are in c's
-// order; closer ones, and tokens that have to look below the window, are left to
-// route_exact, unless logit and bias are equal.  With 256 sigmoid scores and a
-// bias that is one token in two thousand.
+// The value is off from c's place by at most eps kSteps + 2.5 steps for an error eps
+// of c: the difference to the window's end is rounded by half a step, its product
+// with the steps by one, and the fraction is cut.  eps of the sigmoid s, in 2^-24: the
+// argument's product with log2 e 1.22 |l| s (1 - s) <= 0.27, v_exp_f32 (one ulp)
+// 2 s (1 - s) <= 0.5, 1 + e rounded 1, v_rcp_f32 (one ulp) 2: below 2^-22.  Of the
+// softmax, with d = m - l: (2.25 d + 2) 2^-24 of the numerator, s d <= 0.37 / sum; of
+// the sum the same with d's mean, at most ln E <= 6.3, and 35 additions; two more
+// roundings: less than 64 2^-24 / sum.  The sum with the bias adds |c| 2^-24.  Two
+// keys whose values differ by more than twice that are in c's order.  Where closer
+// ones meet among the k first or at their end, all that are that close to the k-th
+// or above it, up to 16, are put in order in 64 bits, one a lane; with a bias on the
+// softmax (whose sum would be needed in 64 bits), with more than 16, with groups
+// that are too close, or where the choice reaches below the window, the token is left
+// to route_exact.  With 256 sigmoid scores, a bias and 8 groups that is one token in
+// ten thousand, and one in three thousand is put in order.
 // With more than 256 experts the index takes 9 bits and the value 23.
 template <bool BIASED, int PER>
 struct Grid {
@@ -340,7 +340,7 @@ template <int PER, bool BIASED, bool GROUPED>
 __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
   using G = Grid<BIASED, PER>;
   constexpr int EXACT = PER > 16 ? 8 : 4;  // experts a lane in route_exact
-  constexpr bool ROOM = GROUPED || (BIASED && EXACT > 4);
+  constexpr bool ROOM = GROUPED || BIASED;
   __shared__ double s_value[ROOM ? kRouteWaves : 1][ROOM ? 64 * EXACT : 1];
   const int lane = threadIdx.x & 63, lane16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
   bool open = m == INFINITY;  // left to route_exact
   if (m == -INFINITY) m = 0.0f;
   // scores (what cannot be chosen: NaN), also where the weights need their sum
-  float inverse = 1.0f, eps = 0x1p-21f;
+  float inverse = 1.0f, eps = 0x1p-22f;
   if (BIASED || pairs || (!p.renormalise && softmax)) {
     float e[PER];
     if (softmax) {
@@ -403,7 +403,8 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
     hi = row_top(hi);
     const float lo = hi - G::window;
     open = open || (hi > -INFINITY && !(fabsf(hi) < 65536.0f));
-    near = 8 + (BIASED ? (uint32_t)(2.0f * G::steps * (fminf(eps, 1.0f) + (fminf(fabsf(hi), 65536.0f) + 2.0f) * 0x1p-24f)) : 0);
+    const float size = fminf(fmaxf(fabsf(hi), fabsf(lo)), 65536.0f);  // of c in the window
+    near = 6 + (BIASED ? (uint32_t)(2.0f * G::steps * (fminf(eps, 1.0f) + size * 0x1p-24f)) : 0);
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const float x = BIASED ? c[q] : v[q];
@@ -443,12 +444,17 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
       if (p.lanes >= 4) value = max(value, dpp<0x4E>(value));
       if (p.lanes >= 8) value = max(value, dpp<0x141>(value));
     }
-    int ahead = 0;  // of the other groups, by rotating the 16 lanes
+    int ahead = 0, level = 0;  // of the other groups, by rotating the 16 lanes
     static_for<15>([&](auto R) {
       constexpr int r = decltype(R)::value + 1;
-      if ((r & (p.lanes - 1)) == 0) ahead += dpp<0x120 + r>(value) > value;
+      if ((r & (p.lanes - 1)) == 0) {
+        const uint32_t o = dpp<0x120 + r>(value);
+        ahead += o > value;
+        level += o >= value;
+      }
     });
     const bool stays = ahead < p.top_groups;
+    open = open || (stays && value > 0 && level >= p.top_groups);  // equal sums
     // the smallest that stays against the largest that does not
     const uint32_t in = ~row_top(stays ? ~value : 0u), out = row_top(stays ? 0u : value);
     if (out > 0) {
@@ -464,10 +470,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
   // k rounds of the largest key below the last one: key - last wraps round to
   // the top of the range for these and stays below them for keys taken before
   uint32_t mine = 0, after = 0, last = 0;
-#pragma unroll
-  for (int q = 0; q < PER; ++q) last = max(last, key[q]);
-  last = row_top(last);
-  for (int j = 0; j < p.k; ++j) {
+  const auto take = [&](int j) {  // lane j gets the largest of what is left
     if (lane16 == j) mine = last;
     uint32_t d = 0u - last;  // no key: 0
 #pragma unroll
@@ -475,31 +478,57 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
     const uint32_t next = last + row_top(d);
     last = last > 0 ? next : 0;
     if (lane16 == j) after = last;
-  }
-  const int id = mine >> shift == 0 ? -1 : (int)((exact ? 0xFFFFu : G::most) - (mine & ((1u << shift) - 1)));
-  const float l = id >= 0 ? load_logit(p, t * p.ldl + id) : -INFINITY;
+  };
+#pragma unroll
+  for (int q = 0; q < PER; ++q) last = max(last, key[q]);
+  last = row_top(last);
+  for (int j = 0; j < p.k; ++j) take(j);
+  const auto id_of = [&](uint32_t k) {
+    return k >> shift == 0 ? -1 : (int)((exact ? 0xFFFFu : G::most) - (k & ((1u << shift) - 1)));
+  };
+  bool chosen = lane16 < p.k, doubt = false;
   if (!exact) {
-    // equal logits and biases are in order, but not at the end of the choice,
-    // where others may be near as well
-    const float b = BIASED && id >= 0 ? p.bias[id] : 0.0f;
-    const float l1 = dpp<0x101>(l), b1 = dpp<0x101>(b);  // the next slot's
-    const bool same = lane16 + 1 < p.k && l1 == l && b1 == b;
-    open = open || (lane16 < p.k && (id < 0 || ((mine >> shift) - (after >> shift) <= near && !same)));
+    open = open || (chosen && mine >> shift == 0);
+    doubt = chosen && (mine >> shift) - (after >> shift) <= near;
+    if (BIASED && softmax) open = open || doubt;
+  }
+  int slot = lane16, id = id_of(mine);
+  float l = chosen && id >= 0 ? load_logit(p, t * p.ldl + id) : -INFINITY;
+  if (__ballot(doubt && !open)) {
+    for (int j = p.k; j < 16; ++j) take(j);
+    const uint32_t kth = (uint32_t)__shfl((int)mine, (lane & 48) + p.k - 1, 64) >> shift;
+    const auto close = [&](uint32_t k) { return k >> shift != 0 && kth - (k >> shift) <= near; };
+    open = open || close(last);  // a seventeenth
+    chosen = chosen || close(mine);
+    id = chosen ? id_of(mine) : -1;
+    l = id >= 0 ? load_logit(p, t * p.ldl + id) : -INFINITY;
+    double x = l;
+    if (BIASED && id >= 0) x = 1.0 / (1.0 + exp(-x)) + (double)p.bias[id];
+    slot = 0;
+    static_for<15>([&](auto R) {
+      constexpr int r = decltype(R)::value + 1;
+      const double o = dpp<0x120 + r>(x);
+      const int oid = (int)dpp<0x120 + r>((uint32_t)id);
+      slot += oid >= 0 && (o > x || (o == x && oid < id));
+    });
+    chosen = chosen && slot < p.k;
+    if (!chosen) l = -INFINITY;
   }
   const uint64_t left = __ballot(open && t0 + (lane >> 4) < p.T);
+  const bool some = chosen && id >= 0;
   float w = 0.0f;
   if (p.renormalise) {
     const float top = row_top(l);
-    const float r = id >= 0 ? relative_score(l, top, p.scoring) : 0.0f;
+    const float r = some ? relative_score(l, top, p.scoring) : 0.0f;
     w = p.scale * r / row_sum(r);
-  } else if (p.scoring == ROUTE_SOFTMAX) {
+  } else if (softmax) {
     w = p.scale * expf(l - m) * inverse;
   } else {
     w = p.scale * sigmoid(l);
   }
-  if (lane16 < p.k && t0 + (lane >> 4) < p.T && !(left >> (lane & 48) & 0xFFFF)) {
-    p.ids[t * p.k + lane16] = id;
-    p.weights[t * p.k + lane16] = id >= 0 ? w : 0.0f;
+  if (chosen && t0 + (lane >> 4) < p.T && !(left >> (lane & 48) & 0xFFFF)) {
+    p.ids[t * p.k + slot] = id;
+    p.weights[t * p.k + slot] = some ? w : 0.0f;
   }
   if (left == 0) return;
   for (int r = 0; r < 4; ++r)

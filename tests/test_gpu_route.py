@@ -110,6 +110,27 @@ def test_close_scores_are_told_apart(dg):
             check(ids, w, l.astype(np.float64), 8, **kw)
 
 
+def test_a_few_close_scores(dg):
+    """Two to eighteen experts that FP32 does not order, at the top, at the end of
+    the choice or below it, among others that are far away."""
+    rng = np.random.default_rng(15)
+    T = 600
+    for E, k in ((60, 4), (256, 8), (500, 16)):
+        l = rng.standard_normal((T, E)).astype(np.float32)
+        for t in range(T):
+            order = np.argsort(-l[t])
+            n, at = rng.integers(2, 19), rng.integers(0, k + 4)
+            some = order[at:at + n]
+            step = rng.choice([2.0 ** -24, 2.0 ** -22, 0.0])
+            l[t, some] = l[t, order[at]] + (rng.integers(-6, 7, some.size) * step).astype(np.float32)
+        few = (rng.integers(-3, 4, E) * 2.0 ** -23).astype(np.float32)
+        for bias in (None, few, (rng.standard_normal(E) * 0.1).astype(np.float32)):
+            for scoring in ("softmax", "sigmoid"):
+                ids, w = run(dg, torch.from_numpy(l).cuda(), k, scoring=scoring,
+                             bias=None if bias is None else torch.from_numpy(bias).cuda())
+                check(ids, w, l.astype(np.float64), k, bias=bias, scoring=scoring)
+
+
 def test_masked_experts(dg):
     """-inf, NaN, the type's lowest value and biases that switch experts off;
     tokens and groups that nothing is left of."""
