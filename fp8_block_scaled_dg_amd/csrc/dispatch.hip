@@ -11,7 +11,16 @@
 //
 // All are bound by HBM.  A wave takes 512 columns, eight a lane, so a 128-column
 // block is one row of 16 lanes; a token's values are read once and leave k
-// times.
+// times.  MI355X, BF16, tokens x columns to k of E experts (a copy moves 5.0 TB/s,
+// stores alone to scattered rows 5.1):
+//   dispatch 8192 x 7168, 8 of 256      148 us  720 MB, of it 117 MB of zeros
+//                                               that fill the experts' blocks
+//   combine  8192 x 7168, 8 of 256      184 us  1058 MB, 5.7 TB/s
+//            4001 x 2048, 4 of 60      14.4 us
+//   its gradient, 4001 x 2048, 4 of 60 22.8 us  113 MB (25.8 in two launches, dy
+//                                               read twice)
+// One token of 4096 columns takes 4.5 us, 64 tokens' combine 3: a launch and its
+// chain of loads (the slots' rows, then what they say).
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
 #include "fp8_rows.hpp"

@@ -11,7 +11,12 @@
 //
 // g and u of hidden unit i are columns 2i and 2i + 1.  Rows that only fill an
 // expert's last 128-row block are written as zeros, blocks without an expert are
-// not touched.  All are bound by HBM.
+// not touched.
+//
+// All are bound by HBM.  MI355X (a copy moves 5.0 TB/s): h alone, 2048 rows of 11008
+// units 24 us (113 MB and 10 MB of fill); with the checkpoint 32768 rows of 1408 and 4
+// thousand to fill 69 us (366 MB, 5.3 TB/s), the gradient with h again 70; turned
+// operands 18 thousand rows of 2048 columns 15.8 (scales of columns, 75 MB).
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
 #include "fp8_rows.hpp"
