@@ -311,10 +311,10 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
 // A token's choice by unsigned keys, value above index, so that one maximum
 // gives both and equal values go to the lowest index.  Value 0: cannot be chosen.
 //   BF16 logits without a bias: the 16 bits of the logit in their order, exact.
-//   else: 24 bits, the place of the choice value c on a grid of kSteps steps over
-//   the kWindow below the largest c (what is further below gets 0 as well).
-// The value is off from c's place by at most eps kSteps + 2.5 steps for an error eps
-// of c: the difference to the window's end is rounded by half a step, its product
+//   else: 24 bits (23 with more than 256 experts), the place of the choice value c
+//   on a grid of `steps` to 1 over the `window` below the largest c (what is
+//   further below gets 0 as well).
+// The value is off from c's place by at most eps steps + 2.5 for an error eps of c: the difference to the window's end is rounded by half a step, its product
 // with the steps by one, and the fraction is cut.  eps of the sigmoid s, in 2^-24: the
 // argument's product with log2 e 1.22 |l| s (1 - s) <= 0.27, v_exp_f32 (one ulp)
 // 2 s (1 - s) <= 0.5, 1 + e rounded 1, v_rcp_f32 (one ulp) 2: below 2^-22.  Of the
@@ -326,9 +326,9 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
 // or above it, up to 16, are put in order in 64 bits, one a lane; with a bias on the
 // softmax (whose sum would be needed in 64 bits), with more than 16, with groups
 // that are too close, or where the choice reaches below the window, the token is left
-// to route_exact.  With 256 sigmoid scores, a bias and 8 groups that is one token in
-// ten thousand, and one in three thousand is put in order.
-// With more than 256 experts the index takes 9 bits and the value 23.
+// to route_exact.  With 256 sigmoid scores of normal logits (deviation 2), a bias
+// (0.1) and 4 of 8 groups that is one token in thirty thousand; one in 1600 is put in
+// order.
 template <bool BIASED, int PER>
 struct Grid {
   static constexpr uint32_t index_bits = PER > 16 ? 9 : 8, most = (1u << index_bits) - 1;
