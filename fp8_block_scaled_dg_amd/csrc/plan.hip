@@ -8,10 +8,11 @@
 // every workgroup counts all of them itself (one launch).  Many: a first launch
 // leaves each chunk's counts in the workspace.
 //
-// MI355X, a call of many in a graph, one launch / two: 128 pairs 3.7 / 6.6 us, 8004 of 60
-// experts 6.3 / 7.8, 16384 of 256 8.3 / 8.9, of 8 (whose counters collide) 10.2 / 8.3, 65536
-// of 256 15.6 / 9.7; 262144 14.8.  Reading and writing take 0.2 us at most; the rest is
-// launches and a chain of four steps, each a memory latency or a barrier.
+// MI355X, a call of many in a graph: 128 pairs 3.8 us, 8004 of 60 experts 5.3, 16384 of
+// 256 8.1, 65536 9.7, 262144 14.7.  One launch / two, with chunks of 1024: 8004 6.3 /
+// 7.8, 16384 of 256 8.3 / 8.9, of 8 (whose counters collide) 10.2 / 8.3, 65536 15.6 / 9.7.
+// Reading and writing take 0.2 us at most; the rest is launches and a chain of four
+// steps, each a memory latency or a barrier.
 //
 // Nothing depends on the order in which workgroups or waves run: the counters
 // in LDS are sums, and a wave ranks its 64 pairs by which lanes hold the same
@@ -207,10 +208,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanArgs p) {
   }
 }
 
-// Chunks of 1024 pairs (128 a wave, two rounds of 64), more where the rows to
-// fill are many next to the pairs, at most 256.
+// Chunks of 512 pairs (a round of 64 a wave), more where the rows to fill are many
+// next to the pairs, at most 256.  8004 pairs 5.3 us, with chunks of 1024 6.3, of 2048
+// 8.2; 65536 9.7, 9.7 and 11.7.
 int plan_chunks(int64_t n, int64_t M) {
-  int64_t c = (n + 1023) / 1024;
+  int64_t c = (n + 511) / 512;
   const int64_t fill = (M + 8191) / 8192;
   if (c < fill) c = fill;
   const int64_t most = (n + 63) / 64;  // not more than there is work for
