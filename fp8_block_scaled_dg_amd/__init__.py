@@ -821,16 +821,19 @@ def _is_fp8(q, s, rows, cols, device):
 def _need_rows(x, dtypes, name):
     """(rows, columns, row stride, device number) of a device matrix with
     contiguous rows of any stride."""
+    try:
+        (rows, cols), (ld, one), device = x.shape, x.stride(), x.get_device()
+        if x.dtype in dtypes and device >= 0 and (one == 1 or cols <= 1) and (ld >= cols or rows <= 1):
+            return rows, cols, ld if rows > 1 else cols, device
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(x, torch.Tensor) or x.dtype not in dtypes:
         raise TypeError("%s must be a tensor of %s" % (name, " or ".join(map(str, dtypes))))
     if x.dim() != 2:
         raise ValueError("%s must be a matrix" % name)
     if not x.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    (rows, cols), (ld, one) = x.shape, x.stride()
-    if cols > 1 and one != 1 or rows > 1 and ld < cols:
-        raise ValueError("the rows of %s must be contiguous and must not overlap" % name)
-    return rows, cols, ld if rows > 1 else cols, x.get_device()
+    raise ValueError("the rows of %s must be contiguous and must not overlap" % name)
 
 
 def _need_matrix(t, name):
@@ -855,11 +858,9 @@ def _scratch(workspace, device):
     """(address, bytes) of a workspace or of none."""
     if workspace is None:
         return None, 0
-    n = _workspace_bytes(workspace)
-    if workspace.get_device() != device:
-        raise ValueError("the workspace is on device %d, other tensors on %d"
-                         % (workspace.get_device(), device))
-    return workspace.data_ptr(), n
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor on device %d" % device)
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _refuse_slots(ids, weights, T, dev, name):
@@ -985,9 +986,10 @@ def _dispatch_workspace(workspace, stream, T, k, H, weights, device):
 
 
 def _are_slots(rows, weights, T, device):
-    return (rows.dtype is _I32 and len(rows.shape) == 2 and rows.shape[0] == T
+    shape = rows.shape
+    return (rows.dtype is _I32 and len(shape) == 2 and shape[0] == T
             and rows.get_device() == device and rows.is_contiguous()
-            and (weights is None or weights.dtype is _F32 and weights.shape == rows.shape
+            and (weights is None or weights.dtype is _F32 and weights.shape == shape
                  and weights.get_device() == device and weights.is_contiguous()))
 
 
@@ -1023,11 +1025,14 @@ def dg_moe_combine(y, c, rows, weights=None, residual=None, stream=None) -> None
     """y [T, H] (bf16) = sum over the slots of weights (float32 [T, k], or all
     1) times the rows of c [M, H] (bf16), plus residual [T, H] (bf16)."""
     try:
-        T, H = shape = y.shape
-        M, dev = c.shape[0], y.get_device()
-        ok = (y.dtype in _BF16_TYPES and c.dtype in _BF16_TYPES and c.shape == (M, H)
-              and c.get_device() == dev >= 0 and y.is_contiguous() and c.is_contiguous()
-              and _are_slots(rows, weights, T, dev)
+        shape, slots, dev = y.shape, rows.shape, y.get_device()
+        (T, H), (M, cols), k = shape, c.shape, slots[1]
+        ok = (cols == H and slots[0] == T and len(slots) == 2 and y.dtype in _BF16_TYPES
+              and c.dtype in _BF16_TYPES and rows.dtype is _I32
+              and c.get_device() == rows.get_device() == dev >= 0
+              and y.is_contiguous() and c.is_contiguous() and rows.is_contiguous()
+              and (weights is None or weights.dtype is _F32 and weights.shape == slots
+                   and weights.get_device() == dev and weights.is_contiguous())
               and (residual is None or residual.dtype in _BF16_TYPES and residual.shape == shape
                    and residual.get_device() == dev and residual.is_contiguous()))
     except (AttributeError, ValueError, IndexError):
@@ -1041,8 +1046,8 @@ def dg_moe_combine(y, c, rows, weights=None, residual=None, stream=None) -> None
         _need(residual, _BF16_TYPES, shape, dev, "residual")
     rc = lib.dg_moe_combine(y.data_ptr(), c.data_ptr(), rows.data_ptr(),
                             None if weights is None else weights.data_ptr(),
-                            None if residual is None else residual.data_ptr(), T, rows.shape[1], M,
-                            H, _launch_stream(stream, dev))
+                            None if residual is None else residual.data_ptr(), T, k, M, H,
+                            _launch_stream(stream, dev))
     if rc:
         raise DGError(rc, "dg_moe_combine")
 
