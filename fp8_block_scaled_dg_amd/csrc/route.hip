@@ -287,7 +287,10 @@ __device__ __forceinline__ T row_join(T v, F&& f) {
   v = f(v, dpp<0x140>(v));
   return v;
 }
-__device__ __forceinline__ float larger(float a, float b) {  // no NaN; one instruction
+// One instruction.  Of a NaN and a number the number; the compiler takes it for
+// the first operand where that is -inf for certain, so a NaN may come out of the
+// first of several values, to go at the next.
+__device__ __forceinline__ float larger(float a, float b) {
   return __builtin_amdgcn_fmed3f(a, b, __builtin_inff());
 }
 __device__ __forceinline__ float row_top(float v) { return row_join(v, larger); }
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     if (softmax && v[q] != v[q]) v[q] = -INFINITY;
-    m = larger(m, v[q]);  // with a NaN: m
+    m = larger(m, v[q]);
   }
   m = row_top(m);
   bool open = m == INFINITY;  // left to route_exact
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
   } else {
     float hi = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < PER; ++q) hi = larger(hi, BIASED ? c[q] : v[q]);  // NaN: the other
+    for (int q = 0; q < PER; ++q) hi = larger(hi, BIASED ? c[q] : v[q]);
     hi = row_top(hi);
     const float lo = hi - G::window;
     open = open || (hi > -INFINITY && !(fabsf(hi) < 65536.0f));
@@ -422,8 +425,9 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
       float a = -INFINITY, b = -INFINITY;  // a >= b
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
-        b = __builtin_amdgcn_fmed3f(a, b, c[q]);  // with a NaN the least of the others: b
-        a = larger(a, c[q]);
+        const float x = c[q] > -INFINITY ? c[q] : -INFINITY;  // no NaN into the median
+        b = __builtin_amdgcn_fmed3f(a, b, x);
+        a = larger(a, x);
       }
       const auto meet = [&](float oa, float ob) {
         b = larger(__builtin_amdgcn_fmed3f(a, b, oa), ob);  // the second of the two firsts, or a second

@@ -169,6 +169,25 @@ def test_masked_experts(dg):
             assert np.all(np.abs(d.double().cpu().numpy() - ww) <= size * (6 * 500 + 200) * ref.U + 2.0 ** -126)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_half_of_the_experts_masked(dg, dtype):
+    """A random half of each token's logits at -inf, NaN or the type's lowest
+    value, in groups of few experts."""
+    rng = np.random.default_rng(16)
+    for E, k, G, tg in ((36, 5, 9, 5), (72, 5, 3, 2), (160, 16, 16, 8), (96, 4, 4, 3), (500, 8, 5, 2), (120, 6, 20, 6)):
+        for fill in (-np.inf, np.nan, float(torch.finfo(dtype).min)):
+            l = (rng.standard_normal((60, E)) * 4).astype(np.float32)
+            l[rng.random(l.shape) < 0.5] = fill
+            logits = torch.from_numpy(l).to(dtype).cuda()
+            l = logits.double().cpu().numpy()
+            for bias in (None, np.zeros(E, np.float32), (rng.standard_normal(E) * 0.3).astype(np.float32)):
+                for scoring in ("softmax", "sigmoid"):
+                    for best in (1, 2):
+                        kw = dict(scoring=scoring, groups=G, top_groups=tg, group_best=best, renormalise=best == 1)
+                        ids, w = run(dg, logits, k, bias=None if bias is None else torch.from_numpy(bias).cuda(), **kw)
+                        check(ids, w, l, k, bias=bias, **kw)
+
+
 def test_infinite_logit(dg):
     """+inf is chosen first; with the softmax its token's weights are NaN."""
     l = torch.zeros(2, 8)
