@@ -13,10 +13,11 @@
 // expert's last 128-row block are written as zeros, blocks without an expert are
 // not touched.
 //
-// All are bound by HBM.  MI355X (a copy moves 5.0 TB/s): h alone, 2048 rows of 11008
-// units 24 us (113 MB and 10 MB of fill); with the checkpoint 32768 rows of 1408 and 4
-// thousand to fill 69 us (366 MB, 5.3 TB/s), the gradient with h again 70; turned
-// operands 18 thousand rows of 2048 columns 15.8 (scales of columns, 75 MB).
+// All are bound by HBM, the gradient with h again by its VALU as well.  MI355X (a copy
+// moves 5.0 TB/s): h alone, 2048 rows of 11008 units 26 us (113 MB and 10 MB of fill);
+// with the checkpoint 32768 rows of 1408 and 8 thousand to fill 70 us (366 MB, 5.2
+// TB/s), the gradient with h again 75; turned operands 18 thousand rows of 2048 columns
+// 15.8 (scales of columns, 75 MB).
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
 #include "fp8_rows.hpp"
@@ -31,10 +32,56 @@ __device__ __forceinline__ float2 decode2(uint32_t codes, bool high) {
                     : __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
   return make_float2(v.x, v.y);
 }
-// 1 / (1 + e^-g) with the hardware's exp2 and reciprocal (one ulp each): off by
-// at most (|g| + 2) 2^-23 relative, against 2^-4 of the E4M3 codes that follow.
-__device__ __forceinline__ float sigmoid(float g) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+// 1 / (1 + e^-g) of N gates, off by four half steps at most.
+//   e^-g : 2^n 2^f, n the integer next to -g log2 e and |f| <= 1/2 what is left of the
+//          product, rounded once; v_exp_f32 is off by one unit in the last place.
+//          SHORT gates have 8 significant bits (BF16): their product with 15 bits of
+//          log2 e is exact, so f takes two instructions, not five (the same f for all
+//          of them)
+//   1/d  : as in row_scale, correctly rounded (here d = 1 to 1 + e^87)
+// Gates beyond 87 in magnitude (rare, a branch of its own) go through the library's
+// e^a; below -87 the sigmoid is e^g (1 + e^g is 1 in FP32 from -17 down), where e^-g
+// would overflow and its reciprocal leave the normal range.
+// With v_exp_f32 of -g log2 e rounded once and v_rcp_f32 alone the sigmoid is off by
+// (|g| + 2) half steps, and subnormal ones are lost; that took 0 to 1.5 us less in the
+// forward, 5 to 6.5 in the gradient of 32768 rows.
+template <bool SHORT, int N>
+__device__ __forceinline__ void sigmoids(const float (&g)[N], float (&sig)[N]) {
+#pragma clang fp contract(off)
+  float top = fabsf(g[0]);
+#pragma unroll
+  for (int j = 1; j < N; ++j) top = fmaxf(top, fabsf(g[j]));
+  constexpr float integer = 0x1.8p23f;  // added: the sum's low bits are the nearest integer
+  constexpr float log2e = 0x1.715476p+0f, rest = 0x1.4ae0cp-26f;  // log2 e: their sum,
+  constexpr float log2e15 = 0x1.7154p+0f, rest15 = 0x1.d94ae0p-18f;  // and theirs
+  float e[N], m[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if constexpr (SHORT) {
+      m[j] = __builtin_fmaf(g[j], -log2e, integer);
+      e[j] = __builtin_fmaf(g[j], -rest15, __builtin_fmaf(g[j], -log2e15, integer - m[j]));
+    } else {
+      const float p = g[j] * -log2e;
+      m[j] = p + integer;
+      const float low = __builtin_fmaf(g[j], -rest, __builtin_fmaf(g[j], -log2e, -p));
+      e[j] = (p - (m[j] - integer)) + low;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) e[j] = __builtin_amdgcn_exp2f(e[j]);
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    e[j] = 1.0f + __uint_as_float(__float_as_uint(e[j]) + (__float_as_uint(m[j]) << 23));
+#pragma unroll
+  for (int j = 0; j < N; ++j) sig[j] = __builtin_amdgcn_rcpf(e[j]);
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    sig[j] = __builtin_fmaf(__builtin_fmaf(-e[j], sig[j], 1.0f), sig[j], sig[j]);
+  if (top > 87.0f) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (fabsf(g[j]) > 87.0f) sig[j] = g[j] < 0.0f ? expf(g[j]) : 1.0f;  // 1 + e^-87 is 1
+  }
 }
 
 // A workgroup takes p.tile_rows rows by 512 hidden units, a wave a row at a time,
@@ -71,22 +118,33 @@ struct RowInput {
       s = p.skept[2 * c / 128 * p.M + r];
     }
   }
-  // g: gate/up or their gradients, h: silu(gate) * up
+  // g: gate/up or their gradients, h: silu(gate) * up, every operation rounded by
+  // itself: the bits that elementary FP32 operations in this order give
   __device__ __forceinline__ void compute(float (&g)[16], float (&h)[8]) const {
+#pragma clang fp contract(off)
+    float gate[8], sig[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if constexpr (FORWARD) {
         const uint32_t u = j < 4 ? a[j & 3] : b[j & 3];
         g[2 * j] = __uint_as_float(u << 16);
         g[2 * j + 1] = __uint_as_float(u & 0xFFFF0000u);
-        h[j] = g[2 * j] * sigmoid(g[2 * j]) * g[2 * j + 1];
       } else {
         const float2 v = decode2(a[j >> 1], j & 1);
+        g[2 * j] = v.x * s;
+        g[2 * j + 1] = v.y * s;
+      }
+      gate[j] = g[2 * j];
+    }
+    sigmoids<FORWARD>(gate, sig);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float up = g[2 * j + 1], x = gate[j] * sig[j];
+      h[j] = x * up;
+      if constexpr (!FORWARD) {
         const float dh = __uint_as_float(j & 1 ? b[j >> 1] & 0xFFFF0000u : b[j >> 1] << 16);
-        const float gate = v.x * s, up = v.y * s, sig = sigmoid(gate), x = gate * sig;
-        g[2 * j] = dh * up * __builtin_fmaf(x, 1.0f - sig, sig);
+        g[2 * j] = dh * up * sig[j] * (1.0f + gate[j] * (1.0f - sig[j]));
         g[2 * j + 1] = dh * x;
-        h[j] = x * up;
       }
     }
   }
