@@ -29,8 +29,9 @@
 // TB/s), with a bias 10.6, and 8 groups by their best two 12.2 (of it about 2 for the
 // tokens that are looked at again, since the last wave waits for them; 15.7 with
 // route_exact for all of these, 37 with a wave per token in 64 bits); 512 experts 21,
-// 1024 with a bias 84; 60 experts, k = 4, 30001 tokens 5.2, the gradient 5.0 (14 and
-// 13 with a wave per token).
+// 1024 with a bias 84; 60 experts, k = 4, 30001 tokens 5.2, the gradient 5.4 (14 and
+// 13 with a wave per token; with e^d from v_exp_f32 of a product rounded once, off by
+// (d + 2) half steps, it took 5.0).
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
 
@@ -125,6 +126,19 @@ __device__ __forceinline__ float load_logit(const RouteArgs& p, int64_t at) {
 __device__ __forceinline__ float relative_score(float v, float m, int scoring) {
   if (scoring == ROUTE_SOFTMAX) return expf(v - m);
   return expf(fminf(v, 0.0f) - fminf(m, 0.0f)) * ((1.0f + expf(-fabsf(m))) / (1.0f + expf(-fabsf(v))));
+}
+
+// The sum of a lane's values in halves: log2 PER roundings deep.
+template <int PER>
+__device__ __forceinline__ float lane_sum(const float (&v)[PER]) {
+  float s[PER];
+#pragma unroll
+  for (int q = 0; q < PER; ++q) s[q] = v[q];
+#pragma unroll
+  for (int n = PER / 2; n >= 1; n /= 2)
+#pragma unroll
+    for (int q = 0; q < n; ++q) s[q] += s[q + n];
+  return s[0];
 }
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
@@ -252,10 +266,10 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t, int l
     const float r = my_id >= 0 ? relative_score(l, top, p.scoring) : 0.0f;
     w = p.scale * r / wave_sum(r);
   } else if (p.scoring == ROUTE_SOFTMAX) {
-    float sum = 0.0f;
+    float e[PER];
 #pragma unroll
-    for (int q = 0; q < PER; ++q) sum += expf(v[q] - m);
-    w = p.scale * expf(l - m) / wave_sum(sum);
+    for (int q = 0; q < PER; ++q) e[q] = expf(v[q] - m);
+    w = p.scale * (expf(l - m) / wave_sum(lane_sum(e)));
   } else {
     w = p.scale * sigmoid(l);
   }
@@ -321,8 +335,8 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
 // with the steps by one, and the fraction is cut.  eps of the sigmoid s, in 2^-24: the
 // argument's product with log2 e 1.22 |l| s (1 - s) <= 0.27, v_exp_f32 (one ulp)
 // 2 s (1 - s) <= 0.5, 1 + e rounded 1, v_rcp_f32 (one ulp) 2: below 2^-22.  Of the
-// softmax, with d = m - l: (2.25 d + 2) 2^-24 of the numerator, s d <= 0.37 / sum; of
-// the sum the same with d's mean, at most ln E <= 6.3, and 35 additions; two more
+// softmax, with d = m - l (rounded): (d + 2) 2^-24 of the numerator, s d <= 0.37 / sum;
+// of the sum the same with d's mean, at most ln E <= 6.3, and 9 additions; two more
 // roundings: less than 64 2^-24 / sum.  The sum with the bias adds |c| 2^-24.  Two
 // keys whose values differ by more than twice that are in c's order.  Where closer
 // ones meet among the k first or at their end, all that are that close to the k-th
@@ -369,17 +383,14 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
   bool open = m == INFINITY;  // left to route_exact
   if (m == -INFINITY) m = 0.0f;
   // scores (what cannot be chosen: NaN), also where the weights need their sum
-  float inverse = 1.0f, eps = 0x1p-22f;
+  float total = 1.0f, eps = 0x1p-22f;
   if (BIASED || pairs || (!p.renormalise && softmax)) {
     float e[PER];
     if (softmax) {
-      float sum = 0.0f;
 #pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        e[q] = __builtin_amdgcn_exp2f((v[q] - m) * 1.44269504f);
-        sum += e[q];
-      }
-      inverse = 1.0f / row_sum(sum);
+      for (int q = 0; q < PER; ++q) e[q] = expf(v[q] - m);
+      total = row_sum(lane_sum(e));
+      const float inverse = 1.0f / total;
       eps = inverse * 0x1p-18f;
 #pragma unroll
       for (int q = 0; q < PER; ++q) e[q] *= inverse;
@@ -526,7 +537,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs p) {
     const float r = some ? relative_score(l, top, p.scoring) : 0.0f;
     w = p.scale * r / row_sum(r);
   } else if (softmax) {
-    w = p.scale * expf(l - m) * inverse;
+    w = p.scale * (expf(l - m) / total);
   } else {
     w = p.scale * sigmoid(l);
   }
@@ -572,7 +583,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_backward_kernel(RouteA
     if (p.scoring == ROUTE_SIGMOID) slot *= sigmoid(-l);
   } else if (p.scoring == ROUTE_SOFTMAX) {
     // every logit: minus the sum of the slots' parts times its score
-    float v[PER], m = -INFINITY, sum = 0.0f;
+    float v[PER], m = -INFINITY;
     load_logits<PER>(p.logits, p.bf16, t * p.ldl + at * PER, p.E - at * PER, v);
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
@@ -582,11 +593,8 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_backward_kernel(RouteA
     m = top_of(m);
     if (!(m > -INFINITY)) m = 0.0f;
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      d[q] = __builtin_amdgcn_exp2f((v[q] - m) * 1.44269504f);
-      sum += d[q];
-    }
-    sum = sum_of(sum);
+    for (int q = 0; q < PER; ++q) d[q] = expf(v[q] - m);
+    const float sum = sum_of(lane_sum(d));
     const float inverse = sum > 0.0f ? 1.0f / sum : 0.0f;
     slot = id >= 0 ? g * (expf(l - m) * inverse) : 0.0f;
     const float all = -sum_of(slot) * inverse;
