@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_backward_kernel(RouteA
     const float top = top_of(l);
     const float r = id >= 0 ? relative_score(l, top, p.scoring) : 0.0f;
     const float sum = sum_of(r);
-    const float q = sum > 0.0f ? r / sum : 0.0f;
+    const float q = sum == 0.0f ? 0.0f : r / sum;  // NaN with +inf among the chosen
     slot = q * (g - sum_of(g * q));
     if (p.scoring == ROUTE_SIGMOID) slot *= sigmoid(-l);
   } else if (p.scoring == ROUTE_SOFTMAX) {
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_backward_kernel(RouteA
 #pragma unroll
     for (int q = 0; q < PER; ++q) d[q] = expf(v[q] - m);
     const float sum = sum_of(lane_sum(d));
-    const float inverse = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
     slot = id >= 0 ? g * (expf(l - m) * inverse) : 0.0f;
     const float all = -sum_of(slot) * inverse;
 #pragma unroll

@@ -582,8 +582,10 @@ int dg_moe_route(int32_t *ids, float *weights, const void *logits, int dtype, in
  * columns written, ldd >= E, aligned to its element) from dweights FP32 [T][k],
  * with the ids, scoring, renormalise and scale of the forward call.  FP32
  * throughout, rounded once.  A slot with an id outside [0, E), or with a logit
- * of -inf or NaN, gives nothing; such logits get 0.  The choice, and with it
- * the bias, has no gradient.
+ * of -inf or NaN, gives nothing; such logits get 0.  With the softmax, +inf
+ * makes the gradients NaN as it does the weights: of the token's chosen logits
+ * if it is chosen itself (renormalise), of all of them (no renormalise).  The
+ * choice, and with it the bias, has no gradient.
  */
 int dg_moe_route_backward(void *dlogits, int64_t ldd, const float *dweights, const int32_t *ids,
                           const void *logits, int dtype, int64_t ldl, int scoring,
