@@ -623,7 +623,8 @@ bool layout_ok(int64_t T, int k, int64_t M, int64_t cols, int64_t step) {
 }
 
 int check_swiglu(const int32_t* m_indices, int64_t M, int64_t I) {
-  if (M < 1 || I < 128 || I % 128 != 0 || I > (int64_t(1) << 34)) return DG_ERR_SHAPE;
+  // a workgroup takes 4 to 32 rows by 512 units: fewer than 2^24 of them for one row too
+  if (M < 1 || I < 128 || I % 128 != 0 || I > (int64_t(1) << 32)) return DG_ERR_SHAPE;
   if (M > (int64_t(1) << 25) / ((I + 511) / 512)) return DG_ERR_SHAPE;
   if (m_indices && M % 128 != 0) return DG_ERR_SHAPE;
   return aligned(m_indices, 4) ? DG_OK : DG_ERR_ALIGN;

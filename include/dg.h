@@ -693,8 +693,8 @@ int dg_moe_combine_backward(uint8_t *dc, float *sdc, float *dweights, const uint
  *          dgu may be kept and sdgu skept: the gradient in its place.
  *   h, sh: out, silu(g) * u again, quantised (the operand of the weight
  *          gradient, so that the forward's h need not be kept); or NULL, both.
- * Requirements: M >= 1, I >= 128, I % 128 == 0, M * ceil(I/512) <= 2^25; codes,
- * gu and dh 16-byte, scales and m_indices 4-byte aligned.  Deterministic.
+ * Requirements: M >= 1, 128 <= I <= 2^32, I % 128 == 0, M * ceil(I/512) <= 2^25;
+ * codes, gu and dh 16-byte, scales and m_indices 4-byte aligned.  Deterministic.
  */
 int dg_swiglu_fp8(uint8_t *h, float *sh, uint8_t *kept, float *skept, const uint16_t *gu,
                   const int32_t *m_indices, int64_t M, int64_t I, void *stream);
