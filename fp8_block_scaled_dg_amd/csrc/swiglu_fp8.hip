@@ -16,7 +16,7 @@
 // All are bound by HBM, the gradient with h again by its VALU as well.  MI355X (a copy
 // moves 5.0 TB/s): h alone, 2048 rows of 11008 units 26 us (113 MB and 10 MB of fill);
 // with the checkpoint 32768 rows of 1408 and 8 thousand to fill 70 us (366 MB, 5.2
-// TB/s), the gradient with h again 75; turned operands 18 thousand rows of 2048 columns
+// TB/s), the gradient with h again 76; turned operands 18 thousand rows of 2048 columns
 // 15.8 (scales of columns, 75 MB).
 #include "dg_device.hpp"
 #include "dg_internal.hpp"
@@ -38,13 +38,13 @@ __device__ __forceinline__ float2 decode2(uint32_t codes, bool high) {
 //          SHORT gates have 8 significant bits (BF16): their product with 15 bits of
 //          log2 e is exact, so f takes two instructions, not five (the same f for all
 //          of them)
-//   1/d  : as in row_scale, correctly rounded (here d = 1 to 1 + e^87)
+//   1/d  : correctly rounded, d = 1 to 1 + e^87
 // Gates beyond 87 in magnitude (rare, a branch of its own) go through the library's
 // e^a; below -87 the sigmoid is e^g (1 + e^g is 1 in FP32 from -17 down), where e^-g
 // would overflow and its reciprocal leave the normal range.
 // With v_exp_f32 of -g log2 e rounded once and v_rcp_f32 alone the sigmoid is off by
-// (|g| + 2) half steps, and subnormal ones are lost; that took 0 to 1.5 us less in the
-// forward, 5 to 6.5 in the gradient of 32768 rows.
+// (|g| + 2) half steps, and subnormal ones are lost; that took 0.7 to 1.7 us less in the
+// forward (of 48 and 70), 7 to 9 in the gradient (of 63 and 76; 32768 rows of 1408).
 template <bool SHORT, int N>
 __device__ __forceinline__ void sigmoids(const float (&g)[N], float (&sig)[N]) {
 #pragma clang fp contract(off)
@@ -73,10 +73,7 @@ __device__ __forceinline__ void sigmoids(const float (&g)[N], float (&sig)[N]) {
   for (int j = 0; j < N; ++j)
     e[j] = 1.0f + __uint_as_float(__float_as_uint(e[j]) + (__float_as_uint(m[j]) << 23));
 #pragma unroll
-  for (int j = 0; j < N; ++j) sig[j] = __builtin_amdgcn_rcpf(e[j]);
-#pragma unroll
-  for (int j = 0; j < N; ++j)
-    sig[j] = __builtin_fmaf(__builtin_fmaf(-e[j], sig[j], 1.0f), sig[j], sig[j]);
+  for (int j = 0; j < N; ++j) sig[j] = reciprocal_rn(e[j]);
   if (top > 87.0f) {
 #pragma unroll
     for (int j = 0; j < N; ++j)
