@@ -623,7 +623,7 @@ bool layout_ok(int64_t T, int k, int64_t M, int64_t cols, int64_t step) {
 }
 
 int check_swiglu(const int32_t* m_indices, int64_t M, int64_t I) {
-  // a workgroup takes 4 to 32 rows by 512 units: fewer than 2^24 of them for one row too
+  // a workgroup takes 4 to 16 rows by 512 units: fewer than 2^24 of them for one row too
   if (M < 1 || I < 128 || I % 128 != 0 || I > (int64_t(1) << 32)) return DG_ERR_SHAPE;
   if (M > (int64_t(1) << 25) / ((I + 511) / 512)) return DG_ERR_SHAPE;
   if (m_indices && M % 128 != 0) return DG_ERR_SHAPE;

@@ -15,7 +15,7 @@
 //
 // All are bound by HBM, the gradient with h again by its VALU as well.  MI355X (a copy
 // moves 5.0 TB/s): h alone, 2048 rows of 11008 units 26 us (113 MB and 10 MB of fill);
-// with the checkpoint 32768 rows of 1408 and 8 thousand to fill 70 us (366 MB, 5.2
+// with the checkpoint 32768 rows of 1408 and 8 thousand to fill 66 us (366 MB, 5.5
 // TB/s), the gradient with h again 76; turned operands 18 thousand rows of 2048 columns
 // 15.8 (scales of columns, 75 MB).
 #include "dg_device.hpp"
@@ -44,7 +44,7 @@ __device__ __forceinline__ float2 decode2(uint32_t codes, bool high) {
 // would overflow and its reciprocal leave the normal range.
 // With v_exp_f32 of -g log2 e rounded once and v_rcp_f32 alone the sigmoid is off by
 // (|g| + 2) half steps, and subnormal ones are lost; that took 0.7 to 1.7 us less in the
-// forward (of 48 and 70), 7 to 9 in the gradient (of 63 and 76; 32768 rows of 1408).
+// forward (of 48 and 66), 7 to 9 in the gradient (of 63 and 76; 32768 rows of 1408).
 template <bool SHORT, int N>
 __device__ __forceinline__ void sigmoids(const float (&g)[N], float (&sig)[N]) {
 #pragma clang fp contract(off)
@@ -84,7 +84,7 @@ __device__ __forceinline__ void sigmoids(const float (&g)[N], float (&sig)[N]) {
 // A workgroup takes p.tile_rows rows by 512 hidden units, a wave a row at a time,
 // eight units a lane: a block of h is 16 lanes, one of gate/up 8.  The scales of
 // the tile are put together in LDS and leave in runs along the rows.
-constexpr int kUnits = 512, kTileRows = 32;
+constexpr int kUnits = 512, kTileRows = 16;
 struct ScaleTile {
   float h[kUnits / 128][kTileRows], g[kUnits / 64][kTileRows];
 };
@@ -252,14 +252,17 @@ __global__ void __launch_bounds__(256) transpose_blocks_kernel(TransposeArgs p) 
 
 hipError_t launch_swiglu(SwigluArgs p, bool backward, hipStream_t stream) {
   const int64_t parts = (p.I + kUnits - 1) / kUnits;
-  // Long runs of scales, but 4096 workgroups, and 1024 before four rows (a row a
-  // wave): rows of 11008 units, 1024 in the layout (128 real) 7.9 us with 8 rows a
-  // workgroup, 8.2 with 16, 8.9 with 4; 3040 (2048 real) 26.1 with 16, 29.0 with 32; 1408
-  // units, 41 thousand rows 69 with 16, 75 with 32.
+  // Rows a workgroup.  Four (a row a wave) where eight would leave fewer than 600
+  // workgroups, two and a bit a CU: h of 512 rows of 4096 units (512 workgroups of 8 rows)
+  // 4.5 us, so 4.9 with eight; 256 of 11008 (704) 5.9, so 5.6.  Eight from there on:
+  // 32768 rows of 1408 with the checkpoint 60 us, 64 with four, 63 with sixteen.  Sixteen
+  // for the gradient from 4096 workgroups on, for longer runs of scales: with h again 70
+  // us, so 72 with eight (2048 of 11008, 2816 workgroups: 34.6 and 34.8); with
+  // thirty-two no less.
   const auto groups = [&] { return (p.M + p.tile_rows - 1) / p.tile_rows * parts; };
   p.tile_rows = kTileRows;
-  while (p.tile_rows > 8 && groups() < 4096) p.tile_rows /= 2;
-  if (groups() < 1024) p.tile_rows = 4;
+  if (!backward || groups() < 4096) p.tile_rows = 8;
+  if (p.tile_rows == 8 && groups() < 600) p.tile_rows = 4;
   const dim3 grid((unsigned)groups()), block(256);
   if (!backward && !p.kept) hipLaunchKernelGGL((swiglu_kernel<true, false>), grid, block, 0, stream, p);
   else if (!backward) hipLaunchKernelGGL((swiglu_kernel<true, true>), grid, block, 0, stream, p);

@@ -1,4 +1,4 @@
-"""The 8-bit SwiGLU with 4, 8, 16 and 32 rows a workgroup: every row, its scales and
+"""The 8-bit SwiGLU with 4, 8 and (the gradient) 16 rows a workgroup: every row, its scales and
 the rows to fill are those of calls on few rows (4 rows a workgroup, each compared with
 the definition elsewhere), and rows at the tiles' ends are compared with the definition."""
 import numpy as np
@@ -18,26 +18,25 @@ def dg():
     return m
 
 
-def tile_rows(M, I):
-    """Rows a workgroup takes: long runs of scales, but 4096 workgroups, and 1024
-    before four rows."""
+def tile_rows(M, I, backward=False):
+    """Rows a workgroup takes."""
     def groups(rows):
         return -(-M // rows) * -(-I // 512)
-    rows = 32
-    while rows > 8 and groups(rows) < 4096:
-        rows //= 2
-    return 4 if groups(rows) < 1024 else rows
+    if backward and groups(16) >= 4096:
+        return 16
+    return 4 if groups(8) < 600 else 8
 
 
-# M, I, grouped, rows a workgroup
-SHAPES = [(8203, 128, False, 8), (1003, 4224, False, 8), (65537, 128, False, 16), (131073, 128, False, 32),
-          (21999, 1152, False, 16), (8320, 128, True, 8), (7296, 1152, True, 8), (22016, 1152, True, 16),
-          (44032, 1152, True, 32), (3968, 1152, True, 8), (2560, 1152, True, 4)]
+# M, I, grouped, rows a workgroup forward and backward
+SHAPES = [(8203, 128, False, 8, 8), (1003, 4224, False, 8, 8), (4801, 128, False, 8, 8), (65537, 128, False, 8, 16),
+          (131073, 128, False, 8, 16), (21999, 1152, False, 8, 16), (8320, 128, True, 8, 8), (7296, 1152, True, 8, 8),
+          (22016, 1152, True, 8, 16), (44032, 1152, True, 8, 16), (3968, 1152, True, 8, 8), (1536, 1152, True, 4, 4)]
 
 
 def test_every_tiling_is_there():
-    assert [tile_rows(M, I) for M, I, _, _ in SHAPES] == [rows for _, _, _, rows in SHAPES]
-    assert {rows for _, _, g, rows in SHAPES if g} == {4, 8, 16, 32}
+    assert [(tile_rows(M, I), tile_rows(M, I, True)) for M, I, *_ in SHAPES] == [tuple(s[3:]) for s in SHAPES]
+    for grouped in (False, True):
+        assert {rows for s in SHAPES if s[2] == grouped for rows in s[3:]} >= {8, 16}
 
 
 def spoiled(M, C):
@@ -59,8 +58,8 @@ def calls(dg, gu, dh, mi):
     return out + [same]
 
 
-@pytest.mark.parametrize("M,I,grouped,rows", SHAPES)
-def test_tiling(dg, M, I, grouped, rows):
+@pytest.mark.parametrize("M,I,grouped,forward,rows", SHAPES)
+def test_tiling(dg, M, I, grouped, forward, rows):
     g = torch.Generator(device="cuda").manual_seed(M)
     rng = np.random.default_rng(M)
     gu = (torch.randn(M, 2 * I, device="cuda", generator=g) * 4).to(torch.bfloat16)
