@@ -979,8 +979,8 @@ def _dispatch_workspace(workspace, stream, T, k, H, weights, device):
     """The caller's workspace, else one from torch for a call that has use for
     it; torch's memory belongs to its current stream, so not where the call
     is sent to another one."""
-    if workspace is not None or stream is not None or T * k * H < 1 << 26:  # as the library says
-        return workspace
+    if workspace is not None or stream is not None or T * k * H < 1 << 26:
+        return workspace  # that few have no use for one: the library is asked about the others
     n = lib.dg_moe_dispatch_fp8_workspace_bytes(T, k, H, weights is not None)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 

@@ -13,10 +13,13 @@
 // block is one row of 16 lanes; a token's values are read once and leave k
 // times.  MI355X, BF16, tokens x columns to k of E experts (a copy moves 5.0 TB/s,
 // stores alone to scattered rows 5.1):
-//   dispatch 8192 x 7168, 8 of 256      148 us  720 MB, of it 117 MB of zeros
-//                                               that fill the experts' blocks
+//   dispatch 8192 x 7168, 8 of 256      145 us  720 MB, of it 117 MB of zeros
+//                                               that fill the experts' blocks;
+//                                               times the weights 147
+//            4001 x 2048, 4 of 60      12.8 us  times the weights 13.7
+//            64 x 7168, 8 of 256         45 us  nearly all of it the zeros (236 MB)
 //   combine  8192 x 7168, 8 of 256      184 us  1058 MB, 5.7 TB/s
-//            4001 x 2048, 4 of 60      14.4 us
+//            4001 x 2048, 4 of 60      15.0 us
 //   its gradient, 4001 x 2048, 4 of 60 22.8 us  113 MB (25.8 in two launches, dy
 //                                               read twice)
 // One token of 4096 columns takes 4.5 us, 64 tokens' combine 3: a launch and its
@@ -283,10 +286,19 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineArgs p, Di
 
 }  // namespace
 
-// A scale stored by itself is one request to the L2, and there are as many of them
-// as of the codes' lines: 8192 x 7168 to 8 of 256 (3.7 million scales) 193 us with
-// them, 148 us parked (111 + 37).  The second launch is worth it from about a million scales:
-// 4001 x 2048 to 4 of 60 (256 thousand) 15.3 against 18.1 us.
+// A scale stored by itself is one request to the L2, and with hundreds of experts, whose
+// rows grow at the same time, no line of scales fills up there before it leaves.  Few
+// experts fill their lines, and the second launch costs more than it saves.  us without
+// and with the workspace, in the order of the scales' number:
+//   8 of 256, 7168 columns   0.9 million  61, 51   1.1  67, 56   1.3  70, 59   1.8  81, 75
+//                            2.2  114, 110         3.7  170, 143
+//   8 of 128, 4096           1.0  38.6, 38.3       2.1  65.6, 65.7
+//   4 of 60, 2048            0.26 13.0, 15.1  0.5  21.8, 23.1  1.0  39.4, 40.2  2.1  88.4, 87.8
+//   6 of 64, 2048            1.6  51.2, 52.0       3.1  122, 114
+//   2 of 8, 4096             1.0  52.8, 56.7       2.1  99, 105      4.2  194, 200
+//   1 of 8, 8192             1.0  77, 87           2.1  144, 166
+// (weighted, the scales of a token k times, 1 to 5 us more with the workspace).  The rule
+// knows the scales' number alone: from 2^20 on.
 size_t dispatch_workspace_bytes(int64_t T, int k, int64_t H, bool weighted) {
   if (T * k < (int64_t(1) << 20) / (H / 128)) return 0;
   return (size_t)(weighted ? T * k : T) * (H / 128) * sizeof(float);

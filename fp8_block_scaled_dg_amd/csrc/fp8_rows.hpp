@@ -3,8 +3,8 @@
 // (s = binary32(amax / 448), code = E4M3(binary32(x / s)), dg_device.hpp) in as few
 // instructions as they can be had, since these kernels quantise two or three
 // values for each one they read and the VALU would bound them (SwiGLU with its
-// checkpoint, 32768 rows of 1408 units: 88 us with dg_device.hpp's encoder and
-// fmaxf, some 54 instructions a unit, 75 with these).
+// checkpoint, 32768 rows of 1408 units, 32 rows a workgroup: 88 us with dg_device.hpp's
+// encoder and fmaxf, some 54 instructions a unit, 75 with these).
 #pragma once
 
 #include "dg_device.hpp"

@@ -24,7 +24,7 @@ extern "C" {
 // For each of the n positive numbers x (at most 2^31 - 256 of them): RN(1 / x), and the
 // scale, divisor and RN(1 / divisor) of a block with the largest magnitude x.  Returns
 // 0, or the HIP error of the launch.
-int dg_probe_row_scale(const float* x, float* reciprocal, float* scale, float* divisor, float* inverse,
+int dgp_row_scale(const float* x, float* reciprocal, float* scale, float* divisor, float* inverse,
                        int64_t n, void* stream) {
   if (!x || !reciprocal || !scale || !divisor || !inverse || n < 1 || n > INT32_MAX - 255) return -1;
   hipLaunchKernelGGL(row_scale_list, dim3((unsigned)((n + 255) / 256)), dim3(256), 0,

@@ -25,11 +25,11 @@
 //
 // What bounds it is the chain of k rounds of a maximum over 16 lanes (45
 // instructions a round for 256 experts), not the logits' bytes.  MI355X, 16384 tokens,
-// k = 8, in a graph: 256 experts without a bias 7.3 us (FP32; 16.8 MB, 3.4 us at 5.0
-// TB/s), with a bias 10.6, and 8 groups by their best two 12.2 (of it about 2 for the
+// k = 8, in a graph: 256 experts without a bias 8.5 us (FP32; 16.8 MB, 3.4 us at 5.0
+// TB/s), with a bias 10.3, and 8 groups by their best two 12.3 (of it about 2 for the
 // tokens that are looked at again, since the last wave waits for them; 15.7 with
-// route_exact for all of these, 37 with a wave per token in 64 bits); 512 experts 21,
-// 1024 with a bias 84; 60 experts, k = 4, 30001 tokens 5.2, the gradient 5.4 (14 and
+// route_exact for all of these, 37 with a wave per token in 64 bits); 512 experts in 8
+// groups 18.6, 1024 without a bias 32, with one 84; 60 experts, k = 4, 30001 tokens 5.2, the gradient 5.4 (14 and
 // 13 with a wave per token; with e^d from v_exp_f32 of a product rounded once, off by
 // (d + 2) half steps, it took 5.0).
 #include "dg_device.hpp"

@@ -632,9 +632,10 @@ int dg_moe_plan(int32_t *rows, int32_t *pairs, int32_t *m_indices, int64_t *offs
  *   workspace : optional (NULL or 0 bytes: none; the results are the same), of
  *         dg_moe_dispatch_fp8_workspace_bytes(T, k, H, weights given) bytes,
  *         16-byte aligned, any contents, clobbered: the scales meet there on
- *         their way to sa, which saves a large call a fifth to a quarter of its time.  The
- *         query returns 0 for calls that have no use for one.  Calls that may
- *         run at the same time need distinct ones.
+ *         their way to sa, which saves a large call to hundreds of experts up to
+ *         a sixth of its time and costs one to few experts 5 to 15 in a hundred.
+ *         The query returns 0 for calls of less than 2^20 scales, which have no
+ *         use for one.  Calls that may run at the same time need distinct ones.
  * Requirements: T >= 1, 1 <= k <= DG_MOE_MAX_SLOTS, M >= 128, M % 128 == 0,
  * H >= 128, H % 128 == 0; T <= 2^23, T * ceil(H/512) <= 2^25, M * ceil(H/512) <= 2^27;
  * a 16-byte, the rest 4-byte aligned.  Deterministic.

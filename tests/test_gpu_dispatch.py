@@ -41,7 +41,7 @@ def layout(dg, ids, E, extra=0):
     return dg.MoePlan(*out)
 
 
-# T, E, k: one launch up to 16384 pairs, then chunks with their counts in the workspace
+# T, E, k: one launch up to 8192 pairs, then chunks with their counts in the workspace
 PLANS = [(1, 1, 1), (1, 8, 2), (1, 1024, 16), (3, 1000, 3), (64, 8, 2), (127, 3, 1), (128, 1, 1), (129, 2, 2), (300, 60, 4),
          (512, 256, 8), (1365, 7, 3), (4097, 5, 1), (2001, 60, 4), (700, 1023, 7), (9001, 256, 8), (40000, 3, 2)]
 

@@ -17,12 +17,12 @@ def probe():
     need_gpu()
     import fp8_block_scaled_dg_amd as dg
     lib = ctypes.CDLL(os.path.join(os.path.dirname(dg.__file__), "lib", "libdg_probe.so"))
-    lib.dg_probe_row_scale.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_int64, ctypes.c_void_p]
+    lib.dgp_row_scale.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_int64, ctypes.c_void_p]
 
     def run(x):
         d = torch.from_numpy(x).cuda()
         out = [torch.full_like(d, float("nan")) for _ in range(4)]
-        rc = lib.dg_probe_row_scale(d.data_ptr(), *(o.data_ptr() for o in out), d.numel(),
+        rc = lib.dgp_row_scale(d.data_ptr(), *(o.data_ptr() for o in out), d.numel(),
                                     torch.cuda.current_stream().cuda_stream)
         assert rc == 0
         return [o.cpu().numpy() for o in out]
